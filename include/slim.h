@@ -355,6 +355,121 @@ slim_status slim_pack_transposed(const uint8_t* values, const uint8_t* meta,
                                  int64_t group, uint16_t* tvalues, uint16_t* tmeta,
                                  hipStream_t stream);
 
+/*
+ * Attention over a paged key-value cache: what a decoder block computes
+ * between its q/k/v projections and o_proj when it serves tokens.
+ *
+ * The cache.  One layer's pool is two arrays K and V, each
+ *   [pages][kv_heads][page_size][head_dim],  fp16 or bf16 (dtype),
+ * and a sequence owns an ordered list of pages: key j of sequence b lies in
+ * page table[b][j / page_size], row j % page_size.
+ *   table   int32 [seqs][table_width]
+ *   lens    int32 [seqs]: tokens of each sequence in the cache, the new ones
+ *           of this step included; a negative length counts as 0
+ *   starts  int32 [seqs + 1], not decreasing: the new tokens of sequence b
+ *           are rows starts[b] .. starts[b+1] - 1 of the [tokens] arrays, and
+ *           the i-th of them has position lens[b] - (starts[b+1] - starts[b])
+ *           + i.  NULL: one new token per sequence (row b; tokens == seqs).
+ * table, lens and starts are device arrays that the calls read when they run,
+ * so one captured graph serves a cache that grows.  Their values are checked
+ * where they are used: a table entry outside [0, pages), and a position past
+ * table_width * page_size, holds no key (it is masked; append writes nothing
+ * there), rows outside [0, tokens) are left alone, and no value reads or
+ * writes out of range.
+ *
+ * What a query at position p sees: key j if j <= p and (window == 0, or
+ * j > p - window, or j < sinks): causal, the last `window` positions (its own
+ * among them) and the first `sinks` ones.  Query head h reads key head
+ * h / (q_heads / kv_heads).
+ *   s_j = scale * q . k_j,   O = sum_j exp(s_j - m) v_j / l,
+ *   m = max_j s_j, l = sum_j exp(s_j - m) over the keys seen, lse = m + ln l.
+ * A row that sees no key (or only scores of -inf) gives O = 0, lse = -inf.
+ * Keys and values that a row does not see do not reach it, whatever they
+ * hold, NaN and infinities included.  Scores, m, l and O are held in fp32;
+ * the products take fp16 or bf16 operands.  Results do not depend on other
+ * sequences' values and repeat bit for bit.
+ *
+ * Arguments of all calls: dtype SLIM_FP16 or SLIM_BF16 (of every half tensor);
+ * head_dim 64, 96, 128 or 256; page_size a power of two from 16 to 1024;
+ * q_heads a multiple of kv_heads; heads at most 1024; tokens and
+ * seqs up to 2^22, pages and table_width up to 2^24, table_width * page_size
+ * up to 2^30.  Rows
+ * of Q and O are [q_heads][head_dim], rows of the new K and V
+ * [kv_heads][head_dim], consecutive rows stride_* elements apart (a multiple of
+ * 8, at least a row: a slice of a joint q/k/v array is taken as it is).
+ * Pointers are 16-byte aligned except table, lens, starts, src, dst and lse
+ * (4 bytes).  Errors: SLIM_EINVAL for a broken rule, a NULL pointer or a
+ * workspace too small, SLIM_EUNSUPPORTED for a head_dim, page_size or dtype
+ * that is not listed and for a device that is not gfx950, SLIM_EHIP.
+ * tokens == 0 (n == 0 for copies) is a no-op.
+ */
+typedef enum { SLIM_FP16 = 0, SLIM_BF16 = 1 } slim_dtype;
+
+/*
+ * slim_kv_append — writes new keys and values to the pages of their
+ * positions: K, V rows [tokens] as described above; Kpool, Vpool one layer's
+ * pool.  Two sequences must not share the page of a new position.
+ */
+slim_status slim_kv_append(const uint16_t* K, int64_t stride_K, const uint16_t* V, int64_t stride_V,
+                           int64_t tokens, int64_t seqs, int64_t kv_heads, int64_t head_dim, int dtype,
+                           const int32_t* table, int64_t table_width, const int32_t* lens,
+                           const int32_t* starts, uint16_t* Kpool, uint16_t* Vpool, int64_t pages,
+                           int64_t page_size, hipStream_t stream);
+
+/*
+ * slim_kv_copy_pages — for each i < n and each layer: page src[i] of Kpool
+ * and Vpool is copied to page dst[i] (forks give a sequence its own copy of a
+ * shared page, compaction moves pages).  The pools are [layers][pages] pages
+ * of page_bytes bytes (a multiple of 16, up to 2^30); src, dst int32 [n].  A pair with
+ * an index outside [0, pages) is skipped.  No page may be a destination twice,
+ * nor both a source and another pair's destination (its bytes would be
+ * undefined).
+ */
+slim_status slim_kv_copy_pages(void* Kpool, void* Vpool, int64_t layers, int64_t pages, int64_t page_bytes,
+                               const int32_t* src, const int32_t* dst, int64_t n, hipStream_t stream);
+
+/*
+ * Workspace of slim_attention_decode (tokens == seqs) and
+ * slim_attention_prefill in bytes, 0 for a rejected shape; it does not grow with
+ * the lengths.  Caller-owned device memory with the rules of
+ * slim_linear_workspace_bytes: zero its first 16384 bytes before the first
+ * use; every call leaves it valid for the next of any shape that it is large
+ * enough for; calls that share it must be ordered on one stream.
+ */
+size_t slim_attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t q_heads, int64_t kv_heads,
+                                      int64_t head_dim);
+
+/*
+ * slim_attention_decode — attention of one new token of each sequence (row b
+ * of Q at position lens[b] - 1), its key and value already in the cache.
+ *   Q, O     [seqs] rows;  lse: fp32 [seqs][q_heads] or NULL
+ *   max_len  the longest length expected: it only sets how far the work is split over
+ *            the keys (longer sequences are computed as well); it may
+ *            change results in their last bits
+ *   window   0 or the number of last positions seen; sinks >= 0
+ */
+slim_status slim_attention_decode(const uint16_t* Q, int64_t stride_Q, uint16_t* O, int64_t stride_O, float* lse,
+                                  int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int dtype,
+                                  const uint16_t* Kpool, const uint16_t* Vpool, int64_t pages, int64_t page_size,
+                                  const int32_t* table, int64_t table_width, const int32_t* lens, int64_t max_len,
+                                  int64_t window, int64_t sinks, float scale, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * slim_attention_prefill — the same for any number of new tokens of each
+ * sequence (starts), whole prompts or chunks behind a cached prefix, their keys and
+ * values already in the cache.  Q, O: [tokens] rows; lse: fp32
+ * [tokens][q_heads] or NULL; rows at or past starts[seqs] are not written.
+ * Other arguments as slim_attention_decode.
+ */
+slim_status slim_attention_prefill(const uint16_t* Q, int64_t stride_Q, uint16_t* O, int64_t stride_O, float* lse,
+                                   int64_t tokens, int64_t seqs, int64_t q_heads, int64_t kv_heads,
+                                   int64_t head_dim, int dtype, const uint16_t* Kpool, const uint16_t* Vpool,
+                                   int64_t pages, int64_t page_size, const int32_t* table, int64_t table_width,
+                                   const int32_t* lens, const int32_t* starts, int64_t max_len, int64_t window,
+                                   int64_t sinks, float scale, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -17,7 +17,9 @@ from ._lib import (SlimError, slim_adapter_codes_bytes, slim_adapter_scales_byte
                    slim_pack_transposed, slim_scales_bytes, slim_transposed_meta_bytes,
                    slim_transposed_values_bytes, slim_values_bytes, slim_linear_giveups,
                    slim_set_wait_limit, slim_quantize_input, slim_linear_a8_workspace_bytes, slim_linear_a8,
-                   slim_pack_hybrid, slim_linear_hybrid)
+                   slim_pack_hybrid, slim_linear_hybrid, slim_kv_append, slim_kv_copy_pages,
+                   slim_attention_workspace_bytes, slim_attention_decode, slim_attention_prefill)
+from .kv_cache import CacheFull, KVCache
 
 GROUP = 128
 
@@ -30,7 +32,10 @@ __all__ = ["SlimError", "slim_pack", "slim_linear", "slim_linear_batched",
            "slim_transposed_values_bytes", "slim_transposed_meta_bytes", "pack_transposed",
            "slim_linear_giveups", "slim_set_wait_limit", "slim_quantize_input", "slim_linear_a8_workspace_bytes",
            "slim_linear_a8", "quantize_input", "linear_a8", "slim_pack_hybrid", "slim_linear_hybrid",
-           "HybridWeight", "pack_hybrid", "linear_hybrid"]
+           "HybridWeight", "pack_hybrid", "linear_hybrid",
+           "slim_kv_append", "slim_kv_copy_pages", "slim_attention_workspace_bytes", "slim_attention_decode",
+           "slim_attention_prefill", "kv_append", "kv_copy_pages", "workspace_attention", "attention_decode",
+           "attention_prefill", "KVCache", "CacheFull"]
 
 GROUP_L = 128          # quantised Lt: groups along K
 GROUP_R = 32           # quantised Rt: groups along r
@@ -201,4 +206,84 @@ def linear_hybrid(X: torch.Tensor, w: HybridWeight, Lt: torch.Tensor | None, Rt:
     if ws is None:
         ws = workspace(M, w.N, K, r, device=X.device)
     slim_linear_hybrid(X, w.values, w.meta, w.scales, w.dvalues, w.dense, Lt, Rt, out, ws, stream=stream)
+    return out
+
+
+def kv_append(K: torch.Tensor, V: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor, table: torch.Tensor,
+              lens: torch.Tensor, starts: torch.Tensor | None = None, stream=None) -> None:
+    """Write new keys and values [tokens, kv_heads, head_dim] (fp16 or bf16) to
+    the pages of their positions in one layer's pools [pages, kv_heads,
+    page_size, head_dim].
+
+    table int32 [seqs, width]: the pages of each sequence; lens int32 [seqs]:
+    its tokens, the new ones included; starts int32 [seqs + 1]: its rows among
+    the new tokens (None: one new token per sequence)."""
+    slim_kv_append(K, V, kpool, vpool, table, lens, starts, stream=stream)
+
+
+def kv_copy_pages(kpool: torch.Tensor, vpool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Copy pages src[i] to dst[i] (int32) in every layer of the pools
+    [layers, pages, kv_heads, page_size, head_dim]."""
+    slim_kv_copy_pages(kpool, vpool, src, dst, stream=stream)
+
+
+def workspace_attention(tokens: int, seqs: int, q_heads: int, kv_heads: int, head_dim: int,
+                        device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for attention_decode (tokens == seqs) and
+    attention_prefill; its size does not depend on the lengths."""
+    nbytes = slim_attention_workspace_bytes(tokens, seqs, q_heads, kv_heads, head_dim)
+    if nbytes == 0:
+        raise ValueError(f"no attention of this shape: {tokens} tokens, {seqs} sequences, {q_heads} query heads, "
+                         f"{kv_heads} key heads, head size {head_dim}")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def _attention_buffers(q, seqs, kpool, ws, out, stream):
+    """Output and workspace of a call that was not given them, made on the
+    stream that the call runs on (so that it, not the current one, owns them)."""
+    if out is not None and ws is not None:
+        return out, ws
+    with torch.cuda.stream(stream):            # None: no change
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if ws is None:
+            ws = workspace_attention(q.shape[0], seqs, q.shape[1], kpool.shape[1], kpool.shape[3], device=q.device)
+    return out, ws
+
+
+def attention_decode(q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor, table: torch.Tensor,
+                     lens: torch.Tensor, max_len: int | None = None, window: int = 0, sinks: int = 0,
+                     scale: float | None = None, lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence over the paged cache: q
+    [seqs, q_heads, head_dim] at positions lens - 1, their keys and values
+    already appended.
+
+    window: 0, or the number of last positions seen, with the first `sinks`
+    ones; max_len: the longest length expected (None: the table's capacity),
+    which only plans how the work is split; scale: 1 / sqrt(head_dim) if None;
+    lse: float32 [seqs, q_heads], receives the log of the softmax sums."""
+    if q.dim() != 3 or kpool.dim() != 4:
+        raise ValueError("q must be [seqs, q_heads, head_dim], the pools [pages, kv_heads, page_size, head_dim]")
+    out, ws = _attention_buffers(q, lens.shape[0], kpool, ws, out, stream)
+    slim_attention_decode(q, out, kpool, vpool, table, lens, ws,
+                          table.shape[1] * kpool.shape[2] if max_len is None else max_len, window, sinks,
+                          q.shape[2] ** -0.5 if scale is None else scale, lse, stream=stream)
+    return out
+
+
+def attention_prefill(q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor, table: torch.Tensor,
+                      lens: torch.Tensor, starts: torch.Tensor | None, max_len: int | None = None, window: int = 0,
+                      sinks: int = 0, scale: float | None = None, lse: torch.Tensor | None = None,
+                      ws: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of the new tokens of every sequence over the paged
+    cache (whole prompts, or chunks behind what is cached): q [tokens, q_heads,
+    head_dim], starts int32 [seqs + 1] as for kv_append, the tokens' keys and
+    values already appended.  Other arguments as attention_decode."""
+    if q.dim() != 3 or kpool.dim() != 4:
+        raise ValueError("q must be [tokens, q_heads, head_dim], the pools [pages, kv_heads, page_size, head_dim]")
+    out, ws = _attention_buffers(q, lens.shape[0], kpool, ws, out, stream)
+    slim_attention_prefill(q, out, kpool, vpool, table, lens, starts, ws,
+                           table.shape[1] * kpool.shape[2] if max_len is None else max_len, window, sinks,
+                           q.shape[2] ** -0.5 if scale is None else scale, lse, stream=stream)
     return out

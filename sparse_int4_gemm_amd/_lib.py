@@ -30,6 +30,8 @@ EXPORTED = (
     "slim_linear_giveups", "slim_set_wait_limit", "slim_linear_noalloc",
     "slim_quantize_input", "slim_linear_a8_workspace_bytes", "slim_linear_a8",
     "slim_pack_hybrid", "slim_linear_hybrid",
+    "slim_kv_append", "slim_kv_copy_pages", "slim_attention_workspace_bytes",
+    "slim_attention_decode", "slim_attention_prefill",
 )
 
 _lib = None
@@ -102,6 +104,19 @@ def load() -> ctypes.CDLL:
     lib.slim_linear_hybrid.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp, vp, i64, vp, vp, sz, vp]
     lib.slim_linear_noalloc.restype = ctypes.c_int
     lib.slim_linear_noalloc.argtypes = [vp, i64, i64, i64, vp, vp, vp, i64, vp, vp, i64, vp, vp]
+    i32, f32 = ctypes.c_int, ctypes.c_float
+    lib.slim_kv_append.restype = ctypes.c_int
+    lib.slim_kv_append.argtypes = [vp, i64, vp, i64, i64, i64, i64, i64, i32, vp, i64, vp, vp, vp, vp, i64, i64, vp]
+    lib.slim_kv_copy_pages.restype = ctypes.c_int
+    lib.slim_kv_copy_pages.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, vp]
+    lib.slim_attention_workspace_bytes.restype = sz
+    lib.slim_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.slim_attention_decode.restype = ctypes.c_int
+    lib.slim_attention_decode.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp, vp, i64, i64, vp, i64, vp,
+                                          i64, i64, i64, f32, vp, sz, vp]
+    lib.slim_attention_prefill.restype = ctypes.c_int
+    lib.slim_attention_prefill.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i32, vp, vp, i64, i64, vp,
+                                           i64, vp, vp, i64, i64, i64, f32, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -275,3 +290,137 @@ def slim_linear_hybrid(X, values, meta, scales, dvalues, dense, Lt, Rt, Y, works
     _check(load().slim_linear_hybrid(_ptr(X), M, N, K, _ptr(values), _ptr(meta), _ptr(scales), _ptr(dvalues),
                                      _ptr(dense), group, _ptr(Lt), _ptr(Rt), r, _ptr(Y), _ptr(workspace), ws_bytes,
                                      _stream(stream)))
+
+
+# ------------------------------------- paged key-value cache and attention
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def _rows(name, t, heads, dim, dtype, device):
+    """(pointer, row stride) of a [tokens, heads, dim] tensor whose rows are
+    dense; the rows themselves may lie apart (a slice of a joint array)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    sr, sh, sd = t.stride()
+    if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), sr if t.shape[0] > 1 else heads * dim
+
+
+def _ints(name, t, device, dims):
+    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dims}-dimensional int32 tensor on {device}")
+    return t.data_ptr()
+
+
+def _pools(kpool, vpool, dims):
+    if kpool.device.type != "cuda":
+        raise ValueError("tensors must live on the GPU (a ROCm 'cuda' device)")
+    if kpool.dtype not in _DTYPES:
+        raise TypeError("the pools must be float16 or bfloat16")
+    if kpool.dim() != dims or kpool.shape != vpool.shape or kpool.dtype != vpool.dtype or kpool.device != vpool.device:
+        raise ValueError(f"the pools must be two {dims}-dimensional tensors of one shape, type and device")
+    if not (kpool.is_contiguous() and vpool.is_contiguous()):
+        raise ValueError("the pools must be contiguous")
+    return kpool.device
+
+
+def _stream_on(stream, device):
+    """The HIP stream of a call on `device`, and a check that launches go there."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the current device must be the tensors' {device}")
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _batch(table, lens, starts, tokens, device):
+    seqs = lens.shape[0] if lens.dim() == 1 else -1
+    p_table, p_lens = _ints("table", table, device, 2), _ints("lens", lens, device, 1)
+    if table.shape[0] != seqs:
+        raise ValueError(f"table has {table.shape[0]} rows for {seqs} sequences")
+    if starts is None:
+        if tokens != seqs:
+            raise ValueError(f"{tokens} new tokens for {seqs} sequences without starts")
+        return p_table, p_lens, None, seqs
+    if starts.dim() == 1 and starts.shape[0] != seqs + 1:
+        raise ValueError(f"starts must hold {seqs + 1} values, got {starts.shape[0]}")
+    return p_table, p_lens, _ints("starts", starts, device, 1), seqs
+
+
+def slim_kv_append(K, V, kpool, vpool, table, lens, starts=None, stream=None) -> None:
+    """K, V [tokens, kv_heads, head_dim] to the pages of their positions; pools [pages, kv_heads, page_size, head_dim]."""
+    dev = _pools(kpool, vpool, 4)
+    pages, heads, page, dim = kpool.shape
+    pk, sk = _rows("K", K, heads, dim, kpool.dtype, dev)
+    pv, sv = _rows("V", V, heads, dim, kpool.dtype, dev)
+    tokens = K.shape[0]
+    if V.shape[0] != tokens:
+        raise ValueError(f"K has {tokens} rows and V {V.shape[0]}")
+    pt, pl, ps, seqs = _batch(table, lens, starts, tokens, dev)
+    _check(load().slim_kv_append(pk, sk, pv, sv, tokens, seqs, heads, dim, _DTYPES[kpool.dtype], pt, table.shape[1], pl,
+                                 ps, kpool.data_ptr(), vpool.data_ptr(), pages, page, _stream_on(stream, dev)))
+
+
+def slim_kv_copy_pages(kpool, vpool, src, dst, stream=None) -> None:
+    """Pages src[i] to dst[i] of every layer; pools [layers, pages, ...] or one layer's [pages, kv_heads, page_size, head_dim]."""
+    dev = _pools(kpool, vpool, kpool.dim())
+    if kpool.dim() not in (4, 5):
+        raise ValueError("the pools must be [layers, pages, kv_heads, page_size, head_dim] or one layer of it")
+    layers = kpool.shape[0] if kpool.dim() == 5 else 1
+    pages, heads, page, dim = kpool.shape[-4:]
+    ps, pd = _ints("src", src, dev, 1), _ints("dst", dst, dev, 1)
+    if src.shape != dst.shape:
+        raise ValueError(f"{src.shape[0]} sources and {dst.shape[0]} destinations")
+    _check(load().slim_kv_copy_pages(kpool.data_ptr(), vpool.data_ptr(), layers, pages,
+                                     heads * page * dim * kpool.element_size(), ps, pd, src.shape[0],
+                                     _stream_on(stream, dev)))
+
+
+def slim_attention_workspace_bytes(tokens: int, seqs: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return load().slim_attention_workspace_bytes(tokens, seqs, q_heads, kv_heads, head_dim)
+
+
+def _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace):
+    dev = _pools(kpool, vpool, 4)
+    pages, kv_heads, page, dim = kpool.shape
+    if Q.dim() != 3:
+        raise ValueError(f"Q must be [tokens, q_heads, {dim}], got {tuple(Q.shape)}")
+    tokens, q_heads = Q.shape[0], Q.shape[1]
+    pq, sq = _rows("Q", Q, q_heads, dim, kpool.dtype, dev)
+    po, so = _rows("O", O, q_heads, dim, kpool.dtype, dev)
+    if O.shape[0] != tokens:
+        raise ValueError(f"Q has {tokens} rows and O {O.shape[0]}")
+    p_lse = None
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.shape != (tokens, q_heads) or not lse.is_contiguous() or lse.device != dev:
+            raise ValueError(f"lse must be a contiguous float32 [{tokens}, {q_heads}] tensor on {dev}")
+        p_lse = lse.data_ptr()
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {dev}")
+    pt, pl, ps, seqs = _batch(table, lens, starts, tokens, dev)
+    return (dev, pq, sq, po, so, p_lse, tokens, seqs, q_heads, kv_heads, dim, pages, page, pt, pl, ps,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def slim_attention_decode(Q, O, kpool, vpool, table, lens, workspace, max_len: int, window: int = 0, sinks: int = 0,
+                          scale: float = 1.0, lse=None, stream=None) -> None:
+    """Attention of one new token per sequence: Q, O [seqs, q_heads, head_dim]."""
+    (dev, pq, sq, po, so, p_lse, _, seqs, q_heads, kv_heads, dim, pages, page, pt, pl, _, ws,
+     ws_bytes) = _attention_args(Q, O, lse, kpool, vpool, table, lens, None, workspace)
+    _check(load().slim_attention_decode(pq, sq, po, so, p_lse, seqs, q_heads, kv_heads, dim, _DTYPES[kpool.dtype],
+                                        kpool.data_ptr(), vpool.data_ptr(), pages, page, pt, table.shape[1], pl, max_len,
+                                        window, sinks, scale, ws, ws_bytes, _stream_on(stream, dev)))
+
+
+def slim_attention_prefill(Q, O, kpool, vpool, table, lens, starts, workspace, max_len: int, window: int = 0,
+                           sinks: int = 0, scale: float = 1.0, lse=None, stream=None) -> None:
+    """Attention of any number of new tokens per sequence: Q, O [tokens, q_heads, head_dim]."""
+    (dev, pq, sq, po, so, p_lse, tokens, seqs, q_heads, kv_heads, dim, pages, page, pt, pl, ps, ws,
+     ws_bytes) = _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace)
+    _check(load().slim_attention_prefill(pq, sq, po, so, p_lse, tokens, seqs, q_heads, kv_heads, dim,
+                                         _DTYPES[kpool.dtype], kpool.data_ptr(), vpool.data_ptr(), pages, page, pt,
+                                         table.shape[1], pl, ps, max_len, window, sinks, scale, ws, ws_bytes,
+                                         _stream_on(stream, dev)))

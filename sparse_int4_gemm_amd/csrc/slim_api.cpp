@@ -11,8 +11,8 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
-#include <string>
 
+#include "api_util.hpp"
 #include "internal.hpp"
 
 // Scratch of slim_linear_noalloc, for callers that cannot allocate: one copy
@@ -26,25 +26,29 @@ static __device__ __align__(256) unsigned char scratch[kNoallocScratchBytes];
 
 namespace {
 
-thread_local std::string g_last_error;
-
-slim_status fail(slim_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-slim_status fail(slim_status s, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return s;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+thread_local char g_last_error[512];
 
 // Cached "is the current device gfx950" per device ordinal.
 constexpr int kMaxDevices = 64;
 int g_arch_state[kMaxDevices];  // 0 unknown, 1 gfx950, 2 other
 std::mutex g_arch_mutex;
+
+}  // namespace
+
+namespace slim {
+
+slim_status fail(slim_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+slim_status done() {
+    g_last_error[0] = 0;
+    return SLIM_OK;
+}
 
 slim_status check_device() {
     int dev = 0;
@@ -66,16 +70,22 @@ slim_status check_device() {
 
 slim_status launched(hipError_t e, const char* what) {
     if (e != hipSuccess) return fail(SLIM_EHIP, "%s: %s", what, hipGetErrorString(e));
-    g_last_error.clear();
-    return SLIM_OK;
+    return done();
 }
 
-// Largest sizes any call accepts: every product of two of them fits int64
-// (the kernels' grid and offset math, and the size queries, stay exact).
-constexpr int64_t kMaxDim = int64_t(1) << 24;
+}  // namespace slim
+
+namespace {
+
+using slim::aligned16;
+using slim::check_device;
+using slim::fail;
+using slim::kMaxDim;
+using slim::kMaxStride;
+using slim::launched;
+
 constexpr int64_t kMaxRank = 4096;
 constexpr int64_t kMaxWeights = int64_t(1) << 40;   // N * K of one weight or factor
-constexpr int64_t kMaxStride = int64_t(1) << 40;    // elements between batched problems
 
 bool dims_ok(int64_t a, int64_t b) { return a > 0 && b > 0 && a <= kMaxDim && b <= kMaxDim; }
 
@@ -111,9 +121,8 @@ slim_status check_linear_args(int64_t batch, int64_t M, int64_t N, int64_t K, in
     if (batch < 0) return fail(SLIM_EINVAL, "batch must be >= 0");
     if (batch > 65535) return fail(SLIM_EINVAL, "batch must be <= 65535");
     if (batch == 0 || M == 0) {
-        g_last_error.clear();
         *nothing = true;
-        return SLIM_OK;
+        return slim::done();
     }
     if (!X || !values || !meta || !scales || !Y) return fail(SLIM_EINVAL, "NULL tensor pointer");
     if (r > 0 && (!Lt || !Rt)) return fail(SLIM_EINVAL, "Lt and Rt must be non-NULL when r > 0");
@@ -196,7 +205,7 @@ const char* slim_status_string(int status) {
     }
 }
 
-const char* slim_last_error(void) { return g_last_error.c_str(); }
+const char* slim_last_error(void) { return g_last_error; }
 
 int slim_version(void) { return 1; }
 
@@ -360,7 +369,7 @@ slim_status slim_linear_qa(const uint16_t* X, int64_t M, int64_t N, int64_t K, c
     slim_status st = check_linear_shape(M, N, K, r, group);
     if (st != SLIM_OK) return st;
     if (r == 0) return fail(SLIM_EINVAL, "slim_linear_qa: r must be > 0 (use slim_linear without an adapter)");
-    if (M == 0) { g_last_error.clear(); return SLIM_OK; }
+    if (M == 0) return slim::done();
     if (!X || !values || !meta || !scales || !Y || !Lq || !Ls || !Rq || !Rs)
         return fail(SLIM_EINVAL, "NULL tensor pointer");
     if (!aligned16(X) || !aligned16(values) || !aligned16(meta) || !aligned16(scales) || !aligned16(Y) ||
@@ -392,7 +401,7 @@ slim_status slim_quantize_input(const uint16_t* X, int64_t M, int64_t K, int8_t*
                                 hipStream_t stream) {
     if (M < 0 || K <= 0 || K % 8) return fail(SLIM_EINVAL, "slim_quantize_input: need M >= 0 and K a positive multiple of 8");
     if (M > kMaxDim || K > kMaxDim) return fail(SLIM_EINVAL, "slim_quantize_input: shape too large");
-    if (M == 0) { g_last_error.clear(); return SLIM_OK; }
+    if (M == 0) return slim::done();
     if (!X || !q || !s) return fail(SLIM_EINVAL, "slim_quantize_input: NULL pointer");
     if (!aligned16(X) || !aligned16(q) || !aligned16(s))
         return fail(SLIM_EINVAL, "slim_quantize_input: pointers must be 16-byte aligned");
@@ -490,8 +499,7 @@ slim_status slim_linear_giveups(const void* workspace, int reset, uint64_t* coun
     }
     if (e != hipSuccess) return fail(SLIM_EHIP, "slim_linear_giveups: %s", hipGetErrorString(e));
     *count = v;
-    g_last_error.clear();
-    return SLIM_OK;
+    return slim::done();
 }
 
 }  // extern "C"
