@@ -4,7 +4,7 @@
 //   lane j scores key base + j:  s_j = scale * sum_d q_d k_jd
 //   running maximum m and sum l over blocks of 64 keys,
 //   lane owns the output elements d = lane + 64 i.
-#include "attention_util.hpp"
+#include "attention_device.hpp"
 
 namespace slim {
 namespace {
@@ -64,16 +64,21 @@ __global__ __launch_bounds__(64) void attention_plain_kernel(AttnArgs a) {
     if (a.lse && lane == 0) a.lse[(int64_t)t * a.q_heads + h] = l == 0.0f ? -INFINITY : m + logf(l);
 }
 
-hipError_t launch(const AttnArgs& a, hipStream_t stream) {
+hipError_t launch_plain(const AttnArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(attention_plain_kernel, dim3((unsigned)a.tokens, (unsigned)a.q_heads), dim3(64), 0, stream, a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 16384; }
+// Partials of the split form: at most kSplitTarget workgroups of at most 16
+// rows, whatever the batch, so a workspace serves every batch of its heads.
+size_t attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    const int64_t share = q_heads / kv_heads;
+    const size_t parts = (size_t)(kSplitTarget * (share < 16 ? share : 16)) * (size_t)(head_dim + 2) * sizeof(float);
+    return kAttnCounters + ((parts + 255) & ~size_t(255));
+}
 
-hipError_t launch_attention_decode(const AttnArgs& a, hipStream_t stream) { return launch(a, stream); }
-hipError_t launch_attention_prefill(const AttnArgs& a, hipStream_t stream) { return launch(a, stream); }
+hipError_t launch_attention_prefill(const AttnArgs& a, hipStream_t stream) { return launch_plain(a, stream); }
 
 }  // namespace slim

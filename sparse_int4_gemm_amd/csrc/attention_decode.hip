@@ -1,0 +1,264 @@
+// slim_attention_decode: attention of one new token per sequence.
+//
+//   s_j = scale q . k_j,  O = sum_j 2^(c s_j - m) v_j / l,  c = log2 e,
+//   m a running maximum of c s_j, l the sum of the weights (all fp32).
+//
+// Bound by the keys and values read once from HBM (1 to 16 flops a byte), so
+// the kernel is built around loads: each wave streams tiles of 32 keys
+// straight into registers, one tile ahead of the one it computes on, and every
+// load is as wide as the layout gives (16 bytes a lane at head size 128).
+//  - One wave serves up to 16 query heads of a key head: the matrix
+//    instruction's 16 columns.  Keys are its rows: S^T = K Q^T leaves a
+//    lane with one query (column) and the 4 keys 16 t + 4 g + [0, 4) of each
+//    16-key half t (g = lane / 16).
+//  - O^T = V^T P^T then takes these weights as they lie: its 32 contraction
+//    slots are bound to keys so that a lane's slots are the keys it
+//    scored, and the lane loads exactly those 8 rows of V, head_dim/16
+//    elements each.  Pairing two rows' 16-bit elements is one byte permute
+//    per operand register: V is never transposed through LDS.
+//  - Weights enter the product as two halves (high and low part of the fp32
+//    value): the matrix unit idles anyway, and the result then keeps fp32
+//    weights' accuracy.
+//  - A sequence's tiles are cut into chunks, one workgroup each; its 4 waves
+//    take every fourth tile and join through LDS.
+#include "attention_device.hpp"
+
+namespace slim {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kTile = 32;            // keys of one wave's step
+
+// The registers of one tile.
+template <int D>
+struct Tile {
+    u4 k[2][D / 32];                 // K rows 16 t + lane % 16, elements 32 c + 8 g + [0, 8)
+    uint32_t v[8][D / 32];           // V rows 16 t + 4 g + i, elements (D/16)(lane % 16) + [0, D/16)
+    int base;                        // first key
+    bool owned[2];                   // both 16-key halves: a valid page
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(Tile<D>& x, const AttnArgs& a, const int32_t* table, int kvh, int base) {
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    x.base = base;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int key = base + 16 * t;
+        const int at = key >> a.kv.page_shift;
+        const int page = at < a.kv.width ? table[at] : -1;
+        x.owned[t] = page >= 0 && page < a.kv.pages;
+        const int64_t row = (((int64_t)(x.owned[t] ? page : 0) * a.kv_heads + kvh) << a.kv.page_shift) +
+                            (key & ((1 << a.kv.page_shift) - 1));
+        const uint16_t* k = a.kv.k + row * D;
+        const uint16_t* v = a.kv.v + row * D;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) x.k[t][i] = *reinterpret_cast<const u4*>(k + c * D + 32 * i + 8 * g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_words<D / 32>(x.v[4 * t + i], v + (4 * g + i) * D + (D / 16) * c);
+    }
+}
+
+template <class T, int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnArgs a, int splits, int chunk,
+                                                                          int groups) {
+    constexpr int VE = D / 16;
+    __shared__ float o_join[kWaves][16][D + 4];
+    __shared__ float m_join[kWaves][16], l_join[kWaves][16];
+    __shared__ int arrived;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+    const int split = blockIdx.x % splits, b = blockIdx.x / splits;
+    const int kvh = blockIdx.y / groups, share = a.q_heads / a.kv_heads;
+    const int h0 = kvh * share + (blockIdx.y - kvh * groups) * 16;             // this workgroup's query heads
+    const int heads = min(16, (kvh + 1) * share - h0);
+
+    const Span span = key_span(a, seq_len(a.kv, b) - 1);
+    const int tiles = span.tiles(kTile);
+    // At least `chunk` tiles a workgroup, more where the length passes what was planned for.
+    const int per = max(chunk, (tiles + splits - 1) / splits);
+    const int active = max(1, (tiles + per - 1) / per);
+    if (split >= active) return;
+    const int first = split * per, last = min(tiles, first + per);
+
+    u4 qf[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        qf[i] = u4{0, 0, 0, 0};
+        if (c < heads) qf[i] = *reinterpret_cast<const u4*>(a.q + b * a.sq + (int64_t)(h0 + c) * D + 32 * i + 8 * g);
+    }
+    const float scale = a.scale * 1.4426950408889634f;
+    float m = -INFINITY, l = 0.0f;
+    f4 o[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) o[e] = f4{0, 0, 0, 0};
+
+    const int32_t* table = a.kv.table + (int64_t)b * a.kv.width;
+    auto step = [&](Tile<D>& x) {
+        f4 s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t] = f4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) s[t] = T::mfma16(x.k[t][i], qf[i], s[t]);
+            s[t] *= scale;
+        }
+        // A tile whose every key is seen and owned needs no mask (the same answer in all lanes).
+        if (!(span.all_seen(x.base, kTile) && x.owned[0] && x.owned[1])) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool seen = x.owned[t] && span.seen(x.base + 16 * t + 4 * g + i);
+                    if (!seen) {
+                        s[t][i] = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < D / 32; ++e) x.v[4 * t + i][e] = 0;      // what lies there must not reach 0 * v
+                    }
+                }
+        }
+        float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                          fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top);
+        const float ms = mn == -INFINITY ? 0.0f : mn;        // nothing seen so far: all weights are 2^-inf = 0
+        const float f = exp2_fast(m - ms);
+        m = mn;
+        float w[8], sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            w[j] = exp2_fast(s[j >> 2][j & 3] - ms);
+            sum += w[j];
+        }
+        l = l * f + sum;
+        u4 hi, lo;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            hi[j] = T::pack(w[2 * j], w[2 * j + 1]);
+            lo[j] = T::pack(w[2 * j] - T::low(hi[j]), w[2 * j + 1] - T::high(hi[j]));
+        }
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            u4 vt;                                            // slots 2 j, 2 j + 1: two rows' element e
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                vt[j] = __builtin_amdgcn_perm(x.v[2 * j + 1][e >> 1], x.v[2 * j][e >> 1],
+                                              (e & 1) ? 0x07060302u : 0x05040100u);
+            o[e] = T::mfma16(vt, lo, T::mfma16(vt, hi, o[e] * f));
+        }
+    };
+
+    // Two tiles in flight: the next one's loads are issued before the current
+    // one is used.  At head size 256 two tiles (256 registers) do not fit; the CU's
+    // eight waves then keep eight 32 KB tiles in flight between them.
+    int i = first + wave;
+    if constexpr (D > 128) {
+        for (; i < last; i += kWaves) {
+            Tile<D> x;
+            load_tile<D>(x, a, table, kvh, span.base(i, kTile));
+            step(x);
+        }
+    } else if (i < last) {
+        Tile<D> x, y;
+        load_tile<D>(x, a, table, kvh, span.base(i, kTile));
+        for (;;) {
+            load_tile<D>(y, a, table, kvh, span.base(min(i + kWaves, last - 1), kTile));
+            step(x);
+            i += kWaves;
+            if (i >= last) break;
+            load_tile<D>(x, a, table, kvh, span.base(min(i + kWaves, last - 1), kTile));
+            step(y);
+            i += kWaves;
+            if (i >= last) break;
+        }
+    }
+
+    // Join the waves: a lane's o[e][r] is O^T of query c at d = (D/16)(4 g + r) + e.
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) {
+        m_join[wave][c] = m;
+        l_join[wave][c] = l;
+    }
+    if (c < heads) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) o_join[wave][c][VE * (4 * g + r) + e] = o[e][r];
+    }
+    __syncthreads();
+    const int unit = b * gridDim.y + blockIdx.y;
+    const Partials parts(a, D, splits);
+    for (int at = threadIdx.x; at < heads * (D / 4); at += 64 * kWaves) {
+        const int r = at / (D / 4), d = (at - r * (D / 4)) * 4;
+        float top = m_join[0][r];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, m_join[w][r]);
+        const float ms = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f;
+        f4 acc = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float f = exp2_fast(m_join[w][r] - ms);
+            sum += l_join[w][r] * f;
+            acc += *reinterpret_cast<const f4*>(&o_join[w][r][d]) * f;
+        }
+        const int64_t row = (int64_t)b * a.q_heads + h0 + r;
+        if (active == 1) {
+            store_row4<T>(a, b, h0 + r, D, d, acc, top, sum);
+        } else {
+            parts.put(row, split, d, acc, top, sum);
+        }
+    }
+    if (active == 1) return;
+
+    // The chunk that arrives last joins them all, in their order whichever it is.
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int* counter = reinterpret_cast<int*>(a.ws) + unit;
+        arrived = __hip_atomic_fetch_add(counter, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        if (arrived == active - 1) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (arrived != active - 1) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    for (int at = threadIdx.x; at < heads * (D / 4); at += 64 * kWaves) {
+        const int r = at / (D / 4), d = (at - r * (D / 4)) * 4;
+        f4 acc;
+        float top, sum;
+        parts.join((int64_t)b * a.q_heads + h0 + r, active, d, acc, top, sum);
+        store_row4<T>(a, b, h0 + r, D, d, acc, top, sum);
+    }
+}
+
+template <class T, int D>
+hipError_t launch(const AttnArgs& a, hipStream_t stream) {
+    const int share = a.q_heads / a.kv_heads, groups = (share + 15) / 16;
+    int64_t most = (int64_t)a.max_len;
+    if (a.window && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;
+    const int tiles = (int)((most + kTile - 1) / kTile);
+    const int64_t units = (int64_t)a.tokens * a.kv_heads * groups;
+    const int splits = decode_splits(units, tiles);
+    const int chunk = max(kWaves, (tiles + splits - 1) / splits);
+    dim3 grid((unsigned)(a.tokens * splits), (unsigned)(a.kv_heads * groups));
+    hipLaunchKernelGGL((attention_decode_kernel<T, D>), grid, dim3(64 * kWaves), 0, stream, a, splits, chunk, groups);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
+    switch (a.head_dim) {
+        case 64: return launch<T, 64>(a, stream);
+        case 96: return launch<T, 96>(a, stream);
+        case 128: return launch<T, 128>(a, stream);
+        default: return launch<T, 256>(a, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_attention_decode(const AttnArgs& a, hipStream_t stream) {
+    return a.dtype == 0 ? launch_dim<Fp16>(a, stream) : launch_dim<Bf16>(a, stream);
+}
+
+}  // namespace slim

@@ -1,0 +1,161 @@
+// What the attention kernels share: the half types' operations, which keys a
+// query sees, the partial results of a split key axis, and the rule of the split.
+#pragma once
+
+#include "attention_util.hpp"
+#include "mfma_util.hpp"
+
+namespace slim {
+
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+// Operands travel as dwords of two halves; `pack` rounds to nearest even.
+struct Fp16 {
+    static __device__ __forceinline__ f4 mfma16(u4 a, u4 b, f4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f16v mfma32(u4 a, u4 b, f16v c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ uint32_t pack(float x, float y) {
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{x, y}), h2));
+    }
+    static __device__ __forceinline__ float low(uint32_t x) { return (float)__builtin_bit_cast(h2, x)[0]; }
+    static __device__ __forceinline__ float high(uint32_t x) { return (float)__builtin_bit_cast(h2, x)[1]; }
+};
+struct Bf16 {
+    static __device__ __forceinline__ f4 mfma16(u4 a, u4 b, f4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f16v mfma32(u4 a, u4 b, f16v c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ uint32_t pack(float x, float y) {
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{x, y}), bf2));
+    }
+    static __device__ __forceinline__ float low(uint32_t x) { return __builtin_bit_cast(float, x << 16); }
+    static __device__ __forceinline__ float high(uint32_t x) { return __builtin_bit_cast(float, x & 0xFFFF0000u); }
+};
+
+// 2^x by the hardware instruction (one ulp; results below 2^-126 are zero,
+// which a weight relative to the row's maximum of 1 may lose).
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// N dwords from p; p is aligned to the largest power of two that divides N dwords.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&to)[N], const uint16_t* p) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const u4 x = reinterpret_cast<const u4*>(w)[i];
+            to[4 * i] = x[0]; to[4 * i + 1] = x[1]; to[4 * i + 2] = x[2]; to[4 * i + 3] = x[3];
+        }
+    } else if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const u2 x = reinterpret_cast<const u2*>(w)[i];
+            to[2 * i] = x[0]; to[2 * i + 1] = x[1];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) to[i] = w[i];
+    }
+}
+
+// The keys that positions p0 .. p1 of one sequence see, as a run of tiles:
+// those that hold sinks, then those from the first window's start on.
+struct Span {
+    int p;                // (last) position; -1 or less: nothing is seen
+    int end;              // keys below min(p + 1, capacity of the table)
+    int start;            // first key of the (first position's) window
+    int sinks;
+
+    __device__ __forceinline__ int sink_tiles(int t) const { return min((min(sinks, end) + t - 1) / t, start / t); }
+    __device__ __forceinline__ int tiles(int t) const {
+        return end <= 0 ? 0 : sink_tiles(t) + max(0, (end + t - 1) / t - start / t);
+    }
+    __device__ __forceinline__ int base(int i, int t) const {
+        const int s = sink_tiles(t);
+        return (i < s ? i : i - s + start / t) * t;
+    }
+    __device__ __forceinline__ bool seen(int j) const { return j < end && (j >= start || j < sinks); }
+    __device__ __forceinline__ bool all_seen(int base, int t) const {
+        return base + t <= end && (base >= start || base + t <= sinks);
+    }
+};
+
+// Of a single position p.
+__device__ __forceinline__ Span key_span(const AttnArgs& a, int p) {
+    const int64_t capacity = (int64_t)a.kv.width << a.kv.page_shift;      // at most 2^30
+    Span s;
+    s.p = p;
+    s.end = (int)min((int64_t)p + 1, capacity);
+    s.start = a.window ? max(0, p - a.window + 1) : 0;
+    s.sinks = a.window ? a.sinks : 0;
+    return s;
+}
+
+// Writes four elements of an output row, and lse with the first of them.
+// sum == 0: no key was seen, or none with a score above -inf.
+template <class T>
+__device__ __forceinline__ void store_row4(const AttnArgs& a, int64_t token, int head, int D, int d, f4 acc, float top,
+                                           float sum) {
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (sum == 0.0f) acc = f4{0, 0, 0, 0};
+    const u2 y = {T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
+    *reinterpret_cast<u2*>(a.o + token * a.so + (int64_t)head * D + d) = y;
+    if (a.lse && d == 0)
+        a.lse[token * a.q_heads + head] = sum == 0.0f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
+}
+
+// Partial results of the rows whose keys are split: after the counters, for
+// each row and split the unscaled fp32 output and (m, l), m in units of log2.
+constexpr size_t kAttnCounters = 16384;
+
+struct Partials {
+    float* o;             // [rows][splits][D]
+    float* ml;            // [rows][splits][2]
+    int D, splits;
+    __device__ Partials(const AttnArgs& a, int D_, int splits_) : D(D_), splits(splits_) {
+        o = reinterpret_cast<float*>(a.ws + kAttnCounters);
+        ml = o + (int64_t)a.tokens * a.q_heads * splits * D;
+    }
+    __device__ __forceinline__ void put(int64_t row, int split, int d, f4 acc, float top, float sum) const {
+        const int64_t at = row * splits + split;
+        *reinterpret_cast<f4*>(o + at * D + d) = acc;
+        if (d == 0) {
+            ml[2 * at] = top;
+            ml[2 * at + 1] = sum;
+        }
+    }
+    __device__ __forceinline__ void join(int64_t row, int count, int d, f4& acc, float& top, float& sum) const {
+        const int64_t at = row * splits;
+        top = -INFINITY;
+        for (int i = 0; i < count; ++i) top = fmaxf(top, ml[2 * (at + i)]);
+        const float ms = top == -INFINITY ? 0.0f : top;
+        acc = f4{0, 0, 0, 0};
+        sum = 0.0f;
+        for (int i = 0; i < count; ++i) {
+            const float f = exp2_fast(ml[2 * (at + i)] - ms);
+            sum += ml[2 * (at + i) + 1] * f;
+            acc += *reinterpret_cast<const f4*>(o + (at + i) * D + d) * f;
+        }
+    }
+};
+
+// How many workgroups share a row block's keys: enough that `units` blocks
+// make kSplitTarget workgroups, each with at least kSplitTiles tiles.
+constexpr int kSplitTarget = 2048;
+constexpr int kSplitTiles = 16;
+
+inline int decode_splits(int64_t units, int tiles) {
+    const int64_t want = kSplitTarget / units, most = (tiles + kSplitTiles - 1) / kSplitTiles;
+    const int64_t n = want < most ? want : most;
+    return n < 1 ? 1 : (int)n;
+}
+
+}  // namespace slim
