@@ -39,9 +39,17 @@ struct AppendArgs {
     int32_t tokens, kv_heads, head_dim;
 };
 
+// Workspace: kAttnReserved bytes, then the partial results of split key axes.
+constexpr size_t kAttnReserved = 256;
+// Workgroups that a split may make, and output rows of each, at most.
+constexpr int kDecodeSplitTarget = 2048, kDecodeRows = 16;
+constexpr int kPrefillSplitTarget = 256, kPrefillRows = 128;
+
 size_t attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 hipError_t launch_attention_decode(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attention_prefill(const AttnArgs& a, hipStream_t stream);
+// Joins the partial results of a call's rows, `splits` each.
+hipError_t launch_attention_join(const AttnArgs& a, int splits, hipStream_t stream);
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream);
 hipError_t launch_kv_copy_pages(void* k, void* v, int64_t layers, int64_t pages, int64_t page_bytes,
                                 const int32_t* src, const int32_t* dst, int64_t n, hipStream_t stream);

@@ -65,7 +65,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
     constexpr int VE = D / 16;
     __shared__ float o_join[kWaves][16][D + 4];
     __shared__ float m_join[kWaves][16], l_join[kWaves][16];
-    __shared__ int arrived;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
     const int split = blockIdx.x % splits, b = blockIdx.x / splits;
     const int kvh = blockIdx.y / groups, share = a.q_heads / a.kv_heads;
@@ -77,7 +76,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
     // At least `chunk` tiles a workgroup, more where the length passes what was planned for.
     const int per = max(chunk, (tiles + splits - 1) / splits);
     const int active = max(1, (tiles + per - 1) / per);
-    if (split >= active) return;
+    const int64_t row0 = (int64_t)b * a.q_heads + h0;
+    const Partials parts(a, D, splits);
+    if (split >= active) {
+        if ((int)threadIdx.x < heads) parts.mark(row0 + threadIdx.x, split, -INFINITY, 0.0f);
+        return;
+    }
     const int first = split * per, last = min(tiles, first + per);
 
     u4 qf[D / 32];
@@ -187,8 +191,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
             for (int e = 0; e < VE; ++e) o_join[wave][c][VE * (4 * g + r) + e] = o[e][r];
     }
     __syncthreads();
-    const int unit = b * gridDim.y + blockIdx.y;
-    const Partials parts(a, D, splits);
     for (int at = threadIdx.x; at < heads * (D / 4); at += 64 * kWaves) {
         const int r = at / (D / 4), d = (at - r * (D / 4)) * 4;
         float top = m_join[0][r];
@@ -203,33 +205,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
             sum += l_join[w][r] * f;
             acc += *reinterpret_cast<const f4*>(&o_join[w][r][d]) * f;
         }
-        const int64_t row = (int64_t)b * a.q_heads + h0 + r;
         if (active == 1) {
             store_row4<T>(a, b, h0 + r, D, d, acc, top, sum);
+            if (splits > 1 && d == 0) parts.mark(row0 + r, 0, top, kWhole);
         } else {
-            parts.put(row, split, d, acc, top, sum);
+            parts.put4(row0 + r, split, d, acc);
+            if (d == 0) parts.mark(row0 + r, split, top, sum);
         }
     }
-    if (active == 1) return;
-
-    // The chunk that arrives last joins them all, in their order whichever it is.
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int* counter = reinterpret_cast<int*>(a.ws) + unit;
-        arrived = __hip_atomic_fetch_add(counter, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        if (arrived == active - 1) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (arrived != active - 1) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-    for (int at = threadIdx.x; at < heads * (D / 4); at += 64 * kWaves) {
-        const int r = at / (D / 4), d = (at - r * (D / 4)) * 4;
-        f4 acc;
-        float top, sum;
-        parts.join((int64_t)b * a.q_heads + h0 + r, active, d, acc, top, sum);
-        store_row4<T>(a, b, h0 + r, D, d, acc, top, sum);
-    }
 }
+
+// Splits of each of `units` row blocks: kDecodeSplitTarget workgroups in all,
+// each with at least kMinTiles tiles.
+constexpr int kMinTiles = 16;
 
 template <class T, int D>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
@@ -238,11 +226,12 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     if (a.window && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;
     const int tiles = (int)((most + kTile - 1) / kTile);
     const int64_t units = (int64_t)a.tokens * a.kv_heads * groups;
-    const int splits = decode_splits(units, tiles);
+    const int splits = (int)max((int64_t)1, min(kDecodeSplitTarget / units, (int64_t)((tiles + kMinTiles - 1) / kMinTiles)));
     const int chunk = max(kWaves, (tiles + splits - 1) / splits);
     dim3 grid((unsigned)(a.tokens * splits), (unsigned)(a.kv_heads * groups));
     hipLaunchKernelGGL((attention_decode_kernel<T, D>), grid, dim3(64 * kWaves), 0, stream, a, splits, chunk, groups);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || splits == 1 ? e : launch_attention_join(a, splits, stream);
 }
 
 template <class T>

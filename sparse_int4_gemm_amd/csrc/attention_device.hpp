@@ -112,50 +112,29 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, int64_t token, int
         a.lse[token * a.q_heads + head] = sum == 0.0f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
 }
 
-// Partial results of the rows whose keys are split: after the counters, for
-// each row and split the unscaled fp32 output and (m, l), m in units of log2.
-constexpr size_t kAttnCounters = 16384;
+// Partial results of rows whose keys are split over workgroups: for each row
+// (token * q_heads + head) and split the unscaled fp32 output, its maximum (in
+// units of log2) and sum.  Every split of a row is marked, also one without
+// keys (sum 0, no output stored), so attention_join_kernel needs no knowledge of
+// how the row was cut; a row that needed no join is marked kWhole in its split 0.
+constexpr float kWhole = -1.0f;
 
 struct Partials {
     float* o;             // [rows][splits][D]
     float* ml;            // [rows][splits][2]
     int D, splits;
-    __device__ Partials(const AttnArgs& a, int D_, int splits_) : D(D_), splits(splits_) {
-        o = reinterpret_cast<float*>(a.ws + kAttnCounters);
+    __host__ __device__ Partials(const AttnArgs& a, int D_, int splits_) : D(D_), splits(splits_) {
+        o = reinterpret_cast<float*>(a.ws + kAttnReserved);
         ml = o + (int64_t)a.tokens * a.q_heads * splits * D;
     }
-    __device__ __forceinline__ void put(int64_t row, int split, int d, f4 acc, float top, float sum) const {
-        const int64_t at = row * splits + split;
-        *reinterpret_cast<f4*>(o + at * D + d) = acc;
-        if (d == 0) {
-            ml[2 * at] = top;
-            ml[2 * at + 1] = sum;
-        }
+    __device__ __forceinline__ void mark(int64_t row, int split, float top, float sum) const {
+        float* at = ml + 2 * (row * splits + split);
+        at[0] = top;
+        at[1] = sum;
     }
-    __device__ __forceinline__ void join(int64_t row, int count, int d, f4& acc, float& top, float& sum) const {
-        const int64_t at = row * splits;
-        top = -INFINITY;
-        for (int i = 0; i < count; ++i) top = fmaxf(top, ml[2 * (at + i)]);
-        const float ms = top == -INFINITY ? 0.0f : top;
-        acc = f4{0, 0, 0, 0};
-        sum = 0.0f;
-        for (int i = 0; i < count; ++i) {
-            const float f = exp2_fast(ml[2 * (at + i)] - ms);
-            sum += ml[2 * (at + i) + 1] * f;
-            acc += *reinterpret_cast<const f4*>(o + (at + i) * D + d) * f;
-        }
+    __device__ __forceinline__ void put4(int64_t row, int split, int d, f4 acc) const {
+        *reinterpret_cast<f4*>(o + (row * splits + split) * D + d) = acc;
     }
 };
-
-// How many workgroups share a row block's keys: enough that `units` blocks
-// make kSplitTarget workgroups, each with at least kSplitTiles tiles.
-constexpr int kSplitTarget = 2048;
-constexpr int kSplitTiles = 16;
-
-inline int decode_splits(int64_t units, int tiles) {
-    const int64_t want = kSplitTarget / units, most = (tiles + kSplitTiles - 1) / kSplitTiles;
-    const int64_t n = want < most ? want : most;
-    return n < 1 ? 1 : (int)n;
-}
 
 }  // namespace slim

@@ -1,0 +1,390 @@
+// slim_attention_prefill: causal attention of many new tokens over the paged
+// cache.
+//
+// Bound by the matrix cores (4 head_dim flops for each query, head and key it
+// sees).  A workgroup holds a block of query rows of one key head (row r is
+// token r / share, head r % share of the group, so grouped heads read each key
+// tile once) and walks the key tiles that any of its rows sees.
+//  - Keys and values go from the pages straight into LDS, 64 keys a tile, two
+//    tiles deep, 16 bytes a lane, no registers between; the 16-byte chunks of a row are
+//    permuted by the row on the way in, so that no LDS read below meets a
+//    bank twice.  Rows past the sequence's end, and pages that are none, arrive as zeros.
+//  - A wave owns 32 rows.  S^T = K Q^T on 32 x 32 x 16 matrix instructions: a lane
+//    holds one query (column lane % 32) and 16 keys of every 32, the lane 32 away
+//    the other 16, so a row's maximum is a chain of v_max and one exchange.
+//  - O^T = V^T P^T takes the weights as they lie in registers: its contraction
+//    slots are bound to the keys that a lane scored.  V^T comes out of LDS
+//    through the transposing read (16 lanes: 4 keys x 16 elements).
+//  - The weights are rounded once to the operands' type (relative error one
+//    unit, averaged over the keys seen).  The running maximum is only raised when a row's
+//    grows by more than 2^kLazy: a rescale of O costs as much as the rest of the softmax.
+//  - A value that is NaN or infinite in a place that only some rows of a tile see
+//    would reach the others as 0 * NaN.  That shows in their results: a
+//    wave whose output is not finite is computed again key by key
+//    (plain_row), which gives rows that do see such a value theirs.
+#include "attention_device.hpp"
+
+namespace slim {
+namespace {
+
+constexpr int kKeys = 64;            // keys of a tile
+constexpr float kLazy = 8.0f;        // weights stay at or below 2^kLazy
+constexpr int kTargetMin = 4;        // tiles of a split, at least
+
+// LDS position of 16-byte chunk c of row r (of a tile's rows of D/8 chunks).
+// K: 16 consecutive rows' same chunk lie in 16 different bank groups.
+template <int D>
+__device__ __forceinline__ int k_place(int r, int c) {
+    if constexpr (D == 64) return c ^ ((r >> 1) & 7);
+    if constexpr (D == 96) return c ^ ((r >> 2) & 3);
+    return c ^ (r & 15);
+}
+// V: 4 consecutive rows' same 64 bytes lie in different bank groups.
+template <int D>
+__device__ __forceinline__ int v_place(int r, int c) {
+    if constexpr (D == 64) return c ^ (((r >> 1) & 1) << 2);
+    if constexpr (D == 96) return c;
+    return c ^ ((r & 3) << 2);
+}
+
+typedef short s4v __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ u2 lds_tr(uint32_t at) {
+    return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                      (__attribute__((address_space(3))) s4v*)(size_t)at));
+}
+
+// x of the lane in the lower half and of the one 32 above it.
+struct Halves { float lo, hi; };
+__device__ __forceinline__ Halves halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(int, x), __builtin_bit_cast(int, x), false, false);
+    const unsigned lo = r[0], hi = r[1];      // a bit_cast of r[1] itself reads element 0
+    return {__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
+}
+
+__device__ __forceinline__ float half_value(const AttnArgs& a, uint16_t x) {
+    return a.dtype == 0 ? (float)__builtin_bit_cast(_Float16, x) : __builtin_bit_cast(float, (uint32_t)x << 16);
+}
+
+// One row by the whole wave, straight from the formula: lane j scores key j of
+// each tile, then owns the output elements lane + 64 i.
+template <int D>
+__device__ void plain_row(const AttnArgs& a, const Span& tiles, int first, int last, const Span& row_span,
+                          const int32_t* table, int kvh, const uint16_t* q, float (&o)[4], float& m, float& l) {
+    const int lane = threadIdx.x & 63;
+    const float scale = a.scale * 1.4426950408889634f;
+    m = -INFINITY;
+    l = 0.0f;
+    for (int i = 0; i < 4; ++i) o[i] = 0.0f;
+    for (int t = first; t < last; ++t) {
+        const int j = tiles.base(t, kKeys) + lane;
+        bool seen = row_span.seen(j);
+        int page = -1;
+        if (seen) page = table[j >> a.kv.page_shift];
+        seen = seen && page >= 0 && page < a.kv.pages;
+        const int64_t at = seen ? ((((int64_t)page * a.kv_heads + kvh) << a.kv.page_shift) +
+                                   (j & ((1 << a.kv.page_shift) - 1))) * D : 0;
+        float s = -INFINITY;
+        if (seen) {
+            s = 0.0f;
+            for (int d = 0; d < D; ++d) s = fmaf(half_value(a, q[d]), half_value(a, a.kv.k[at + d]), s);
+            s *= scale;
+        }
+        float top = s;
+        for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+        const float mn = fmaxf(m, top), ms = mn == -INFINITY ? 0.0f : mn;
+        const float f = exp2_fast(m - ms), w = seen ? exp2_fast(s - ms) : 0.0f;
+        m = mn;
+        l *= f;
+        for (int i = 0; i < 4; ++i) o[i] *= f;
+        for (uint64_t left = __ballot(seen); left; left &= left - 1) {
+            const int k = __builtin_ctzll(left);
+            const float wk = __shfl(w, k);
+            const int64_t r = __shfl(at, k);
+            l += wk;
+            for (int i = 0; i < 4; ++i)
+                if (lane + 64 * i < D) o[i] = fmaf(wk, half_value(a, a.kv.v[r + lane + 64 * i]), o[i]);
+        }
+    }
+}
+
+template <class T, int D, int NW>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_kernel(AttnArgs a, int slots, int slot0,
+                                                                                      int splits, int chunk) {
+    constexpr int kRows = 32 * NW, kTileBytes = kKeys * D * 2, kC = D / 8;      // chunks of a row
+    constexpr int kLoads = D / 32;                       // 64-lane loads of a 16-row block
+    __shared__ __align__(1024) unsigned char lds[2][2][kTileBytes];             // [buffer][K, V]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5, col = lane & 31;
+
+    // Head fastest (a workgroup's XCD is its index mod 8: with 8 or more key
+    // heads an XCD's L2 serves its own heads only), then the split, then the
+    // slot of rows, last ones first: under the causal mask they have the most keys.
+    const int share = a.q_heads / a.kv_heads;
+    int id = blockIdx.x;
+    const int kvh = id % a.kv_heads;
+    id /= a.kv_heads;
+    const int split = id % splits;
+    const int slot = slots - 1 - (slot0 + id / splits);
+
+    // Sequence b's slots begin at starts[b] * share / kRows + b: at least as
+    // many as its rows fill.  Found as find_seq finds a token's sequence.
+    int lo = 0, n = a.kv.seqs;
+    while (n > 1) {
+        const int step = (n + 63) >> 6, at = lane * step;
+        const int s = at < n ? a.kv.starts[lo + at] : 0;
+        const uint64_t ok = __ballot(at < n && (int64_t)s * share / kRows + lo + at <= slot);
+        if (ok == 0) return;
+        const int c = 63 - __builtin_clzll(ok);
+        lo += c * step;
+        n = min(step, n - c * step);
+    }
+    const int b = __builtin_amdgcn_readfirstlane(lo);
+    int row_first, count;
+    new_rows(a.kv, b, a.tokens, row_first, count);
+    const int64_t tile = slot - ((int64_t)a.kv.starts[b] * share / kRows + b);
+    if (tile < 0 || tile * kRows >= (int64_t)count * share) return;
+
+    const int len = seq_len(a.kv, b), before = len - count;             // position of new token 0
+    const int64_t r0 = tile * kRows;
+    const int rows = (int)min((int64_t)kRows, (int64_t)count * share - r0);
+    const int p_first = before + (int)(r0 / share), p_last = before + (int)((r0 + rows - 1) / share);
+    Span span = key_span(a, p_last);
+    span.start = a.window ? max(0, p_first - a.window + 1) : 0;
+    const int keys = min(len, (int)min((int64_t)a.kv.width << a.kv.page_shift, (int64_t)kMaxLen));
+    const int32_t* table = a.kv.table + (int64_t)b * a.kv.width;
+
+    const int tiles = span.tiles(kKeys);
+    const int per = max(chunk, (tiles + splits - 1) / splits);
+    const int first = min(tiles, split * per), last = min(tiles, first + per);
+
+    // This lane's query.
+    const int r = 32 * wave + col;
+    const bool live = r < rows;
+    const int token = row_first + (int)((r0 + (live ? r : 0)) / share);
+    const int head = kvh * share + (int)((r0 + (live ? r : 0)) % share);
+    const int pos = live ? before + (token - row_first) : -1;
+    Span mine = key_span(a, pos);
+    // Positions of the wave's rows: what all of them see needs no mask, what none sees is skipped.
+    const int w_rows = min(32, rows - 32 * wave);
+    const int w_first = before + (int)((r0 + 32 * wave) / share);
+    const int w_last = w_rows > 0 ? before + (int)((r0 + 32 * wave + w_rows - 1) / share) : -1;
+    const bool whole_wave = w_rows == 32;
+
+    u4 qf[D / 16];
+    // Scores are compared before they are scaled, so the scale's sign goes into the queries (exact).
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+    const float scale = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        qf[i] = u4{0, 0, 0, 0};
+        if (live && a.scale != 0.0f) {
+            qf[i] = *reinterpret_cast<const u4*>(a.q + token * a.sq + (int64_t)head * D + 16 * i + 8 * half);
+            qf[i] ^= flip;
+        }
+    }
+
+    // Loads of a tile: its eight 16-row blocks (4 of K, 4 of V) over the waves.
+    const uint32_t lds0 = lds_u32(&lds[0][0][0]);
+    auto block_page = [&](int key) {
+        const int at = key >> a.kv.page_shift;
+        const int page = key < keys ? table[at] : -1;
+        return page >= 0 && page < a.kv.pages ? page : -1;
+    };
+    auto load = [&](int buf, int base) {
+#pragma unroll
+        for (int i = 0; i < 8 / NW; ++i) {
+            const int block = wave * (8 / NW) + i, rb = block >> 1;     // 16-row block, K or V
+            const bool is_v = block & 1;
+            const int key = base + 16 * rb;
+            const int page = block_page(key);
+            const uint16_t* pool = is_v ? a.kv.v : a.kv.k;
+            const int64_t row = (((int64_t)max(page, 0) * a.kv_heads + kvh) << a.kv.page_shift) +
+                                (key & ((1 << a.kv.page_shift) - 1));
+            const int valid = page < 0 ? 0 : min(16, keys - key);
+            const u4 rsrc = rsrc_words(pool + row * D, (int64_t)valid * D * 2);
+            const uint32_t to = lds0 + (buf * 2 + is_v) * kTileBytes + rb * 16 * D * 2;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int c = 64 * j + lane, rr = c / kC, place = c - rr * kC;
+                const int from = is_v ? v_place<D>(rr, place) : k_place<D>(rr, place);
+                lds_load16_at(rsrc, to + 1024 * j, rr * (D * 2) + from * 16, 0);
+            }
+        }
+    };
+
+    float m = -INFINITY, l = 0.0f;
+    f16v o[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+
+    if (first < last) load(0, span.base(first, kKeys));
+    for (int t = first; t < last; ++t) {
+        const int buf = (t - first) & 1, base = span.base(t, kKeys);
+        wait_vmem_below<0>();
+        __syncthreads();                      // tile t has landed for all waves, and all are done with tile t - 1
+        if (t + 1 < last) load(buf ^ 1, span.base(t + 1, kKeys));
+        const uint32_t kt = lds0 + buf * 2 * kTileBytes, vt = kt + kTileBytes;
+
+        // Skip what no row of the wave sees (its rows' windows start at or after the first one's).
+        if (w_rows <= 0 || base > w_last ||
+            (a.window && base + kKeys <= w_first - a.window + 1 && base >= a.sinks)) continue;
+
+        f16v s[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[kb][e] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const int row = 32 * kb + col;
+                const u4 kf = lds_ld<u4>(kt + row * (D * 2) + k_place<D>(row, 2 * i + half) * 16);
+                s[kb] = T::mfma32(kf, qf[i], s[kb]);
+            }
+        }
+
+        bool owned = true;
+#pragma unroll
+        for (int rb = 0; rb < 4; ++rb) owned = owned && block_page(base + 16 * rb) >= 0;
+        const bool all = whole_wave && owned && base + kKeys <= min(w_first + 1, keys) &&
+                         (!a.window || base > w_last - a.window || base + kKeys <= a.sinks);
+        if (!all) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int j = base + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
+                    const bool seen = mine.seen(j) && block_page(base + 32 * kb + 16 * (e >> 3)) >= 0;
+                    s[kb][e] = seen ? s[kb][e] : -INFINITY;
+                }
+        }
+
+        float top = s[0][0];
+#pragma unroll
+        for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
+        const Halves tops = halves(top);
+        top = fmaxf(tops.lo, tops.hi) * scale;
+        if (__any(top > m + kLazy)) {
+            const float mn = fmaxf(m, top);
+            const float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) o[i] *= f;
+        }
+        const float ms = m == -INFINITY ? 0.0f : m;
+        u4 w[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = exp2_fast(fmaf(s[g >> 1][8 * (g & 1) + 2 * i], scale, -ms));
+                const float y = exp2_fast(fmaf(s[g >> 1][8 * (g & 1) + 2 * i + 1], scale, -ms));
+                l += x + y;
+                w[g][i] = T::pack(x, y);
+            }
+
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            // Rows 16 g + 4 half + lane % 16 / 4 and 8 further; 16 elements of 32 i + 16 (col / 16).
+            const int row = 16 * g + 4 * half + ((lane & 15) >> 2);
+            const int c0 = 2 * (col >> 4) + ((lane & 3) >> 1);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint32_t at = vt + row * (D * 2) + v_place<D>(row, 4 * i + c0) * 16 + (lane & 1) * 8;
+                const u2 x = lds_tr(at), y = lds_tr(at + 8 * D * 2);            // v_place repeats every 8 rows
+                o[i] = T::mfma32(u4{x[0], x[1], y[0], y[1]}, w[g], o[i]);
+            }
+        }
+    }
+
+    // Lane and the one 32 away hold the two halves of a row's sum.
+    const Halves sums = halves(l);
+    l = sums.lo + sums.hi;
+    float probe = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) probe = fmaf(o[i][e], 0.0f, probe);
+    const Partials parts(a, D, splits);
+    if (__any(live && !(probe == 0.0f))) {
+        for (int i = 0; i < w_rows; ++i) {
+            const int64_t rr = r0 + 32 * wave + i;
+            const int tk = row_first + (int)(rr / share), hd = kvh * share + (int)(rr % share);
+            float x[4], mx, lx;
+            plain_row<D>(a, span, first, last, key_span(a, before + tk - row_first), table, kvh,
+                         a.q + tk * a.sq + (int64_t)hd * D, x, mx, lx);
+            const int64_t row = (int64_t)tk * a.q_heads + hd;
+            for (int k = 0; k < 4; ++k) {
+                const int d = lane + 64 * k;
+                if (d >= D) continue;
+                if (splits > 1) {
+                    parts.o[(row * splits + split) * D + d] = x[k];
+                } else {
+                    a.o[tk * a.so + (int64_t)hd * D + d] = (uint16_t)T::pack(lx == 0.0f ? 0.0f : x[k] / lx, 0.0f);
+                    if (d == 0 && a.lse)
+                        a.lse[row] = lx == 0.0f ? -INFINITY : mx * 0.6931471805599453f + logf(lx);
+                }
+            }
+            if (splits > 1 && lane == 0) parts.mark(row, split, mx, lx);
+        }
+        return;
+    }
+    if (!live) return;
+    const int64_t row = (int64_t)token * a.q_heads + head;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f4 x = {o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
+            const int d = 32 * i + 8 * e + 4 * half;
+            if (splits > 1) parts.put4(row, split, d, x);
+            else store_row4<T>(a, token, head, D, d, x, m, l);
+        }
+    if (splits > 1 && half == 0) parts.mark(row, split, m, l);
+}
+
+template <class T, int D, int NW>
+hipError_t launch(const AttnArgs& a, hipStream_t stream) {
+    constexpr int kRows = 32 * NW;
+    const int share = a.q_heads / a.kv_heads;
+    const int64_t slots = (int64_t)a.tokens * share / kRows + a.kv.seqs;
+    int64_t most = a.max_len;
+    if (a.window && (int64_t)a.window + a.sinks + kRows < most) most = (int64_t)a.window + a.sinks + kRows;
+    const int64_t tiles = (most + kKeys - 1) / kKeys, units = slots * a.kv_heads;
+    const int64_t want = kPrefillSplitTarget / units, can = (tiles + kTargetMin - 1) / kTargetMin;
+    const int64_t splits = max((int64_t)1, min(want, can));
+    const int chunk = (int)max((int64_t)1, (tiles + splits - 1) / splits);
+    // A grid holds fewer than 2^32 threads; slots past it go into further launches.
+    const int64_t per_slot = a.kv_heads * splits, at_once = ((int64_t(1) << 32) / (64 * NW) - 1) / per_slot;
+    for (int64_t s = 0; s < slots; s += at_once) {
+        const int64_t n = min(at_once, slots - s);
+        hipLaunchKernelGGL((attention_prefill_kernel<T, D, NW>), dim3((unsigned)(n * per_slot)), dim3(64 * NW), 0, stream,
+                           a, (int)slots, (int)s, (int)splits, chunk);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return splits == 1 ? hipSuccess : launch_attention_join(a, (int)splits, stream);
+}
+
+template <class T>
+hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
+    switch (a.head_dim) {
+        case 64: return launch<T, 64, 4>(a, stream);
+        case 96: return launch<T, 96, 4>(a, stream);
+        case 128: return launch<T, 128, 4>(a, stream);
+        default: return launch<T, 256, 4>(a, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_attention_prefill(const AttnArgs& a, hipStream_t stream) {
+    // One new token of every sequence is the single-token form.
+    if (!a.kv.starts) return launch_attention_decode(a, stream);
+    return a.dtype == 0 ? launch_dim<Fp16>(a, stream) : launch_dim<Bf16>(a, stream);
+}
+
+}  // namespace slim
