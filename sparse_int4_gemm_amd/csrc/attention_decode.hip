@@ -29,27 +29,27 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = 32;            // keys of one wave's step
 
+// Where a tile lies: its first key and the pages of its 16-key halves (-1: none).
+struct Place {
+    int base, page[2];
+};
+
 // The registers of one tile.
 template <int D>
 struct Tile {
     u4 k[2][D / 32];                 // K rows 16 t + lane % 16, elements 32 c + 8 g + [0, 8)
     uint32_t v[8][D / 32];           // V rows 16 t + 4 g + i, elements (D/16)(lane % 16) + [0, D/16)
-    int base;                        // first key
-    bool owned[2];                   // both 16-key halves: a valid page
+    Place at;
 };
 
 template <int D>
-__device__ __forceinline__ void load_tile(Tile<D>& x, const AttnArgs& a, const int32_t* table, int kvh, int base) {
+__device__ __forceinline__ void load_tile(Tile<D>& x, const AttnArgs& a, int kvh, const Place& at) {
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    x.base = base;
+    x.at = at;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const int key = base + 16 * t;
-        const int at = key >> a.kv.page_shift;
-        const int page = at < a.kv.width ? table[at] : -1;
-        x.owned[t] = page >= 0 && page < a.kv.pages;
-        const int64_t row = (((int64_t)(x.owned[t] ? page : 0) * a.kv_heads + kvh) << a.kv.page_shift) +
-                            (key & ((1 << a.kv.page_shift) - 1));
+        const int64_t row = (((int64_t)max(at.page[t], 0) * a.kv_heads + kvh) << a.kv.page_shift) +
+                            ((at.base + 16 * t) & ((1 << a.kv.page_shift) - 1));
         const uint16_t* k = a.kv.k + row * D;
         const uint16_t* v = a.kv.v + row * D;
 #pragma unroll
@@ -65,7 +65,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
     constexpr int VE = D / 16;
     __shared__ float o_join[kWaves][16][D + 4];
     __shared__ float m_join[kWaves][16], l_join[kWaves][16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
     const int split = blockIdx.x % splits, b = blockIdx.x / splits;
     const int kvh = blockIdx.y / groups, share = a.q_heads / a.kv_heads;
     const int h0 = kvh * share + (blockIdx.y - kvh * groups) * 16;             // this workgroup's query heads
@@ -96,7 +97,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
 #pragma unroll
     for (int e = 0; e < VE; ++e) o[e] = f4{0, 0, 0, 0};
 
-    const int32_t* table = a.kv.table + (int64_t)b * a.kv.width;
     auto step = [&](Tile<D>& x) {
         f4 s[2];
 #pragma unroll
@@ -107,12 +107,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
             s[t] *= scale;
         }
         // A tile whose every key is seen and owned needs no mask (the same answer in all lanes).
-        if (!(span.all_seen(x.base, kTile) && x.owned[0] && x.owned[1])) {
+        if (!(span.all_seen(x.at.base, kTile) && x.at.page[0] >= 0 && x.at.page[1] >= 0)) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const bool seen = x.owned[t] && span.seen(x.base + 16 * t + 4 * g + i);
+                    const bool seen = x.at.page[t] >= 0 && span.seen(x.at.base + 16 * t + 4 * g + i);
                     if (!seen) {
                         s[t][i] = -INFINITY;
 #pragma unroll
@@ -153,27 +153,43 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
     };
 
     // Two tiles in flight: the next one's loads are issued before the current
-    // one is used.  At head size 256 two tiles (256 registers) do not fit; the CU's
-    // eight waves then keep eight 32 KB tiles in flight between them.
+    // one is used, with the pages of the one after it.  At head size 256 two tiles (256
+    // registers) do not fit; the CU's eight waves then keep eight 32 KB tiles
+    // in flight between them.
+    const int keys = max(0, span.end);
+    auto place = [&](int i) {
+        Place at;
+        at.base = __builtin_amdgcn_readfirstlane(span.base(min(i, last - 1), kTile));
+        at.page[0] = page_of(a, b, at.base, keys);
+        at.page[1] = page_of(a, b, at.base + 16, keys);
+        return at;
+    };
     int i = first + wave;
-    if constexpr (D > 128) {
-        for (; i < last; i += kWaves) {
-            Tile<D> x;
-            load_tile<D>(x, a, table, kvh, span.base(i, kTile));
-            step(x);
-        }
-    } else if (i < last) {
-        Tile<D> x, y;
-        load_tile<D>(x, a, table, kvh, span.base(i, kTile));
-        for (;;) {
-            load_tile<D>(y, a, table, kvh, span.base(min(i + kWaves, last - 1), kTile));
-            step(x);
-            i += kWaves;
-            if (i >= last) break;
-            load_tile<D>(x, a, table, kvh, span.base(min(i + kWaves, last - 1), kTile));
-            step(y);
-            i += kWaves;
-            if (i >= last) break;
+    if (i < last) {
+        Place next = place(i);
+        if constexpr (D > 128) {
+            for (; i < last; i += kWaves) {
+                Tile<D> x;
+                load_tile<D>(x, a, kvh, next);
+                next = place(i + kWaves);
+                step(x);
+            }
+        } else {
+            Tile<D> x, y;
+            load_tile<D>(x, a, kvh, next);
+            next = place(i + kWaves);
+            for (;;) {
+                load_tile<D>(y, a, kvh, next);
+                next = place(i + 2 * kWaves);
+                step(x);
+                i += kWaves;
+                if (i >= last) break;
+                load_tile<D>(x, a, kvh, next);
+                next = place(i + 2 * kWaves);
+                step(y);
+                i += kWaves;
+                if (i >= last) break;
+            }
         }
     }
 

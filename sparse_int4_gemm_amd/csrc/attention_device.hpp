@@ -88,6 +88,19 @@ struct Span {
     }
 };
 
+// Page of a sequence's key `key` (the same in all lanes), -1 if it has none
+// (from `keys` on, or an entry out of range).  Read through the scalar cache: a
+// vector load would be waited for behind every key and value load in flight,
+// since those return in order.
+typedef const __attribute__((address_space(4))) int32_t* ScalarInts;
+__device__ __forceinline__ int page_of(const AttnArgs& a, int b, int key, int keys) {
+    key = __builtin_amdgcn_readfirstlane(key);
+    if (key >= keys) return -1;
+    const ScalarInts table = (ScalarInts)(uintptr_t)(a.kv.table + (int64_t)b * a.kv.width);
+    const int page = table[key >> a.kv.page_shift];
+    return page >= 0 && page < a.kv.pages ? page : -1;
+}
+
 // Of a single position p.
 __device__ __forceinline__ Span key_span(const AttnArgs& a, int p) {
     const int64_t capacity = (int64_t)a.kv.width << a.kv.page_shift;      // at most 2^30

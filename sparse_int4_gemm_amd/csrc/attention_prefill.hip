@@ -184,20 +184,24 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
         }
     }
 
+    // Where a tile lies: its first key and the pages of its 16-key blocks (-1: none).
+    struct Place { int base, page[4]; };
+    auto place = [&](int t) {
+        Place at;
+        at.base = __builtin_amdgcn_readfirstlane(span.base(min(t, last - 1), kKeys));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at.page[i] = page_of(a, b, at.base + 16 * i, keys);
+        return at;
+    };
     // Loads of a tile: its eight 16-row blocks (4 of K, 4 of V) over the waves.
     const uint32_t lds0 = lds_u32(&lds[0][0][0]);
-    auto block_page = [&](int key) {
-        const int at = key >> a.kv.page_shift;
-        const int page = key < keys ? table[at] : -1;
-        return page >= 0 && page < a.kv.pages ? page : -1;
-    };
-    auto load = [&](int buf, int base) {
+    auto load = [&](int buf, const Place& at) {
 #pragma unroll
         for (int i = 0; i < 8 / NW; ++i) {
             const int block = wave * (8 / NW) + i, rb = block >> 1;     // 16-row block, K or V
             const bool is_v = block & 1;
-            const int key = base + 16 * rb;
-            const int page = block_page(key);
+            const int key = at.base + 16 * rb;
+            const int page = rb == 0 ? at.page[0] : rb == 1 ? at.page[1] : rb == 2 ? at.page[2] : at.page[3];
             const uint16_t* pool = is_v ? a.kv.v : a.kv.k;
             const int64_t row = (((int64_t)max(page, 0) * a.kv_heads + kvh) << a.kv.page_shift) +
                                 (key & ((1 << a.kv.page_shift) - 1));
@@ -220,12 +224,25 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
 
-    if (first < last) load(0, span.base(first, kKeys));
+    // Pages are read a tile ahead of the loads that need them.
+    Place now, next;
+    if (first < last) {
+        next = place(first);
+        load(0, next);
+        now = next;
+        next = place(first + 1);
+    }
     for (int t = first; t < last; ++t) {
-        const int buf = (t - first) & 1, base = span.base(t, kKeys);
+        const int buf = (t - first) & 1, base = now.base;
+        const bool owned = now.page[0] >= 0 && now.page[1] >= 0 && now.page[2] >= 0 && now.page[3] >= 0;
+        const Place cur = now;
         wait_vmem_below<0>();
         __syncthreads();                      // tile t has landed for all waves, and all are done with tile t - 1
-        if (t + 1 < last) load(buf ^ 1, span.base(t + 1, kKeys));
+        if (t + 1 < last) {
+            load(buf ^ 1, next);
+            now = next;
+            next = place(t + 2);
+        }
         const uint32_t kt = lds0 + buf * 2 * kTileBytes, vt = kt + kTileBytes;
 
         // Skip what no row of the wave sees (its rows' windows start at or after the first one's).
@@ -245,9 +262,6 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
             }
         }
 
-        bool owned = true;
-#pragma unroll
-        for (int rb = 0; rb < 4; ++rb) owned = owned && block_page(base + 16 * rb) >= 0;
         const bool all = whole_wave && owned && base + kKeys <= min(w_first + 1, keys) &&
                          (!a.window || base > w_last - a.window || base + kKeys <= a.sinks);
         if (!all) {
@@ -256,7 +270,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int j = base + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
-                    const bool seen = mine.seen(j) && block_page(base + 32 * kb + 16 * (e >> 3)) >= 0;
+                    const bool seen = mine.seen(j) && cur.page[2 * kb + (e >> 3)] >= 0;
                     s[kb][e] = seen ? s[kb][e] : -INFINITY;
                 }
         }
