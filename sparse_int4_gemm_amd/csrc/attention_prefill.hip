@@ -217,6 +217,18 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
         }
     };
 
+    // Where this lane reads a tile (K in buffer 0): K row col, chunk 2 i + half,
+    // and 32 rows on; V rows 4 half + lane % 16 / 4 (+ 8, + 16 g), elements
+    // 32 i + 16 (col / 16) + 4 (lane % 4).  The other rows are constant offsets.
+    uint32_t k_at[D / 16], v_at[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) k_at[i] = lds0 + col * (D * 2) + k_place<D>(col, 2 * i + half) * 16;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        const int row = 4 * half + ((lane & 15) >> 2), chunk = 4 * i + 2 * (col >> 4) + ((lane & 3) >> 1);
+        v_at[i] = lds0 + kTileBytes + row * (D * 2) + v_place<D>(row, chunk) * 16 + (lane & 1) * 8;
+    }
+
     float m = -INFINITY, l = 0.0f;
     f16v o[D / 32];
 #pragma unroll
@@ -243,24 +255,40 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
             now = next;
             next = place(t + 2);
         }
-        const uint32_t kt = lds0 + buf * 2 * kTileBytes, vt = kt + kTileBytes;
+        const uint32_t in_buf = buf * 2 * kTileBytes;
 
         // Skip what no row of the wave sees (its rows' windows start at or after the first one's).
         if (w_rows <= 0 || base > w_last ||
             (a.window && base + kKeys <= w_first - a.window + 1 && base >= a.sinks)) continue;
 
+        // All reads of K first: one by one, each matrix instruction would wait for its own.
         f16v s[2];
+        u4 kf[2][D / 16];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) kf[kb][i] = lds_ld<u4>(k_at[i] + in_buf + kb * 32 * D * 2);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[kb][e] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const int row = 32 * kb + col;
-                const u4 kf = lds_ld<u4>(kt + row * (D * 2) + k_place<D>(row, 2 * i + half) * 16);
-                s[kb] = T::mfma32(kf, qf[i], s[kb]);
-            }
+            for (int i = 0; i < D / 16; ++i) s[kb] = T::mfma32(kf[kb][i], qf[i], s[kb]);
         }
+        // The first half of V is read while the weights are made.
+        u4 vf[4][D / 32];
+        auto read_v = [&](int g) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint32_t at = v_at[i] + in_buf + g * 16 * D * 2;
+                const u2 x = lds_tr(at), y = lds_tr(at + 8 * D * 2);            // v_place repeats every 8 rows
+                vf[g][i] = u4{x[0], x[1], y[0], y[1]};
+            }
+        };
+        read_v(0);
+        read_v(1);
+        __builtin_amdgcn_sched_barrier(0);
 
         const bool all = whole_wave && owned && base + kKeys <= min(w_first + 1, keys) &&
                          (!a.window || base > w_last - a.window || base + kKeys <= a.sinks);
@@ -302,15 +330,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
 
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            // Rows 16 g + 4 half + lane % 16 / 4 and 8 further; 16 elements of 32 i + 16 (col / 16).
-            const int row = 16 * g + 4 * half + ((lane & 15) >> 2);
-            const int c0 = 2 * (col >> 4) + ((lane & 3) >> 1);
+            if (g < 2) read_v(g + 2);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint32_t at = vt + row * (D * 2) + v_place<D>(row, 4 * i + c0) * 16 + (lane & 1) * 8;
-                const u2 x = lds_tr(at), y = lds_tr(at + 8 * D * 2);            // v_place repeats every 8 rows
-                o[i] = T::mfma32(u4{x[0], x[1], y[0], y[1]}, w[g], o[i]);
-            }
+            for (int i = 0; i < D / 32; ++i) o[i] = T::mfma32(vf[g][i], w[g], o[i]);
         }
     }
 
