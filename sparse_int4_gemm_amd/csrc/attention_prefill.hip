@@ -165,11 +165,16 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
     const int head = kvh * share + (int)((r0 + (live ? r : 0)) % share);
     const int pos = live ? before + (token - row_first) : -1;
     Span mine = key_span(a, pos);
-    // Positions of the wave's rows: what all of them see needs no mask, what none sees is skipped.
+    // Positions of the wave's rows.  No row sees a tile that begins past w_last,
+    // nor one from `sinks` on that begins at or before `hidden`; every row sees all of
+    // one that begins in [all_from, all_to], or that holds sinks only, up to all_to.
     const int w_rows = min(32, rows - 32 * wave);
     const int w_first = before + (int)((r0 + 32 * wave) / share);
     const int w_last = w_rows > 0 ? before + (int)((r0 + 32 * wave + w_rows - 1) / share) : -1;
-    const bool whole_wave = w_rows == 32;
+    const int sinks = a.window ? a.sinks : 0;
+    const int hidden = a.window ? w_first - a.window + 1 - kKeys : -1;
+    const int all_to = w_rows == 32 ? min(w_first + 1, keys) - kKeys : -1;
+    const int all_from = a.window ? w_last - a.window + 1 : 0;
 
     u4 qf[D / 16];
     // Scores are compared before they are scaled, so the scale's sign goes into the queries (exact).
@@ -184,36 +189,57 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
         }
     }
 
-    // Where a tile lies: its first key and the pages of its 16-key blocks (-1: none).
-    struct Place { int base, page[4]; };
+    // Scalar bookkeeping of a tile, made a tile ahead of the loads that need it:
+    // its first key, which of its four 16-key blocks have a page, and for the
+    // block that this wave loads its place in the pool and its bytes (none
+    // past the sequence's end).  The tile's K and V rows go 16 a wave, or with 8
+    // waves K to the lower four and V to the upper four.
+    constexpr int kSides = NW == 8 ? 1 : 2;
+    const int own = 16 * (wave & 3);
+    const int64_t page_bytes = ((int64_t)a.kv_heads * D * 2) << a.kv.page_shift;
+    const int64_t head_bytes = ((int64_t)kvh * D * 2) << a.kv.page_shift;
+    const int row_mask = (1 << a.kv.page_shift) - 1;
+    const int sink_tiles = span.sink_tiles(kKeys), window_tile = span.start / kKeys - sink_tiles;
+    struct Place { int base, pages, bytes; int64_t at; };
     auto place = [&](int t) {
-        Place at;
-        at.base = __builtin_amdgcn_readfirstlane(span.base(min(t, last - 1), kKeys));
+        Place x;
+        t = __builtin_amdgcn_readfirstlane(min(t, last - 1));
+        x.base = (t < sink_tiles ? t : t + window_tile) * kKeys;
+        int page;
+        if (a.kv.page_shift >= 6) {                          // the tile lies in one page
+            page = page_of(a, b, x.base, keys);
+            x.pages = page < 0 ? 0 : 15;
+        } else {
+            x.pages = 0;
+            page = page_of(a, b, x.base + own, keys);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) at.page[i] = page_of(a, b, at.base + 16 * i, keys);
-        return at;
+            for (int i = 0; i < 4; ++i) x.pages |= page_of(a, b, x.base + 16 * i, keys) < 0 ? 0 : 1 << i;
+        }
+        const int key = x.base + own;
+        x.bytes = page < 0 ? 0 : max(0, min(16, keys - key)) * (D * 2);
+        x.at = max(page, 0) * page_bytes + head_bytes + (key & row_mask) * (D * 2);
+        return x;
     };
-    // Loads of a tile: its eight 16-row blocks (4 of K, 4 of V) over the waves.
+    // Of a 16-row block's 16-byte chunks, load j takes 64 j + lane in LDS order.
     const uint32_t lds0 = lds_u32(&lds[0][0][0]);
-    auto load = [&](int buf, const Place& at) {
+    uint32_t k_from[kLoads], v_from[kLoads];
 #pragma unroll
-        for (int i = 0; i < 8 / NW; ++i) {
-            const int block = wave * (8 / NW) + i, rb = block >> 1;     // 16-row block, K or V
-            const bool is_v = block & 1;
-            const int key = at.base + 16 * rb;
-            const int page = rb == 0 ? at.page[0] : rb == 1 ? at.page[1] : rb == 2 ? at.page[2] : at.page[3];
-            const uint16_t* pool = is_v ? a.kv.v : a.kv.k;
-            const int64_t row = (((int64_t)max(page, 0) * a.kv_heads + kvh) << a.kv.page_shift) +
-                                (key & ((1 << a.kv.page_shift) - 1));
-            const int valid = page < 0 ? 0 : min(16, keys - key);
-            const u4 rsrc = rsrc_words(pool + row * D, (int64_t)valid * D * 2);
-            const uint32_t to = lds0 + (buf * 2 + is_v) * kTileBytes + rb * 16 * D * 2;
+    for (int j = 0; j < kLoads; ++j) {
+        const int c = 64 * j + lane, r = c / kC;
+        k_from[j] = r * (D * 2) + k_place<D>(r, c - r * kC) * 16;
+        v_from[j] = r * (D * 2) + v_place<D>(r, c - r * kC) * 16;
+    }
+    auto load = [&](int buf, const Place& x) {
+        const uint32_t to = lds0 + buf * 2 * kTileBytes + own * (D * 2);
+        if (kSides == 2 || wave < 4) {
+            const u4 rsrc = rsrc_words(reinterpret_cast<const unsigned char*>(a.kv.k) + x.at, x.bytes);
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int c = 64 * j + lane, rr = c / kC, place = c - rr * kC;
-                const int from = is_v ? v_place<D>(rr, place) : k_place<D>(rr, place);
-                lds_load16_at(rsrc, to + 1024 * j, rr * (D * 2) + from * 16, 0);
-            }
+            for (int j = 0; j < kLoads; ++j) lds_load16_at(rsrc, to + 1024 * j, k_from[j], 0);
+        }
+        if (kSides == 2 || wave >= 4) {
+            const u4 rsrc = rsrc_words(reinterpret_cast<const unsigned char*>(a.kv.v) + x.at, x.bytes);
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) lds_load16_at(rsrc, to + kTileBytes + 1024 * j, v_from[j], 0);
         }
     };
 
@@ -236,7 +262,6 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
 
-    // Pages are read a tile ahead of the loads that need them.
     Place now, next;
     if (first < last) {
         next = place(first);
@@ -245,9 +270,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
         next = place(first + 1);
     }
     for (int t = first; t < last; ++t) {
-        const int buf = (t - first) & 1, base = now.base;
-        const bool owned = now.page[0] >= 0 && now.page[1] >= 0 && now.page[2] >= 0 && now.page[3] >= 0;
-        const Place cur = now;
+        const int buf = (t - first) & 1, base = now.base, pages = now.pages;
         wait_vmem_below<0>();
         __syncthreads();                      // tile t has landed for all waves, and all are done with tile t - 1
         if (t + 1 < last) {
@@ -256,10 +279,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
             next = place(t + 2);
         }
         const uint32_t in_buf = buf * 2 * kTileBytes;
+        uint32_t ka[D / 16], va[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) ka[i] = k_at[i] + in_buf;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) va[i] = v_at[i] + in_buf;
 
         // Skip what no row of the wave sees (its rows' windows start at or after the first one's).
-        if (w_rows <= 0 || base > w_last ||
-            (a.window && base + kKeys <= w_first - a.window + 1 && base >= a.sinks)) continue;
+        if (base > w_last || (base <= hidden && base >= sinks)) continue;
 
         // All reads of K first: one by one, each matrix instruction would wait for its own.
         f16v s[2];
@@ -267,7 +294,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) kf[kb][i] = lds_ld<u4>(k_at[i] + in_buf + kb * 32 * D * 2);
+            for (int i = 0; i < D / 16; ++i) kf[kb][i] = lds_ld<u4>(ka[i] + kb * 32 * D * 2);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
@@ -281,7 +308,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
         auto read_v = [&](int g) {
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                const uint32_t at = v_at[i] + in_buf + g * 16 * D * 2;
+                const uint32_t at = va[i] + g * 16 * D * 2;
                 const u2 x = lds_tr(at), y = lds_tr(at + 8 * D * 2);            // v_place repeats every 8 rows
                 vf[g][i] = u4{x[0], x[1], y[0], y[1]};
             }
@@ -290,18 +317,18 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
         read_v(1);
         __builtin_amdgcn_sched_barrier(0);
 
-        const bool all = whole_wave && owned && base + kKeys <= min(w_first + 1, keys) &&
-                         (!a.window || base > w_last - a.window || base + kKeys <= a.sinks);
+        const bool all = pages == 15 && base <= all_to && (base >= all_from || base <= sinks - kKeys);
         if (!all) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int j = base + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
-                    const bool seen = mine.seen(j) && cur.page[2 * kb + (e >> 3)] >= 0;
+                    const bool seen = mine.seen(j) && (pages >> (2 * kb + (e >> 3)) & 1);
                     s[kb][e] = seen ? s[kb][e] : -INFINITY;
                 }
         }
+        asm("" : "+v"(s[0]), "+v"(s[1]));      // one set of registers for both paths
 
         float top = s[0][0];
 #pragma unroll
