@@ -189,33 +189,43 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
         }
     }
 
-    // Scalar bookkeeping of a tile, made a tile ahead of the loads that need it:
-    // its first key, which of its four 16-key blocks have a page, and for the
-    // block that this wave loads its place in the pool and its bytes (none
-    // past the sequence's end).  The tile's K and V rows go 16 a wave, or with 8
-    // waves K to the lower four and V to the upper four.
+    // Bookkeeping of a tile: its first key, which of its four 16-key blocks have
+    // a page, and of the block that this wave loads its place in the pool
+    // and its bytes (none past the sequence's end).  The tile's K and V rows
+    // go 16 a wave, or with 8 waves K to the lower four and V to the upper
+    // four.  Lane j of `pages` and `page` holds tile from + j's: a table entry
+    // looked up for each tile would be waited for each time.
     constexpr int kSides = NW == 8 ? 1 : 2;
     const int own = 16 * (wave & 3);
     const int64_t page_bytes = ((int64_t)a.kv_heads * D * 2) << a.kv.page_shift;
     const int64_t head_bytes = ((int64_t)kvh * D * 2) << a.kv.page_shift;
     const int row_mask = (1 << a.kv.page_shift) - 1;
     const int sink_tiles = span.sink_tiles(kKeys), window_tile = span.start / kKeys - sink_tiles;
+    int pages_of = 0, page_of_own = 0, from = first;
+    auto look_up = [&](int t0) {
+        from = t0;
+        const int t = min(t0 + lane, last - 1), base = (t < sink_tiles ? t : t + window_tile) * kKeys;
+        int page[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = base + 16 * i;
+            page[i] = key < keys ? table[key >> a.kv.page_shift] : -1;
+        }
+        pages_of = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool is = page[i] >= 0 && page[i] < a.kv.pages;
+            pages_of |= is ? 1 << i : 0;
+            if (i == (wave & 3)) page_of_own = is ? page[i] : -1;
+        }
+    };
     struct Place { int base, pages, bytes; int64_t at; };
     auto place = [&](int t) {
         Place x;
-        t = __builtin_amdgcn_readfirstlane(min(t, last - 1));
+        t = min(t, last - 1);
         x.base = (t < sink_tiles ? t : t + window_tile) * kKeys;
-        int page;
-        if (a.kv.page_shift >= 6) {                          // the tile lies in one page
-            page = page_of(a, b, x.base, keys);
-            x.pages = page < 0 ? 0 : 15;
-        } else {
-            x.pages = 0;
-            page = page_of(a, b, x.base + own, keys);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x.pages |= page_of(a, b, x.base + 16 * i, keys) < 0 ? 0 : 1 << i;
-        }
-        const int key = x.base + own;
+        x.pages = __builtin_amdgcn_readlane(pages_of, t - from);
+        const int page = __builtin_amdgcn_readlane(page_of_own, t - from), key = x.base + own;
         x.bytes = page < 0 ? 0 : max(0, min(16, keys - key)) * (D * 2);
         x.at = max(page, 0) * page_bytes + head_bytes + (key & row_mask) * (D * 2);
         return x;
@@ -262,21 +272,20 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
 
-    Place now, next;
+    Place now;
     if (first < last) {
-        next = place(first);
-        load(0, next);
-        now = next;
-        next = place(first + 1);
+        look_up(first);
+        now = place(first);
+        load(0, now);
     }
     for (int t = first; t < last; ++t) {
         const int buf = (t - first) & 1, base = now.base, pages = now.pages;
         wait_vmem_below<0>();
         __syncthreads();                      // tile t has landed for all waves, and all are done with tile t - 1
         if (t + 1 < last) {
-            load(buf ^ 1, next);
-            now = next;
-            next = place(t + 2);
+            if (t + 1 - from == 64) look_up(t + 1);
+            now = place(t + 1);
+            load(buf ^ 1, now);
         }
         const uint32_t in_buf = buf * 2 * kTileBytes;
         uint32_t ka[D / 16], va[D / 32];
