@@ -164,16 +164,18 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
     const int token = row_first + (int)((r0 + (live ? r : 0)) / share);
     const int head = kvh * share + (int)((r0 + (live ? r : 0)) % share);
     const int pos = live ? before + (token - row_first) : -1;
-    Span mine = key_span(a, pos);
-    // Positions of the wave's rows.  No row sees a tile that begins past w_last,
-    // nor one from `sinks` on that begins at or before `hidden`; every row sees all of
-    // one that begins in [all_from, all_to], or that holds sinks only, up to all_to.
+    const Span mine = key_span(a, pos);
+    // The wave's own tiles [w_begin, w_end): its rows see none of the others.
+    // Every row sees all of a 32-key half that begins in [all_from, all_to],
+    // and of one that holds sinks only, up to all_to.
     const int w_rows = min(32, rows - 32 * wave);
     const int w_first = before + (int)((r0 + 32 * wave) / share);
     const int w_last = w_rows > 0 ? before + (int)((r0 + 32 * wave + w_rows - 1) / share) : -1;
-    const int sinks = a.window ? a.sinks : 0;
-    const int hidden = a.window ? w_first - a.window + 1 - kKeys : -1;
-    const int all_to = w_rows == 32 ? min(w_first + 1, keys) - kKeys : -1;
+    const int sinks = span.sinks, sink_tiles = span.sink_tiles(kKeys), window_tile = span.start / kKeys - sink_tiles;
+    const int w_end = w_last < 0 ? first : max(first, min(last, w_last / kKeys - window_tile + 1));
+    const int w_begin = a.window && sinks == 0
+                            ? max(first, min(w_end, max(0, w_first - a.window + 1) / kKeys - window_tile)) : first;
+    const int all_to = w_rows == 32 ? min(w_first + 1, keys) - kKeys / 2 : -1;
     const int all_from = a.window ? w_last - a.window + 1 : 0;
 
     u4 qf[D / 16];
@@ -191,17 +193,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
 
     // Bookkeeping of a tile: its first key, which of its four 16-key blocks have
     // a page, and of the block that this wave loads its place in the pool
-    // and its bytes (none past the sequence's end).  The tile's K and V rows
+    // and its rows (those before the sequence's end).  The tile's K and V rows
     // go 16 a wave, or with 8 waves K to the lower four and V to the upper
-    // four.  Lane j of `pages` and `page` holds tile from + j's: a table entry
-    // looked up for each tile would be waited for each time.
+    // four.  Lane j holds it for tile from + j: a table entry looked up for
+    // each tile would be waited for each time.
     constexpr int kSides = NW == 8 ? 1 : 2;
     const int own = 16 * (wave & 3);
-    const int64_t page_bytes = ((int64_t)a.kv_heads * D * 2) << a.kv.page_shift;
-    const int64_t head_bytes = ((int64_t)kvh * D * 2) << a.kv.page_shift;
     const int row_mask = (1 << a.kv.page_shift) - 1;
-    const int sink_tiles = span.sink_tiles(kKeys), window_tile = span.start / kKeys - sink_tiles;
-    int pages_of = 0, page_of_own = 0, from = first;
+    int at_lo = 0, at_hi = 0, blocks = 0, from = first;
     auto look_up = [&](int t0) {
         from = t0;
         const int t = min(t0 + lane, last - 1), base = (t < sink_tiles ? t : t + window_tile) * kKeys;
@@ -211,59 +210,70 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
             const int key = base + 16 * i;
             page[i] = key < keys ? table[key >> a.kv.page_shift] : -1;
         }
-        pages_of = 0;
+        blocks = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bool is = page[i] >= 0 && page[i] < a.kv.pages;
-            pages_of |= is ? 1 << i : 0;
-            if (i == (wave & 3)) page_of_own = is ? page[i] : -1;
+            blocks |= is ? 1 << i : 0;
+            if (i == (wave & 3)) {
+                const int key = base + own;
+                const int64_t at = ((((int64_t)(is ? page[i] : 0) * a.kv_heads + kvh) << a.kv.page_shift) +
+                                    (key & row_mask)) * (D * 2);
+                at_lo = (int)at;
+                at_hi = (int)(at >> 32);
+                blocks |= is ? max(0, min(16, keys - key)) << 4 : 0;
+            }
         }
     };
-    struct Place { int base, pages, bytes; int64_t at; };
+    struct Place { int base, blocks, lo, hi; };
     auto place = [&](int t) {
         Place x;
-        t = min(t, last - 1);
         x.base = (t < sink_tiles ? t : t + window_tile) * kKeys;
-        x.pages = __builtin_amdgcn_readlane(pages_of, t - from);
-        const int page = __builtin_amdgcn_readlane(page_of_own, t - from), key = x.base + own;
-        x.bytes = page < 0 ? 0 : max(0, min(16, keys - key)) * (D * 2);
-        x.at = max(page, 0) * page_bytes + head_bytes + (key & row_mask) * (D * 2);
+        x.blocks = __builtin_amdgcn_readlane(blocks, t - from);
+        x.lo = __builtin_amdgcn_readlane(at_lo, t - from);
+        x.hi = __builtin_amdgcn_readlane(at_hi, t - from);
         return x;
     };
     // Of a 16-row block's 16-byte chunks, load j takes 64 j + lane in LDS order.
+    // Load j's rows differ from load 0's in bits that the permutation moves
+    // through unchanged, so one register gives all (not at D = 96, where a load
+    // ends inside a row).
     const uint32_t lds0 = lds_u32(&lds[0][0][0]);
-    uint32_t k_from[kLoads], v_from[kLoads];
+    auto source = [&](bool is_v, int j) {
+        const int c = 64 * j + lane, r = c / kC, at = c - r * kC;
+        return (uint32_t)(r * (D * 2) + (is_v ? v_place<D>(r, at) : k_place<D>(r, at)) * 16);
+    };
+    constexpr int kKept = D == 96 ? kLoads : 1;
+    uint32_t k_from[kKept], v_from[kKept];
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-        const int c = 64 * j + lane, r = c / kC;
-        k_from[j] = r * (D * 2) + k_place<D>(r, c - r * kC) * 16;
-        v_from[j] = r * (D * 2) + v_place<D>(r, c - r * kC) * 16;
+    for (int j = 0; j < kKept; ++j) {
+        k_from[j] = source(false, j);
+        v_from[j] = source(true, j);
     }
-    auto load = [&](int buf, const Place& x) {
-        const uint32_t to = lds0 + buf * 2 * kTileBytes + own * (D * 2);
-        if (kSides == 2 || wave < 4) {
-            const u4 rsrc = rsrc_words(reinterpret_cast<const unsigned char*>(a.kv.k) + x.at, x.bytes);
+    auto from_of = [&](bool is_v, int j) {
+        if constexpr (D == 96) return is_v ? v_from[j] : k_from[j];
+        const int r = 64 / kC * j;                // load j's first row
+        return is_v ? (v_from[0] ^ (uint32_t)(v_place<D>(r, 0) * 16)) + 1024 * j
+                    : (k_from[0] ^ (uint32_t)(k_place<D>(r, 0) * 16)) + 1024 * j;
+    };
+    auto load = [&](bool is_v, int buf, const Place& x) {
+        const unsigned char* pool = reinterpret_cast<const unsigned char*>(is_v ? a.kv.v : a.kv.k);
+        const u4 rsrc = rsrc_words(pool + (int64_t)((uint64_t)(uint32_t)x.lo | (uint64_t)(uint32_t)x.hi << 32),
+                                   (x.blocks >> 4) * (D * 2));
+        const uint32_t to = lds0 + (2 * buf + is_v) * kTileBytes + own * (D * 2);
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) lds_load16_at(rsrc, to + 1024 * j, k_from[j], 0);
-        }
-        if (kSides == 2 || wave >= 4) {
-            const u4 rsrc = rsrc_words(reinterpret_cast<const unsigned char*>(a.kv.v) + x.at, x.bytes);
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) lds_load16_at(rsrc, to + kTileBytes + 1024 * j, v_from[j], 0);
-        }
+        for (int j = 0; j < kLoads; ++j) lds_load16_at(rsrc, to + 1024 * j, from_of(is_v, j), 0);
     };
 
-    // Where this lane reads a tile (K in buffer 0): K row col, chunk 2 i + half,
-    // and 32 rows on; V rows 4 half + lane % 16 / 4 (+ 8, + 16 g), elements
-    // 32 i + 16 (col / 16) + 4 (lane % 4).  The other rows are constant offsets.
-    uint32_t k_at[D / 16], v_at[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) k_at[i] = lds0 + col * (D * 2) + k_place<D>(col, 2 * i + half) * 16;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        const int row = 4 * half + ((lane & 15) >> 2), chunk = 4 * i + 2 * (col >> 4) + ((lane & 3) >> 1);
-        v_at[i] = lds0 + kTileBytes + row * (D * 2) + v_place<D>(row, chunk) * 16 + (lane & 1) * 8;
-    }
+    // Where this lane reads a tile: K row col, chunk 2 i + half; V rows
+    // 4 half + lane % 16 / 4 (+ 8, + 16 g), elements 32 i + 16 (col / 16) + 4 (lane % 4).
+    // The chunk's i enters as an exclusive or (at D = 96 in part as a sum).
+    const uint32_t k_at = lds0 + col * (D * 2) + k_place<D>(col, half) * 16;
+    const int v_row = 4 * half + ((lane & 15) >> 2);
+    const uint32_t v_at = lds0 + kTileBytes + v_row * (D * 2) +
+                          v_place<D>(v_row, 2 * (col >> 4) + ((lane & 3) >> 1)) * 16 + (lane & 1) * 8;
+    auto k_read = [&](uint32_t at, int i) { return D == 96 ? (at ^ (32u * (i & 1))) + 64 * (i >> 1) : at ^ (32u * i); };
+    auto v_read = [&](uint32_t at, int i) { return D == 96 ? at + 64 * i : at ^ (64u * i); };
 
     float m = -INFINITY, l = 0.0f;
     f16v o[D / 32];
@@ -272,105 +282,140 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
 
-    Place now;
-    if (first < last) {
-        look_up(first);
-        now = place(first);
-        load(0, now);
+    // Software pipeline over 32-key halves j of the tiles.  While the softmax
+    // of half j runs on the vector unit, the matrix unit has the scores of half
+    // j + 1 and the values of half j - 1 to work on, whose operands were read
+    // from LDS during half j - 1; so K is needed a tile ahead of V.
+    f16v s0, s1;
+    u4 kf[D / 16], vf[2][D / 32], w[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        w[g] = u4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) vf[g][i] = u4{0, 0, 0, 0};
     }
-    for (int t = first; t < last; ++t) {
-        const int buf = (t - first) & 1, base = now.base, pages = now.pages;
-        wait_vmem_below<0>();
-        __syncthreads();                      // tile t has landed for all waves, and all are done with tile t - 1
-        if (t + 1 < last) {
-            if (t + 1 - from == 64) look_up(t + 1);
-            now = place(t + 1);
-            load(buf ^ 1, now);
+    auto read_k = [&](uint32_t off) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) kf[i] = lds_ld<u4>(k_read(k_at + off, i));
+    };
+    auto score = [&](f16v& s) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) s = T::mfma32(kf[i], qf[i], s);
+    };
+    auto add_values = [&] {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) o[i] = T::mfma32(vf[g][i], w[g], o[i]);
+    };
+    // Half `u` of the tile at `base`: `cur` holds its scores, `nxt` takes the next ones'.
+    auto half_step = [&](f16v& cur, f16v& nxt, int base, int blocks_of, uint32_t k_next, uint32_t v_cur) {
+        const bool all = (blocks_of & 3) == 3 && base <= all_to && (base >= all_from || base <= sinks - kKeys / 2);
+        if (!all) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int j = base + 8 * (e >> 2) + 4 * half + (e & 3);
+                const bool seen = mine.seen(j) && (blocks_of >> (e >> 3) & 1);
+                cur[e] = seen ? cur[e] : -INFINITY;
+            }
         }
-        const uint32_t in_buf = buf * 2 * kTileBytes;
-        uint32_t ka[D / 16], va[D / 32];
+        asm("" : "+v"(cur));                      // one set of registers for both paths
+        add_values();
+        float top = cur[0];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) ka[i] = k_at[i] + in_buf;
+        for (int e = 1; e < 16; ++e) top = fmaxf(top, cur[e]);
+        const Halves tops = halves(top);
+        top = fmaxf(tops.lo, tops.hi) * scale;
+        const bool raise = __any(top > m + kLazy);
+        const float was = m;
+        m = raise ? fmaxf(m, top) : m;
+        const float ms = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) va[i] = v_at[i] + in_buf;
-
-        // Skip what no row of the wave sees (its rows' windows start at or after the first one's).
-        if (base > w_last || (base <= hidden && base >= sinks)) continue;
-
-        // All reads of K first: one by one, each matrix instruction would wait for its own.
-        f16v s[2];
-        u4 kf[2][D / 16];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) kf[kb][i] = lds_ld<u4>(ka[i] + kb * 32 * D * 2);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[kb][e] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) s[kb] = T::mfma32(kf[kb][i], qf[i], s[kb]);
-        }
-        // The first half of V is read while the weights are made.
-        u4 vf[4][D / 32];
-        auto read_v = [&](int g) {
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                const uint32_t at = va[i] + g * 16 * D * 2;
+                const uint32_t at = v_read(v_at + v_cur, i) + g * 16 * D * 2;
                 const u2 x = lds_tr(at), y = lds_tr(at + 8 * D * 2);            // v_place repeats every 8 rows
                 vf[g][i] = u4{x[0], x[1], y[0], y[1]};
             }
-        };
-        read_v(0);
-        read_v(1);
-        __builtin_amdgcn_sched_barrier(0);
-
-        const bool all = pages == 15 && base <= all_to && (base >= all_from || base <= sinks - kKeys);
-        if (!all) {
+        score(nxt);
+        float sum = 0.0f;
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int j = base + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
-                    const bool seen = mine.seen(j) && (pages >> (2 * kb + (e >> 3)) & 1);
-                    s[kb][e] = seen ? s[kb][e] : -INFINITY;
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float x = exp2_fast(fmaf(cur[8 * g + 2 * i], scale, -ms));
+                const float y = exp2_fast(fmaf(cur[8 * g + 2 * i + 1], scale, -ms));
+                sum += x + y;
+                w[g][i] = T::pack(x, y);
+            }
+        read_k(k_next);
+        // The order wanted: the products with V among the search for the maximum, those with K among the exponentials.
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // matrix
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);      // vector
         }
-        asm("" : "+v"(s[0]), "+v"(s[1]));      // one set of registers for both paths
-
-        float top = s[0][0];
 #pragma unroll
-        for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
-        const Halves tops = halves(top);
-        top = fmaxf(tops.lo, tops.hi) * scale;
-        if (__any(top > m + kLazy)) {
-            const float mn = fmaxf(m, top);
-            const float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
-            m = mn;
+        for (int i = 0; i < D / 16; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);      // LDS reads
+            __builtin_amdgcn_sched_group_barrier(0x002, 5 * 8 / (D / 16), 0);
+            __builtin_amdgcn_sched_group_barrier(0x400, 2 * 8 / (D / 16), 0);      // exponentials
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, D / 16, 0);
+        asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(sum));      // the weights are made among the products above
+        if (raise) {
+            const float f = m == -INFINITY ? 1.0f : exp2_fast(was - m);
             l *= f;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) o[i] *= f;
         }
-        const float ms = m == -INFINITY ? 0.0f : m;
-        u4 w[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = exp2_fast(fmaf(s[g >> 1][8 * (g & 1) + 2 * i], scale, -ms));
-                const float y = exp2_fast(fmaf(s[g >> 1][8 * (g & 1) + 2 * i + 1], scale, -ms));
-                l += x + y;
-                w[g][i] = T::pack(x, y);
-            }
+        l += sum;
+    };
 
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            if (g < 2) read_v(g + 2);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) o[i] = T::mfma32(vf[g][i], w[g], o[i]);
-        }
+    // Every wave takes part in every step t of the loads, from first - 1 to last - 1.
+    Place cur, next;                              // of tiles t and t + 1
+    if (first < last) {
+        look_up(first);
+        cur = next = place(first);
+        if (kSides == 2 || wave < 4) load(false, 0, next);
     }
+    Place after = next;
+    auto advance = [&](int t) {
+        const int odd = (t - first) & 1;
+        cur = next;
+        next = after;
+        wait_vmem_below<0>();
+        __syncthreads();          // K of tile t + 1 and V of tile t have landed for all waves; all are done with K t and V t - 1
+        if (t + 2 < last) {
+            if (t + 2 - from == 64) look_up(t + 2);
+            after = place(t + 2);
+            if (kSides == 2 || wave < 4) load(false, odd, after);
+        }
+        if (t + 1 < last && (kSides == 2 || wave >= 4)) load(true, odd ^ 1, next);
+    };
+    constexpr uint32_t kHalf = kKeys / 2 * D * 2;
+    int t = first - 1;
+    if (first == last) t = last;
+    for (; t < w_begin - 1; ++t) advance(t);
+    if (w_begin < w_end) {
+        advance(t);
+        const uint32_t k_buf = ((t - first) & 1 ^ 1) * 2 * kTileBytes;
+        read_k(k_buf);
+        score(s0);
+        read_k(k_buf + kHalf);
+        for (++t; t < w_end; ++t) {
+            advance(t);
+            const uint32_t buf = ((t - first) & 1) * 2 * kTileBytes, other = 2 * kTileBytes - buf;
+            half_step(s0, s1, cur.base, cur.blocks, other, buf);
+            half_step(s1, s0, cur.base + kKeys / 2, cur.blocks >> 2, other + kHalf, buf + kHalf);
+        }
+        add_values();
+    }
+    for (; t < last; ++t) advance(t);
 
     // Lane and the one 32 away hold the two halves of a row's sum.
     const Halves sums = halves(l);
