@@ -74,14 +74,10 @@ hipError_t launch_attention_join(const AttnArgs& a, int splits, hipStream_t stre
     return hipGetLastError();
 }
 
-// Partials of the split forms: a bounded number of workgroups with a bounded
-// number of rows each, whatever the batch, so one workspace serves every
-// batch of its heads.
+// Partials of a bounded number of (row, split) pairs, whatever the batch, so
+// one workspace serves every batch of its heads.
 size_t attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
-    const int64_t share = q_heads / kv_heads;
-    const int64_t decode = kDecodeSplitTarget * (share < kDecodeRows ? share : (int64_t)kDecodeRows);
-    const int64_t prefill = kPrefillSplitTarget * kPrefillRows;
-    const size_t parts = (size_t)(decode > prefill ? decode : prefill) * (size_t)(head_dim + 2) * sizeof(float);
+    const size_t parts = (size_t)kAttnSplitRows * (size_t)(head_dim + 2) * sizeof(float);
     return kAttnReserved + ((parts + 255) & ~size_t(255));
 }
 

@@ -231,9 +231,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
     }
 }
 
-// Splits of each of `units` row blocks: kDecodeSplitTarget workgroups in all,
-// each with at least kMinTiles tiles.
-constexpr int kMinTiles = 16;
+// Splits: kSplitTarget workgroups in all, each with at least kMinTiles tiles.
+constexpr int kSplitTarget = 2048, kMinTiles = 16;
 
 template <class T, int D>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
@@ -242,7 +241,8 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     if (a.window && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;
     const int tiles = (int)((most + kTile - 1) / kTile);
     const int64_t units = (int64_t)a.tokens * a.kv_heads * groups;
-    const int splits = (int)max((int64_t)1, min(kDecodeSplitTarget / units, (int64_t)((tiles + kMinTiles - 1) / kMinTiles)));
+    const int64_t want = min(kSplitTarget / units, (int64_t)((tiles + kMinTiles - 1) / kMinTiles));
+    const int splits = (int)max((int64_t)1, min(want, kAttnSplitRows / ((int64_t)a.tokens * a.q_heads)));
     const int chunk = max(kWaves, (tiles + splits - 1) / splits);
     dim3 grid((unsigned)(a.tokens * splits), (unsigned)(a.kv_heads * groups));
     hipLaunchKernelGGL((attention_decode_kernel<T, D>), grid, dim3(64 * kWaves), 0, stream, a, splits, chunk, groups);

@@ -29,7 +29,12 @@ namespace {
 
 constexpr int kKeys = 64;            // keys of a tile
 constexpr float kLazy = 8.0f;        // weights stay at or below 2^kLazy
-constexpr int kTargetMin = 4;        // tiles of a split, at least
+#ifndef PNW
+#define PNW 4
+#define PQB 1
+#endif
+// Splits: kSplitTarget workgroups in all, each with at least kMinTiles tiles.
+constexpr int kSplitTarget = 256, kMinTiles = 4;
 
 // LDS position of 16-byte chunk c of row r (of a tile's rows of D/8 chunks).
 // K: 16 consecutive rows' same chunk lie in 16 different bank groups.
@@ -108,10 +113,10 @@ __device__ void plain_row(const AttnArgs& a, const Span& tiles, int first, int l
     }
 }
 
-template <class T, int D, int NW>
-__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_kernel(AttnArgs a, int slots, int slot0,
-                                                                                      int splits, int chunk) {
-    constexpr int kRows = 32 * NW, kTileBytes = kKeys * D * 2, kC = D / 8;      // chunks of a row
+template <class T, int D, int NW, int QB>
+__global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attention_prefill_kernel(
+    AttnArgs a, int slots, int slot0, int splits, int chunk) {
+    constexpr int kWaveRows = 32 * QB, kRows = kWaveRows * NW, kTileBytes = kKeys * D * 2, kC = D / 8;      // chunks of a row
     constexpr int kLoads = D / 32;                       // 64-lane loads of a 16-row block
     __shared__ __align__(1024) unsigned char lds[2][2][kTileBytes];             // [buffer][K, V]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -158,49 +163,52 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
     const int per = max(chunk, (tiles + splits - 1) / splits);
     const int first = min(tiles, split * per), last = min(tiles, first + per);
 
-    // This lane's query.
-    const int r = 32 * wave + col;
-    const bool live = r < rows;
-    const int token = row_first + (int)((r0 + (live ? r : 0)) / share);
-    const int head = kvh * share + (int)((r0 + (live ? r : 0)) % share);
-    const int pos = live ? before + (token - row_first) : -1;
-    const Span mine = key_span(a, pos);
-    // The wave's own tiles [w_begin, w_end): its rows see none of the others.
-    // Every row sees all of a 32-key half that begins in [all_from, all_to],
-    // and of one that holds sinks only, up to all_to.
-    const int w_rows = min(32, rows - 32 * wave);
-    const int w_first = before + (int)((r0 + 32 * wave) / share);
-    const int w_last = w_rows > 0 ? before + (int)((r0 + 32 * wave + w_rows - 1) / share) : -1;
-    const int sinks = span.sinks, sink_tiles = span.sink_tiles(kKeys), window_tile = span.start / kKeys - sink_tiles;
-    const int w_end = w_last < 0 ? first : max(first, min(last, w_last / kKeys - window_tile + 1));
-    const int w_begin = a.window && sinks == 0
-                            ? max(first, min(w_end, max(0, w_first - a.window + 1) / kKeys - window_tile)) : first;
-    const int all_to = w_rows == 32 ? min(w_first + 1, keys) - kKeys / 2 : -1;
-    const int all_from = a.window ? w_last - a.window + 1 : 0;
-
-    u4 qf[D / 16];
+    // This lane's queries, one of each of the wave's QB blocks of 32 rows.
+    bool live[QB];
+    int token[QB], head[QB];
+    Span mine[QB];
+    u4 qf[QB][D / 16];
     // Scores are compared before they are scaled, so the scale's sign goes into the queries (exact).
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     const float scale = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-        qf[i] = u4{0, 0, 0, 0};
-        if (live && a.scale != 0.0f) {
-            qf[i] = *reinterpret_cast<const u4*>(a.q + token * a.sq + (int64_t)head * D + 16 * i + 8 * half);
-            qf[i] ^= flip;
+    for (int q = 0; q < QB; ++q) {
+        const int r = kWaveRows * wave + 32 * q + col;
+        live[q] = r < rows;
+        const int64_t at = r0 + (live[q] ? r : 0);
+        token[q] = row_first + (int)(at / share);
+        head[q] = kvh * share + (int)(at % share);
+        mine[q] = key_span(a, live[q] ? before + (token[q] - row_first) : -1);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            qf[q][i] = u4{0, 0, 0, 0};
+            if (live[q] && a.scale != 0.0f) {
+                qf[q][i] = *reinterpret_cast<const u4*>(a.q + token[q] * a.sq + (int64_t)head[q] * D + 16 * i + 8 * half);
+                qf[q][i] ^= flip;
+            }
         }
     }
+    // The wave's own tiles [w_begin, w_end): its rows see none of the others.
+    // Every row sees all of a 32-key half that begins in [all_from, all_to],
+    // and of one that holds sinks only, up to all_to.
+    const int w_rows = min(kWaveRows, rows - kWaveRows * wave);
+    const int w_first = before + (int)((r0 + kWaveRows * wave) / share);
+    const int w_last = w_rows > 0 ? before + (int)((r0 + kWaveRows * wave + w_rows - 1) / share) : -1;
+    const int sinks = span.sinks, sink_tiles = span.sink_tiles(kKeys), window_tile = span.start / kKeys - sink_tiles;
+    const int w_end = w_last < 0 ? first : max(first, min(last, w_last / kKeys - window_tile + 1));
+    const int w_begin = a.window && sinks == 0
+                            ? max(first, min(w_end, max(0, w_first - a.window + 1) / kKeys - window_tile)) : first;
+    const int all_to = w_rows == kWaveRows ? min(w_first + 1, keys) - kKeys / 2 : -1;
+    const int all_from = a.window ? w_last - a.window + 1 : 0;
 
     // Bookkeeping of a tile: its first key, which of its four 16-key blocks have
     // a page, and of the block that this wave loads its place in the pool
-    // and its rows (those before the sequence's end).  The tile's K and V rows
-    // go 16 a wave, or with 8 waves K to the lower four and V to the upper
-    // four.  Lane j holds it for tile from + j: a table entry looked up for
+    // and its rows (those before the sequence's end).  A wave loads the K and V
+    // rows of the blocks wave, wave + NW, ...  Lane j holds it for tile from + j: a table entry looked up for
     // each tile would be waited for each time.
-    constexpr int kSides = NW == 8 ? 1 : 2;
-    const int own = 16 * (wave & 3);
+    constexpr int kOwn = 4 / NW;                  // blocks of a wave
     const int row_mask = (1 << a.kv.page_shift) - 1;
-    int at_lo = 0, at_hi = 0, blocks = 0, from = first;
+    int at_lo[kOwn] = {}, at_hi[kOwn] = {}, blocks = 0, from = first;
     auto look_up = [&](int t0) {
         from = t0;
         const int t = min(t0 + lane, last - 1), base = (t < sink_tiles ? t : t + window_tile) * kKeys;
@@ -215,23 +223,26 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
         for (int i = 0; i < 4; ++i) {
             const bool is = page[i] >= 0 && page[i] < a.kv.pages;
             blocks |= is ? 1 << i : 0;
-            if (i == (wave & 3)) {
-                const int key = base + own;
+            if (i % NW == wave) {
+                const int key = base + 16 * i;
                 const int64_t at = ((((int64_t)(is ? page[i] : 0) * a.kv_heads + kvh) << a.kv.page_shift) +
                                     (key & row_mask)) * (D * 2);
-                at_lo = (int)at;
-                at_hi = (int)(at >> 32);
-                blocks |= is ? max(0, min(16, keys - key)) << 4 : 0;
+                at_lo[i / NW] = (int)at;
+                at_hi[i / NW] = (int)(at >> 32);
+                blocks |= is ? max(0, min(16, keys - key)) << (4 + 8 * (i / NW)) : 0;
             }
         }
     };
-    struct Place { int base, blocks, lo, hi; };
+    struct Place { int base, blocks, lo[kOwn], hi[kOwn]; };
     auto place = [&](int t) {
         Place x;
         x.base = (t < sink_tiles ? t : t + window_tile) * kKeys;
         x.blocks = __builtin_amdgcn_readlane(blocks, t - from);
-        x.lo = __builtin_amdgcn_readlane(at_lo, t - from);
-        x.hi = __builtin_amdgcn_readlane(at_hi, t - from);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            x.lo[i] = __builtin_amdgcn_readlane(at_lo[i], t - from);
+            x.hi[i] = __builtin_amdgcn_readlane(at_hi[i], t - from);
+        }
         return x;
     };
     // Of a 16-row block's 16-byte chunks, load j takes 64 j + lane in LDS order.
@@ -258,11 +269,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
     };
     auto load = [&](bool is_v, int buf, const Place& x) {
         const unsigned char* pool = reinterpret_cast<const unsigned char*>(is_v ? a.kv.v : a.kv.k);
-        const u4 rsrc = rsrc_words(pool + (int64_t)((uint64_t)(uint32_t)x.lo | (uint64_t)(uint32_t)x.hi << 32),
-                                   (x.blocks >> 4) * (D * 2));
-        const uint32_t to = lds0 + (2 * buf + is_v) * kTileBytes + own * (D * 2);
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) lds_load16_at(rsrc, to + 1024 * j, from_of(is_v, j), 0);
+        for (int i = 0; i < kOwn; ++i) {
+            const u4 rsrc = rsrc_words(pool + (int64_t)((uint64_t)(uint32_t)x.lo[i] | (uint64_t)(uint32_t)x.hi[i] << 32),
+                                       (x.blocks >> (4 + 8 * i) & 31) * (D * 2));
+            const uint32_t to = lds0 + (2 * buf + is_v) * kTileBytes + (wave + NW * i) * 16 * (D * 2);
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) lds_load16_at(rsrc, to + 1024 * j, from_of(is_v, j), 0);
+        }
     };
 
     // Where this lane reads a tile: K row col, chunk 2 i + half; V rows
@@ -275,105 +289,153 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
     auto k_read = [&](uint32_t at, int i) { return D == 96 ? (at ^ (32u * (i & 1))) + 64 * (i >> 1) : at ^ (32u * i); };
     auto v_read = [&](uint32_t at, int i) { return D == 96 ? at + 64 * i : at ^ (64u * i); };
 
-    float m = -INFINITY, l = 0.0f;
-    f16v o[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
-
+    float m[QB], l[QB];
+    f16v o[QB][D / 32];
     // Software pipeline over 32-key halves j of the tiles.  While the softmax
     // of half j runs on the vector unit, the matrix unit has the scores of half
     // j + 1 and the values of half j - 1 to work on, whose operands were read
     // from LDS during half j - 1; so K is needed a tile ahead of V.
-    f16v s0, s1;
-    u4 kf[D / 16], vf[2][D / 32], w[2];
+    f16v s0[QB], s1[QB];
+    u4 kf[D / 16], vf[2][D / 32], w[QB][2];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        w[g] = u4{0, 0, 0, 0};
+    for (int q = 0; q < QB; ++q) {
+        m[q] = -INFINITY;
+        l[q] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) vf[g][i] = u4{0, 0, 0, 0};
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[q][i][e] = 0.0f;
+        w[q][0] = w[q][1] = u4{0, 0, 0, 0};
     }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) vf[0][i] = vf[1][i] = u4{0, 0, 0, 0};
     auto read_k = [&](uint32_t off) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) kf[i] = lds_ld<u4>(k_read(k_at + off, i));
     };
-    auto score = [&](f16v& s) {
+    auto score = [&](f16v (&s)[QB]) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+        for (int q = 0; q < QB; ++q)
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) s = T::mfma32(kf[i], qf[i], s);
+            for (int e = 0; e < 16; ++e) s[q][e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int q = 0; q < QB; ++q) s[q] = T::mfma32(kf[i], qf[q][i], s[q]);
     };
-    auto add_values = [&] {
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) o[i] = T::mfma32(vf[g][i], w[g], o[i]);
+    constexpr int kV = D / 32, kK = D / 16;       // matrix operands of 16 keys of V, of 32 keys of K
+    // With two blocks of rows the operands that no vector instruction touches go
+    // to the accumulation registers.
+    auto put_away = [](u4& x) {
+        if constexpr (QB == 2) asm("" : "+a"(x));
     };
-    // Half `u` of the tile at `base`: `cur` holds its scores, `nxt` takes the next ones'.
-    auto half_step = [&](f16v& cur, f16v& nxt, int base, int blocks_of, uint32_t k_next, uint32_t v_cur) {
+    auto add_value = [&](int n) {                 // n of the 2 kV operands of a half
+        put_away(vf[n / kV][n % kV]);
+#pragma unroll
+        for (int q = 0; q < QB; ++q) o[q][n % kV] = T::mfma32(vf[n / kV][n % kV], w[q][n / kV], o[q][n % kV]);
+    };
+    // A half of the tile, from key `base` on: `cur` holds its scores, `nxt` takes the next half's.
+    // The order of the code is the order of issue (the empty barriers hold the
+    // compiler to it): vector work between any two matrix instructions, so
+    // that neither unit waits for the other.
+    auto half_step = [&](f16v (&cur)[QB], f16v (&nxt)[QB], int base, int blocks_of, uint32_t k_next, uint32_t v_cur) {
         const bool all = (blocks_of & 3) == 3 && base <= all_to && (base >= all_from || base <= sinks - kKeys / 2);
         if (!all) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int j = base + 8 * (e >> 2) + 4 * half + (e & 3);
-                const bool seen = mine.seen(j) && (blocks_of >> (e >> 3) & 1);
-                cur[e] = seen ? cur[e] : -INFINITY;
-            }
+            for (int q = 0; q < QB; ++q)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int j = base + 8 * (e >> 2) + 4 * half + (e & 3);
+                    const bool seen = mine[q].seen(j) && (blocks_of >> (e >> 3) & 1);
+                    cur[q][e] = seen ? cur[q][e] : -INFINITY;
+                }
         }
-        asm("" : "+v"(cur));                      // one set of registers for both paths
-        add_values();
-        float top = cur[0];
 #pragma unroll
-        for (int e = 1; e < 16; ++e) top = fmaxf(top, cur[e]);
-        const Halves tops = halves(top);
-        top = fmaxf(tops.lo, tops.hi) * scale;
-        const bool raise = __any(top > m + kLazy);
-        const float was = m;
-        m = raise ? fmaxf(m, top) : m;
-        const float ms = m == -INFINITY ? 0.0f : m;
+        for (int q = 0; q < QB; ++q) asm("" : "+v"(cur[q]));      // one set of registers for both paths
+        // A quarter of the products with V: the rows' maxima.
+        constexpr int kFirst = kV / 2;
+        float was[QB], ms[QB], sum[QB], top[QB];
+        u4 wn[QB][2];
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int n = 0; n < kFirst; ++n) {
+            __builtin_amdgcn_sched_barrier(0);
+            add_value(n);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
+            for (int q = 0; q < QB; ++q)
+#pragma unroll
+                for (int e = n * 16 / kFirst; e < (n + 1) * 16 / kFirst; ++e) top[q] = e == 0 ? cur[q][0] : fmaxf(top[q], cur[q][e]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        add_value(kFirst);
+        bool over = false;
+#pragma unroll
+        for (int q = 0; q < QB; ++q) {
+            const Halves tops = halves(top[q]);
+            top[q] = fmaxf(tops.lo, tops.hi) * scale;
+            over = over || top[q] > m[q] + kLazy;
+        }
+        const bool raise = __any(over);
+#pragma unroll
+        for (int q = 0; q < QB; ++q) {
+            was[q] = m[q];
+            m[q] = raise ? fmaxf(m[q], top[q]) : m[q];
+            ms[q] = m[q] == -INFINITY ? 0.0f : m[q];
+            sum[q] = 0.0f;
+        }
+        // The others, then the scores of the next half: the weights.  Operands are
+        // read for the next half as soon as their registers are free.
+#pragma unroll
+        for (int q = 0; q < QB; ++q)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) nxt[q][e] = 0.0f;
+        constexpr int kRest = 2 * kV - kFirst - 1 + kK;
+#pragma unroll
+        for (int n = 0; n < kRest; ++n) {
+            const int k = n - (kRest - kK);                       // operand of K from 0 on
+            __builtin_amdgcn_sched_barrier(0);
+            if (k < 0) {
+                add_value(kFirst + 1 + n);
+            } else {
+                put_away(kf[k]);
+#pragma unroll
+                for (int q = 0; q < QB; ++q) {
+                    put_away(qf[q][k]);
+                    nxt[q] = T::mfma32(kf[k], qf[q][k], nxt[q]);
+                }
+                const int g = k / kV, i = k % kV;                 // kK == 2 kV
                 const uint32_t at = v_read(v_at + v_cur, i) + g * 16 * D * 2;
                 const u2 x = lds_tr(at), y = lds_tr(at + 8 * D * 2);            // v_place repeats every 8 rows
                 vf[g][i] = u4{x[0], x[1], y[0], y[1]};
+                kf[k] = lds_ld<u4>(k_read(k_at + k_next, k));
             }
-        score(nxt);
-        float sum = 0.0f;
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+            for (int p = n * 8 / kRest; p < (n + 1) * 8 / kRest; ++p)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = exp2_fast(fmaf(cur[8 * g + 2 * i], scale, -ms));
-                const float y = exp2_fast(fmaf(cur[8 * g + 2 * i + 1], scale, -ms));
-                sum += x + y;
-                w[g][i] = T::pack(x, y);
-            }
-        read_k(k_next);
-        // The order wanted: the products with V among the search for the maximum, those with K among the exponentials.
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // matrix
-            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);      // vector
+                for (int q = 0; q < QB; ++q) {
+                    const float x = exp2_fast(fmaf(cur[q][2 * p], scale, -ms[q]));
+                    const float y = exp2_fast(fmaf(cur[q][2 * p + 1], scale, -ms[q]));
+                    sum[q] += x + y;
+                    wn[q][p >> 2][p & 3] = T::pack(x, y);
+                }
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);      // LDS reads
-            __builtin_amdgcn_sched_group_barrier(0x002, 5 * 8 / (D / 16), 0);
-            __builtin_amdgcn_sched_group_barrier(0x400, 2 * 8 / (D / 16), 0);      // exponentials
+        for (int q = 0; q < QB; ++q) {
+            w[q][0] = wn[q][0];
+            w[q][1] = wn[q][1];
+            asm volatile("" : "+v"(w[q][0]), "+v"(w[q][1]), "+v"(sum[q]));      // made among the products above
         }
-        __builtin_amdgcn_sched_group_barrier(0x100, D / 16, 0);
-        asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(sum));      // the weights are made among the products above
         if (raise) {
-            const float f = m == -INFINITY ? 1.0f : exp2_fast(was - m);
-            l *= f;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) o[i] *= f;
+            for (int q = 0; q < QB; ++q) {
+                const float f = m[q] == -INFINITY ? 1.0f : exp2_fast(was[q] - m[q]);
+                l[q] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) o[q][i] *= f;
+            }
         }
-        l += sum;
+#pragma unroll
+        for (int q = 0; q < QB; ++q) l[q] += sum[q];
     };
 
     // Every wave takes part in every step t of the loads, from first - 1 to last - 1.
@@ -381,7 +443,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
     if (first < last) {
         look_up(first);
         cur = next = place(first);
-        if (kSides == 2 || wave < 4) load(false, 0, next);
+        load(false, 0, next);
     }
     Place after = next;
     auto advance = [&](int t) {
@@ -393,9 +455,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
         if (t + 2 < last) {
             if (t + 2 - from == 64) look_up(t + 2);
             after = place(t + 2);
-            if (kSides == 2 || wave < 4) load(false, odd, after);
+            load(false, odd, after);
         }
-        if (t + 1 < last && (kSides == 2 || wave >= 4)) load(true, odd ^ 1, next);
+        if (t + 1 < last) load(true, odd ^ 1, next);
     };
     constexpr uint32_t kHalf = kKeys / 2 * D * 2;
     int t = first - 1;
@@ -410,75 +472,79 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attention_prefill_k
         for (++t; t < w_end; ++t) {
             advance(t);
             const uint32_t buf = ((t - first) & 1) * 2 * kTileBytes, other = 2 * kTileBytes - buf;
-            half_step(s0, s1, cur.base, cur.blocks, other, buf);
-            half_step(s1, s0, cur.base + kKeys / 2, cur.blocks >> 2, other + kHalf, buf + kHalf);
+            half_step(s0, s1, cur.base, cur.blocks & 15, other, buf);
+            half_step(s1, s0, cur.base + kKeys / 2, cur.blocks >> 2 & 3, other + kHalf, buf + kHalf);
         }
-        add_values();
+#pragma unroll
+        for (int n = 0; n < 2 * kV; ++n) add_value(n);
     }
     for (; t < last; ++t) advance(t);
 
-    // Lane and the one 32 away hold the two halves of a row's sum.
-    const Halves sums = halves(l);
-    l = sums.lo + sums.hi;
-    float probe = 0.0f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) probe = fmaf(o[i][e], 0.0f, probe);
     const Partials parts(a, D, splits);
-    if (__any(live && !(probe == 0.0f))) {
-        for (int i = 0; i < w_rows; ++i) {
-            const int64_t rr = r0 + 32 * wave + i;
-            const int tk = row_first + (int)(rr / share), hd = kvh * share + (int)(rr % share);
-            float x[4], mx, lx;
-            plain_row<D>(a, span, first, last, key_span(a, before + tk - row_first), table, kvh,
-                         a.q + tk * a.sq + (int64_t)hd * D, x, mx, lx);
-            const int64_t row = (int64_t)tk * a.q_heads + hd;
-            for (int k = 0; k < 4; ++k) {
-                const int d = lane + 64 * k;
-                if (d >= D) continue;
-                if (splits > 1) {
-                    parts.o[(row * splits + split) * D + d] = x[k];
-                } else {
-                    a.o[tk * a.so + (int64_t)hd * D + d] = (uint16_t)T::pack(lx == 0.0f ? 0.0f : x[k] / lx, 0.0f);
-                    if (d == 0 && a.lse)
-                        a.lse[row] = lx == 0.0f ? -INFINITY : mx * 0.6931471805599453f + logf(lx);
+#pragma unroll
+    for (int q = 0; q < QB; ++q) {
+        // Lane and the one 32 away hold the two halves of a row's sum.
+        const Halves sums = halves(l[q]);
+        l[q] = sums.lo + sums.hi;
+        float probe = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) probe = fmaf(o[q][i][e], 0.0f, probe);
+        if (__any(live[q] && !(probe == 0.0f))) {
+            for (int i = 0; i < min(32, w_rows - 32 * q); ++i) {
+                const int64_t rr = r0 + kWaveRows * wave + 32 * q + i;
+                const int tk = row_first + (int)(rr / share), hd = kvh * share + (int)(rr % share);
+                float x[4], mx, lx;
+                plain_row<D>(a, span, first, last, key_span(a, before + tk - row_first), table, kvh,
+                             a.q + tk * a.sq + (int64_t)hd * D, x, mx, lx);
+                const int64_t row = (int64_t)tk * a.q_heads + hd;
+                for (int k = 0; k < 4; ++k) {
+                    const int d = lane + 64 * k;
+                    if (d >= D) continue;
+                    if (splits > 1) {
+                        parts.o[(row * splits + split) * D + d] = x[k];
+                    } else {
+                        a.o[tk * a.so + (int64_t)hd * D + d] = (uint16_t)T::pack(lx == 0.0f ? 0.0f : x[k] / lx, 0.0f);
+                        if (d == 0 && a.lse)
+                            a.lse[row] = lx == 0.0f ? -INFINITY : mx * 0.6931471805599453f + logf(lx);
+                    }
                 }
+                if (splits > 1 && lane == 0) parts.mark(row, split, mx, lx);
             }
-            if (splits > 1 && lane == 0) parts.mark(row, split, mx, lx);
+            continue;
         }
-        return;
+        if (!live[q]) continue;
+        const int64_t row = (int64_t)token[q] * a.q_heads + head[q];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f4 x = {o[q][i][4 * e], o[q][i][4 * e + 1], o[q][i][4 * e + 2], o[q][i][4 * e + 3]};
+                const int d = 32 * i + 8 * e + 4 * half;
+                if (splits > 1) parts.put4(row, split, d, x);
+                else store_row4<T>(a, token[q], head[q], D, d, x, m[q], l[q]);
+            }
+        if (splits > 1 && half == 0) parts.mark(row, split, m[q], l[q]);
     }
-    if (!live) return;
-    const int64_t row = (int64_t)token * a.q_heads + head;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const f4 x = {o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
-            const int d = 32 * i + 8 * e + 4 * half;
-            if (splits > 1) parts.put4(row, split, d, x);
-            else store_row4<T>(a, token, head, D, d, x, m, l);
-        }
-    if (splits > 1 && half == 0) parts.mark(row, split, m, l);
 }
 
-template <class T, int D, int NW>
+template <class T, int D, int NW, int QB>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-    constexpr int kRows = 32 * NW;
+    constexpr int kRows = 32 * QB * NW;
     const int share = a.q_heads / a.kv_heads;
     const int64_t slots = (int64_t)a.tokens * share / kRows + a.kv.seqs;
     int64_t most = a.max_len;
     if (a.window && (int64_t)a.window + a.sinks + kRows < most) most = (int64_t)a.window + a.sinks + kRows;
     const int64_t tiles = (most + kKeys - 1) / kKeys, units = slots * a.kv_heads;
-    const int64_t want = kPrefillSplitTarget / units, can = (tiles + kTargetMin - 1) / kTargetMin;
-    const int64_t splits = max((int64_t)1, min(want, can));
+    const int64_t want = min(kSplitTarget / units, (tiles + kMinTiles - 1) / kMinTiles);
+    const int64_t splits = max((int64_t)1, min(want, kAttnSplitRows / ((int64_t)a.tokens * a.q_heads)));
     const int chunk = (int)max((int64_t)1, (tiles + splits - 1) / splits);
     // A grid holds fewer than 2^32 threads; slots past it go into further launches.
     const int64_t per_slot = a.kv_heads * splits, at_once = ((int64_t(1) << 32) / (64 * NW) - 1) / per_slot;
     for (int64_t s = 0; s < slots; s += at_once) {
         const int64_t n = min(at_once, slots - s);
-        hipLaunchKernelGGL((attention_prefill_kernel<T, D, NW>), dim3((unsigned)(n * per_slot)), dim3(64 * NW), 0, stream,
+        hipLaunchKernelGGL((attention_prefill_kernel<T, D, NW, QB>), dim3((unsigned)(n * per_slot)), dim3(64 * NW), 0, stream,
                            a, (int)slots, (int)s, (int)splits, chunk);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -489,10 +555,10 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
 template <class T>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
     switch (a.head_dim) {
-        case 64: return launch<T, 64, 4>(a, stream);
-        case 96: return launch<T, 96, 4>(a, stream);
-        case 128: return launch<T, 128, 4>(a, stream);
-        default: return launch<T, 256, 4>(a, stream);
+        case 64: return launch<T, 64, PNW, PQB>(a, stream);
+        case 96: return launch<T, 96, PNW, PQB>(a, stream);
+        case 128: return launch<T, 128, PNW, PQB>(a, stream);
+        default: return launch<T, 256, 4, 1>(a, stream);
     }
 }
 
