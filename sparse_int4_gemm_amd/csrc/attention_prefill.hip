@@ -267,16 +267,27 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attentio
         return is_v ? (v_from[0] ^ (uint32_t)(v_place<D>(r, 0) * 16)) + 1024 * j
                     : (k_from[0] ^ (uint32_t)(k_place<D>(r, 0) * 16)) + 1024 * j;
     };
-    auto load = [&](bool is_v, int buf, const Place& x) {
+    // The wave's loads of a tile of K or V, one by one: n of kOwn * kLoads.
+    struct Source { u4 rsrc[kOwn]; uint32_t to; };
+    auto source_of = [&](bool is_v, int buf, const Place& x, bool any) {
         const unsigned char* pool = reinterpret_cast<const unsigned char*>(is_v ? a.kv.v : a.kv.k);
+        Source s;
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            const u4 rsrc = rsrc_words(pool + (int64_t)((uint64_t)(uint32_t)x.lo[i] | (uint64_t)(uint32_t)x.hi[i] << 32),
-                                       (x.blocks >> (4 + 8 * i) & 31) * (D * 2));
-            const uint32_t to = lds0 + (2 * buf + is_v) * kTileBytes + (wave + NW * i) * 16 * (D * 2);
+        for (int i = 0; i < kOwn; ++i)
+            s.rsrc[i] = rsrc_words(pool + (int64_t)((uint64_t)(uint32_t)x.lo[i] | (uint64_t)(uint32_t)x.hi[i] << 32),
+                                   any ? (x.blocks >> (4 + 8 * i) & 31) * (D * 2) : 0);
+        s.to = lds0 + (2 * buf + is_v) * kTileBytes + wave * 16 * (D * 2);
+        return s;
+    };
+    constexpr int kPieces = kOwn * kLoads;
+    auto load_piece = [&](bool is_v, const Source& s, int n) {
+        const int i = n / kLoads, j = n % kLoads;
+        lds_load16_at(s.rsrc[i], s.to + NW * i * 16 * (D * 2) + 1024 * j, from_of(is_v, j), 0);
+    };
+    auto load = [&](bool is_v, int buf, const Place& x) {
+        const Source s = source_of(is_v, buf, x, true);
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) lds_load16_at(rsrc, to + 1024 * j, from_of(is_v, j), 0);
-        }
+        for (int n = 0; n < kPieces; ++n) load_piece(is_v, s, n);
     };
 
     // Where this lane reads a tile: K row col, chunk 2 i + half; V rows
@@ -338,7 +349,8 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attentio
     // The order of the code is the order of issue (the empty barriers hold the
     // compiler to it): vector work between any two matrix instructions, so
     // that neither unit waits for the other.
-    auto half_step = [&](f16v (&cur)[QB], f16v (&nxt)[QB], int base, int blocks_of, uint32_t k_next, uint32_t v_cur) {
+    auto half_step = [&](f16v (&cur)[QB], f16v (&nxt)[QB], int base, int blocks_of, uint32_t k_next, uint32_t v_cur,
+                         auto&& between) {
         const bool all = (blocks_of & 3) == 3 && base <= all_to && (base >= all_from || base <= sinks - kKeys / 2);
         if (!all) {
 #pragma unroll
@@ -393,6 +405,7 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attentio
         for (int n = 0; n < kRest; ++n) {
             const int k = n - (kRest - kK);                       // operand of K from 0 on
             __builtin_amdgcn_sched_barrier(0);
+            between(n, kRest);
             if (k < 0) {
                 add_value(kFirst + 1 + n);
             } else {
@@ -438,47 +451,78 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attentio
         for (int q = 0; q < QB; ++q) l[q] += sum[q];
     };
 
-    // Every wave takes part in every step t of the loads, from first - 1 to last - 1.
-    Place cur, next;                              // of tiles t and t + 1
+    // Every wave takes part in every step t of the loads, from first - 1 to
+    // last - 1: at the end of `advance` K of tile t + 1 and V of tile t have
+    // landed for all waves, and all are done with K of tile t and V of tile t - 1, so
+    // the loads of K of tile t + 2 and V of tile t + 1 may begin.
+    Place cur, next, after;                       // of tiles t, t + 1 and t + 2
     if (first < last) {
         look_up(first);
         cur = next = place(first);
+        after = place(min(first + 1, last - 1));
         load(false, 0, next);
+        load(true, 0, next);
+        if (first + 1 < last) load(false, 1, after);
     }
-    Place after = next;
     auto advance = [&](int t) {
-        const int odd = (t - first) & 1;
-        cur = next;
-        next = after;
-        wait_vmem_below<0>();
-        __syncthreads();          // K of tile t + 1 and V of tile t have landed for all waves; all are done with K t and V t - 1
-        if (t + 2 < last) {
+        if (t >= first) {
+            cur = next;
+            next = after;
+            wait_vmem_below<0>();
+        } else if (first + 1 < last) {
+            wait_vmem_below<2 * kPieces>();
+        } else {
+            wait_vmem_below<kPieces>();
+        }
+        __syncthreads();
+        if (t >= first && t + 2 < last) {
             if (t + 2 - from == 64) look_up(t + 2);
             after = place(t + 2);
-            load(false, odd, after);
         }
-        if (t + 1 < last) load(true, odd ^ 1, next);
+    };
+    auto load_all = [&](int t) {
+        if (t >= first && t + 2 < last) load(false, (t - first) & 1, after);
+        if (t >= first && t + 1 < last) load(true, (t + 1 - first) & 1, next);
     };
     constexpr uint32_t kHalf = kKeys / 2 * D * 2;
-    int t = first - 1;
-    if (first == last) t = last;
-    for (; t < w_begin - 1; ++t) advance(t);
+    int t = first < last ? first - 1 : last;
+    for (; t < w_begin - 1; ++t) {
+        advance(t);
+        load_all(t);
+    }
     if (w_begin < w_end) {
         advance(t);
-        const uint32_t k_buf = ((t - first) & 1 ^ 1) * 2 * kTileBytes;
+        load_all(t);
+        const uint32_t k_buf = ((t + 1 - first) & 1) * 2 * kTileBytes;
         read_k(k_buf);
         score(s0);
         read_k(k_buf + kHalf);
         for (++t; t < w_end; ++t) {
             advance(t);
-            const uint32_t buf = ((t - first) & 1) * 2 * kTileBytes, other = 2 * kTileBytes - buf;
-            half_step(s0, s1, cur.base, cur.blocks & 15, other, buf);
-            half_step(s1, s0, cur.base + kKeys / 2, cur.blocks >> 2 & 3, other + kHalf, buf + kHalf);
+            const int odd = (t - first) & 1;
+            const uint32_t buf = odd * 2 * kTileBytes, other = 2 * kTileBytes - buf;
+            // A workgroup's loads all at once would queue at the address unit
+            // (32 of 16 cycles); here each wave spreads its own over the first half.
+            // Past the last tile they read nothing (and write zeros nobody reads).
+            const Source k_source = source_of(false, odd, after, t + 2 < last);
+            const Source v_source = source_of(true, odd ^ 1, next, t + 1 < last);
+            half_step(s0, s1, cur.base, cur.blocks & 15, other, buf, [&](int n, int of) {
+#pragma unroll
+                for (int i = n * 2 * kPieces / of; i < (n + 1) * 2 * kPieces / of; ++i) {
+                    if (i < kPieces) load_piece(true, v_source, i);
+                    else load_piece(false, k_source, i - kPieces);
+                }
+            });
+            half_step(s1, s0, cur.base + kKeys / 2, cur.blocks >> 2 & 3, other + kHalf, buf + kHalf, [](int, int) {});
         }
 #pragma unroll
         for (int n = 0; n < 2 * kV; ++n) add_value(n);
     }
-    for (; t < last; ++t) advance(t);
+    for (; t < last; ++t) {
+        advance(t);
+        load_all(t);
+    }
+    wait_vmem_below<0>();                         // no load may write LDS after the workgroup has ended
 
     const Partials parts(a, D, splits);
 #pragma unroll
