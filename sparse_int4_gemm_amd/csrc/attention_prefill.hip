@@ -114,9 +114,11 @@ __device__ void plain_row(const AttnArgs& a, const Span& tiles, int first, int l
 }
 
 template <class T, int D, int NW, int QB>
-__global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attention_prefill_kernel(
+__global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2) void attention_prefill_kernel(
     AttnArgs a, int slots, int slot0, int splits, int chunk) {
-    constexpr int kWaveRows = 32 * QB, kRows = kWaveRows * NW, kTileBytes = kKeys * D * 2, kC = D / 8;      // chunks of a row
+    constexpr int kWaveRows = 32 * QB, kRows = kWaveRows * NW, kRowsLog = kRows == 128 ? 7 : 8;
+    static_assert(kRows == 1 << kRowsLog, "rows of a workgroup");
+    constexpr int kTileBytes = kKeys * D * 2, kC = D / 8;      // chunks of a row
     constexpr int kLoads = D / 32;                       // 64-lane loads of a 16-row block
     __shared__ __align__(1024) unsigned char lds[2][2][kTileBytes];             // [buffer][K, V]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -133,27 +135,41 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attentio
     const int slot = slots - 1 - (slot0 + id / splits);
 
     // Sequence b's slots begin at starts[b] * share / kRows + b: at least as
-    // many as its rows fill.  Found as find_seq finds a token's sequence.
-    int lo = 0, n = a.kv.seqs;
-    while (n > 1) {
-        const int step = (n + 63) >> 6, at = lane * step;
-        const int s = at < n ? a.kv.starts[lo + at] : 0;
-        const uint64_t ok = __ballot(at < n && (int64_t)s * share / kRows + lo + at <= slot);
+    // many as its rows fill.  Found as find_seq finds a token's sequence; the
+    // last step has its starts and length in the lanes already.
+    int lo = 0, n = a.kv.seqs, from_row = 0, to_row = 0, len = 0;
+    for (;;) {
+        const int step = (n + 63) >> 6, i = lo + min(lane * step, n - 1);
+        from_row = a.kv.starts[i];
+        to_row = a.kv.starts[i + 1];
+        len = a.kv.lens[i];
+        const uint64_t ok = __ballot(lane * step < n && (((int64_t)from_row * share) >> kRowsLog) + i <= slot);
         if (ok == 0) return;
         const int c = 63 - __builtin_clzll(ok);
         lo += c * step;
         n = min(step, n - c * step);
+        if (n == 1) {
+            from_row = __builtin_amdgcn_readlane(from_row, c);
+            to_row = __builtin_amdgcn_readlane(to_row, c);
+            len = min(max(__builtin_amdgcn_readlane(len, c), 0), kMaxLen);
+            break;
+        }
     }
     const int b = __builtin_amdgcn_readfirstlane(lo);
-    int row_first, count;
-    new_rows(a.kv, b, a.tokens, row_first, count);
-    const int64_t tile = slot - ((int64_t)a.kv.starts[b] * share / kRows + b);
+    const int64_t tile = slot - ((((int64_t)from_row * share) >> kRowsLog) + b);
+    const int row_first = min(max(from_row, 0), a.tokens), count = max(min(to_row, a.tokens) - row_first, 0);
     if (tile < 0 || tile * kRows >= (int64_t)count * share) return;
 
-    const int len = seq_len(a.kv, b), before = len - count;             // position of new token 0
-    const int64_t r0 = tile * kRows;
+    // Row r of the block is token (skip + r) / share past `token0`: 32-bit
+    // divisions, of small numbers by a product with the reciprocal (exact:
+    // (x + 1/2) / share is at least 1 / 2048 away from a whole number).
+    const uint32_t r0 = (uint32_t)(tile * kRows);
     const int rows = (int)min((int64_t)kRows, (int64_t)count * share - r0);
-    const int p_first = before + (int)(r0 / share), p_last = before + (int)((r0 + rows - 1) / share);
+    const int token0 = (int)(r0 / (uint32_t)share), skip = (int)(r0 - (uint32_t)token0 * (uint32_t)share);
+    const float per_share = 1.0f / (float)share;
+    auto token_of = [&](int r) { return (int)(((float)(skip + r) + 0.5f) * per_share); };
+    const int before = len - count;                                     // position of new token 0
+    const int p_first = before + token0, p_last = before + token0 + token_of(rows - 1);
     Span span = key_span(a, p_last);
     span.start = a.window ? max(0, p_first - a.window + 1) : 0;
     const int keys = min(len, (int)min((int64_t)a.kv.width << a.kv.page_shift, (int64_t)kMaxLen));
@@ -175,25 +191,17 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attentio
     for (int q = 0; q < QB; ++q) {
         const int r = kWaveRows * wave + 32 * q + col;
         live[q] = r < rows;
-        const int64_t at = r0 + (live[q] ? r : 0);
-        token[q] = row_first + (int)(at / share);
-        head[q] = kvh * share + (int)(at % share);
-        mine[q] = key_span(a, live[q] ? before + (token[q] - row_first) : -1);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            qf[q][i] = u4{0, 0, 0, 0};
-            if (live[q] && a.scale != 0.0f) {
-                qf[q][i] = *reinterpret_cast<const u4*>(a.q + token[q] * a.sq + (int64_t)head[q] * D + 16 * i + 8 * half);
-                qf[q][i] ^= flip;
-            }
-        }
+        const int past = token_of(live[q] ? r : 0);
+        token[q] = row_first + token0 + past;
+        head[q] = kvh * share + skip + (live[q] ? r : 0) - past * share;
+        mine[q] = key_span(a, live[q] ? p_first + past : -1);
     }
     // The wave's own tiles [w_begin, w_end): its rows see none of the others.
     // Every row sees all of a 32-key half that begins in [all_from, all_to],
     // and of one that holds sinks only, up to all_to.
     const int w_rows = min(kWaveRows, rows - kWaveRows * wave);
-    const int w_first = before + (int)((r0 + kWaveRows * wave) / share);
-    const int w_last = w_rows > 0 ? before + (int)((r0 + kWaveRows * wave + w_rows - 1) / share) : -1;
+    const int w_first = p_first + __builtin_amdgcn_readfirstlane(token_of(kWaveRows * wave));
+    const int w_last = w_rows > 0 ? p_first + __builtin_amdgcn_readfirstlane(token_of(kWaveRows * wave + w_rows - 1)) : -1;
     const int sinks = span.sinks, sink_tiles = span.sink_tiles(kKeys), window_tile = span.start / kKeys - sink_tiles;
     const int w_end = w_last < 0 ? first : max(first, min(last, w_last / kKeys - window_tile + 1));
     const int w_begin = a.window && sinks == 0
@@ -300,6 +308,19 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attentio
     auto k_read = [&](uint32_t at, int i) { return D == 96 ? (at ^ (32u * (i & 1))) + 64 * (i >> 1) : at ^ (32u * i); };
     auto v_read = [&](uint32_t at, int i) { return D == 96 ? at + 64 * i : at ^ (64u * i); };
 
+    // The queries are asked for after the first tile's pages, which are needed first.
+    if (first < last) look_up(first);
+#pragma unroll
+    for (int q = 0; q < QB; ++q)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            qf[q][i] = u4{0, 0, 0, 0};
+            if (live[q] && a.scale != 0.0f) {
+                qf[q][i] = *reinterpret_cast<const u4*>(a.q + token[q] * a.sq + (int64_t)head[q] * D + 16 * i + 8 * half);
+                qf[q][i] ^= flip;
+            }
+        }
+
     float m[QB], l[QB];
     f16v o[QB][D / 32];
     // Software pipeline over 32-key halves j of the tiles.  While the softmax
@@ -375,7 +396,7 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attentio
 #pragma unroll
             for (int q = 0; q < QB; ++q)
 #pragma unroll
-                for (int e = n * 16 / kFirst; e < (n + 1) * 16 / kFirst; ++e) top[q] = e == 0 ? cur[q][0] : fmaxf(top[q], cur[q][e]);
+                for (int e = n * 16 / kFirst; e < (n + 1) * 16 / kFirst; ++e) top[q] = e == 0 ? cur[q][0] : __builtin_elementwise_maximum(top[q], cur[q][e]);
         }
         __builtin_amdgcn_sched_barrier(0);
         add_value(kFirst);
@@ -457,7 +478,6 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attentio
     // the loads of K of tile t + 2 and V of tile t + 1 may begin.
     Place cur, next, after;                       // of tiles t, t + 1 and t + 2
     if (first < last) {
-        look_up(first);
         cur = next = place(first);
         after = place(min(first + 1, last - 1));
         load(false, 0, next);
@@ -537,10 +557,10 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : 2) void attentio
             for (int e = 0; e < 16; ++e) probe = fmaf(o[q][i][e], 0.0f, probe);
         if (__any(live[q] && !(probe == 0.0f))) {
             for (int i = 0; i < min(32, w_rows - 32 * q); ++i) {
-                const int64_t rr = r0 + kWaveRows * wave + 32 * q + i;
-                const int tk = row_first + (int)(rr / share), hd = kvh * share + (int)(rr % share);
+                const int r = kWaveRows * wave + 32 * q + i, past = token_of(r);
+                const int tk = row_first + token0 + past, hd = kvh * share + skip + r - past * share;
                 float x[4], mx, lx;
-                plain_row<D>(a, span, first, last, key_span(a, before + tk - row_first), table, kvh,
+                plain_row<D>(a, span, first, last, key_span(a, p_first + past), table, kvh,
                              a.q + tk * a.sq + (int64_t)hd * D, x, mx, lx);
                 const int64_t row = (int64_t)tk * a.q_heads + hd;
                 for (int k = 0; k < 4; ++k) {
