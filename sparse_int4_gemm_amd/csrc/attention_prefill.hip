@@ -29,10 +29,6 @@ namespace {
 
 constexpr int kKeys = 64;            // keys of a tile
 constexpr float kLazy = 8.0f;        // weights stay at or below 2^kLazy
-#ifndef PNW
-#define PNW 4
-#define PQB 1
-#endif
 // Splits: kSplitTarget workgroups in all, each with at least kMinTiles tiles.
 constexpr int kSplitTarget = 256, kMinTiles = 4;
 
@@ -113,15 +109,17 @@ __device__ void plain_row(const AttnArgs& a, const Span& tiles, int first, int l
     }
 }
 
-template <class T, int D, int NW, int QB>
-__global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2) void attention_prefill_kernel(
+template <class T, int D, int NW, int QB, int KG>
+__global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && KG == 1 ? 3 : 2) void attention_prefill_kernel(
     AttnArgs a, int slots, int slot0, int splits, int chunk) {
     constexpr int kWaveRows = 32 * QB, kRows = kWaveRows * NW, kRowsLog = kRows == 128 ? 7 : 8;
     static_assert(kRows == 1 << kRowsLog, "rows of a workgroup");
     constexpr int kTileBytes = kKeys * D * 2, kC = D / 8;      // chunks of a row
     constexpr int kLoads = D / 32;                       // 64-lane loads of a 16-row block
-    __shared__ __align__(1024) unsigned char lds[2][2][kTileBytes];             // [buffer][K, V]
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __shared__ __align__(1024) unsigned char lds[KG][2][2][kTileBytes];         // [group][buffer][K, V]
+    // Waves in KG groups: each group has all the rows, and every KG-th tile.
+    const int lane = threadIdx.x & 63, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = any_wave / NW, wave = any_wave % NW;
     const int half = lane >> 5, col = lane & 31;
 
     // Head fastest (a workgroup's XCD is its index mod 8: with 8 or more key
@@ -177,7 +175,11 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2)
 
     const int tiles = span.tiles(kKeys);
     const int per = max(chunk, (tiles + splits - 1) / splits);
-    const int first = min(tiles, split * per), last = min(tiles, first + per);
+    // Tiles [begin, end) of the list are this workgroup's; its group's t-th is begin + group + KG t.
+    const int begin = min(tiles, split * per), end = min(tiles, begin + per);
+    auto tiles_before = [&](int i) { return max(0, (i - begin - group + KG - 1) / KG); };      // of the group's, below i
+    constexpr int first = 0;
+    const int last = tiles_before(end), steps = (end - begin + KG - 1) / KG;
 
     // This lane's queries, one of each of the wave's QB blocks of 32 rows.
     bool live[QB];
@@ -203,9 +205,9 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2)
     const int w_first = p_first + __builtin_amdgcn_readfirstlane(token_of(kWaveRows * wave));
     const int w_last = w_rows > 0 ? p_first + __builtin_amdgcn_readfirstlane(token_of(kWaveRows * wave + w_rows - 1)) : -1;
     const int sinks = span.sinks, sink_tiles = span.sink_tiles(kKeys), window_tile = span.start / kKeys - sink_tiles;
-    const int w_end = w_last < 0 ? first : max(first, min(last, w_last / kKeys - window_tile + 1));
+    const int w_end = w_last < 0 ? 0 : min(last, tiles_before(w_last / kKeys - window_tile + 1));
     const int w_begin = a.window && sinks == 0
-                            ? max(first, min(w_end, max(0, w_first - a.window + 1) / kKeys - window_tile)) : first;
+                            ? min(w_end, tiles_before(max(0, w_first - a.window + 1) / kKeys - window_tile)) : 0;
     const int all_to = w_rows == kWaveRows ? min(w_first + 1, keys) - kKeys / 2 : -1;
     const int all_from = a.window ? w_last - a.window + 1 : 0;
 
@@ -217,9 +219,13 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2)
     constexpr int kOwn = 4 / NW;                  // blocks of a wave
     const int row_mask = (1 << a.kv.page_shift) - 1;
     int at_lo[kOwn] = {}, at_hi[kOwn] = {}, blocks = 0, from = first;
+    auto base_of = [&](int t) {
+        t = begin + group + KG * t;
+        return (t < sink_tiles ? t : t + window_tile) * kKeys;
+    };
     auto look_up = [&](int t0) {
         from = t0;
-        const int t = min(t0 + lane, last - 1), base = (t < sink_tiles ? t : t + window_tile) * kKeys;
+        const int base = base_of(min(t0 + lane, last - 1));
         int page[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -244,7 +250,7 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2)
     struct Place { int base, blocks, lo[kOwn], hi[kOwn]; };
     auto place = [&](int t) {
         Place x;
-        x.base = (t < sink_tiles ? t : t + window_tile) * kKeys;
+        x.base = base_of(t);
         x.blocks = __builtin_amdgcn_readlane(blocks, t - from);
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
@@ -257,7 +263,7 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2)
     // Load j's rows differ from load 0's in bits that the permutation moves
     // through unchanged, so one register gives all (not at D = 96, where a load
     // ends inside a row).
-    const uint32_t lds0 = lds_u32(&lds[0][0][0]);
+    const uint32_t lds0 = lds_u32(&lds[group][0][0][0]);
     auto source = [&](bool is_v, int j) {
         const int c = 64 * j + lane, r = c / kC, at = c - r * kC;
         return (uint32_t)(r * (D * 2) + (is_v ? v_place<D>(r, at) : k_place<D>(r, at)) * 16);
@@ -422,6 +428,26 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2)
 #pragma unroll
             for (int e = 0; e < 16; ++e) nxt[q][e] = 0.0f;
         constexpr int kRest = 2 * kV - kFirst - 1 + kK;
+        // Weight pair p of a lane's 8 passes through three chunks: its
+        // exponents, the exponentials, their sum and rounding, so that none waits
+        // for the one before.
+        float ex[QB][16];
+        auto exponents = [&](int n) {
+#pragma unroll
+            for (int e = n * 8 / kRest * 2; e < (n + 1) * 8 / kRest * 2; ++e)
+#pragma unroll
+                for (int q = 0; q < QB; ++q) ex[q][e] = fmaf(cur[q][e], scale, -ms[q]);
+        };
+        auto weights = [&](int n) {
+#pragma unroll
+            for (int p = n * 8 / kRest; p < (n + 1) * 8 / kRest; ++p)
+#pragma unroll
+                for (int q = 0; q < QB; ++q) {
+                    sum[q] += ex[q][2 * p] + ex[q][2 * p + 1];
+                    wn[q][p >> 2][p & 3] = T::pack(ex[q][2 * p], ex[q][2 * p + 1]);
+                }
+        };
+        exponents(0);
 #pragma unroll
         for (int n = 0; n < kRest; ++n) {
             const int k = n - (kRest - kK);                       // operand of K from 0 on
@@ -443,16 +469,14 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2)
                 kf[k] = lds_ld<u4>(k_read(k_at + k_next, k));
             }
 #pragma unroll
-            for (int p = n * 8 / kRest; p < (n + 1) * 8 / kRest; ++p)
+            for (int e = n * 8 / kRest * 2; e < (n + 1) * 8 / kRest * 2; ++e)
 #pragma unroll
-                for (int q = 0; q < QB; ++q) {
-                    const float x = exp2_fast(fmaf(cur[q][2 * p], scale, -ms[q]));
-                    const float y = exp2_fast(fmaf(cur[q][2 * p + 1], scale, -ms[q]));
-                    sum[q] += x + y;
-                    wn[q][p >> 2][p & 3] = T::pack(x, y);
-                }
+                for (int q = 0; q < QB; ++q) ex[q][e] = exp2_fast(ex[q][e]);
+            if (n + 1 < kRest) exponents(n + 1);
+            if (n > 0) weights(n - 1);
         }
         __builtin_amdgcn_sched_barrier(0);
+        weights(kRest - 1);
 #pragma unroll
         for (int q = 0; q < QB; ++q) {
             w[q][0] = wn[q][0];
@@ -505,7 +529,8 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2)
         if (t >= first && t + 1 < last) load(true, (t + 1 - first) & 1, next);
     };
     constexpr uint32_t kHalf = kKeys / 2 * D * 2;
-    int t = first < last ? first - 1 : last;
+    // (A group without tiles, or with one fewer, only takes part in the barriers.)
+    int t = begin < end ? first - 1 : steps;
     for (; t < w_begin - 1; ++t) {
         advance(t);
         load_all(t);
@@ -538,11 +563,37 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2)
 #pragma unroll
         for (int n = 0; n < 2 * kV; ++n) add_value(n);
     }
-    for (; t < last; ++t) {
+    for (; t < steps; ++t) {
         advance(t);
         load_all(t);
     }
-    wait_vmem_below<0>();                         // no load may write LDS after the workgroup has ended
+    wait_vmem_below<0>();                         // no load may write LDS from here on
+
+    if constexpr (KG == 2) {
+        // The second group leaves its results in LDS, the first joins them.  One
+        // group at most has seen nothing (m = -inf), or both.
+        constexpr int kRegs = QB * (D / 32) * 16;
+        static_assert(NW * kRegs * 64 * 4 <= (int)sizeof lds && QB == 1, "room for the second group's results");
+        float* const at = reinterpret_cast<float*>(lds) + wave * kRegs * 64 + lane;
+        __syncthreads();
+        if (group == 1) {
+#pragma unroll
+            for (int i = 0; i < kRegs; ++i) at[i * 64] = o[0][i / 16][i % 16];
+        }
+        __shared__ float stats[NW][2][64];
+        if (group == 1) {
+            stats[wave][0][lane] = m[0];
+            stats[wave][1][lane] = l[0];
+        }
+        __syncthreads();
+        if (group == 1) return;
+        const float m1 = stats[wave][0][lane], l1 = stats[wave][1][lane], mn = fmaxf(m[0], m1);
+        const float f0 = mn == -INFINITY ? 1.0f : exp2_fast(m[0] - mn), f1 = mn == -INFINITY ? 0.0f : exp2_fast(m1 - mn);
+        m[0] = mn;
+        l[0] = l[0] * f0 + l1 * f1;
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i) o[0][i / 16][i % 16] = o[0][i / 16][i % 16] * f0 + at[i * 64] * f1;
+    }
 
     const Partials parts(a, D, splits);
 #pragma unroll
@@ -560,7 +611,7 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2)
                 const int r = kWaveRows * wave + 32 * q + i, past = token_of(r);
                 const int tk = row_first + token0 + past, hd = kvh * share + skip + r - past * share;
                 float x[4], mx, lx;
-                plain_row<D>(a, span, first, last, key_span(a, p_first + past), table, kvh,
+                plain_row<D>(a, span, begin, end, key_span(a, p_first + past), table, kvh,
                              a.q + tk * a.sq + (int64_t)hd * D, x, mx, lx);
                 const int64_t row = (int64_t)tk * a.q_heads + hd;
                 for (int k = 0; k < 4; ++k) {
@@ -593,11 +644,15 @@ __global__ __launch_bounds__(64 * NW, QB == 2 || D == 256 ? 1 : D == 64 ? 3 : 2)
     }
 }
 
-template <class T, int D, int NW, int QB>
+// Slots of `rows` query rows, enough for every sequence's.
+int64_t slots_of(const AttnArgs& a, int rows) {
+    return (int64_t)a.tokens * (a.q_heads / a.kv_heads) / rows + a.kv.seqs;
+}
+
+template <class T, int D, int NW, int QB, int KG>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     constexpr int kRows = 32 * QB * NW;
-    const int share = a.q_heads / a.kv_heads;
-    const int64_t slots = (int64_t)a.tokens * share / kRows + a.kv.seqs;
+    const int64_t slots = slots_of(a, kRows);
     int64_t most = a.max_len;
     if (a.window && (int64_t)a.window + a.sinks + kRows < most) most = (int64_t)a.window + a.sinks + kRows;
     const int64_t tiles = (most + kKeys - 1) / kKeys, units = slots * a.kv_heads;
@@ -605,10 +660,10 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     const int64_t splits = max((int64_t)1, min(want, kAttnSplitRows / ((int64_t)a.tokens * a.q_heads)));
     const int chunk = (int)max((int64_t)1, (tiles + splits - 1) / splits);
     // A grid holds fewer than 2^32 threads; slots past it go into further launches.
-    const int64_t per_slot = a.kv_heads * splits, at_once = ((int64_t(1) << 32) / (64 * NW) - 1) / per_slot;
+    const int64_t per_slot = a.kv_heads * splits, at_once = ((int64_t(1) << 32) / (64 * NW * KG) - 1) / per_slot;
     for (int64_t s = 0; s < slots; s += at_once) {
         const int64_t n = min(at_once, slots - s);
-        hipLaunchKernelGGL((attention_prefill_kernel<T, D, NW, QB>), dim3((unsigned)(n * per_slot)), dim3(64 * NW), 0, stream,
+        hipLaunchKernelGGL((attention_prefill_kernel<T, D, NW, QB, KG>), dim3((unsigned)(n * per_slot)), dim3(64 * NW * KG), 0, stream,
                            a, (int)slots, (int)s, (int)splits, chunk);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -616,13 +671,23 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     return splits == 1 ? hipSuccess : launch_attention_join(a, (int)splits, stream);
 }
 
+// Two groups of waves on every other tile where one round of workgroups (one
+// a CU) holds all rows: half the tiles one after another (61 tokens on 24576:
+// @KG2@).  With more, two workgroups of one group share a CU and
+// hide each other's beginnings and ends (2048 tokens: @KG1@).
+template <class T, int D>
+hipError_t launch_groups(const AttnArgs& a, hipStream_t stream) {
+    if (slots_of(a, 128) * a.kv_heads <= kSplitTarget) return launch<T, D, 4, 1, 2>(a, stream);
+    return launch<T, D, 4, 1, 1>(a, stream);
+}
+
 template <class T>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
     switch (a.head_dim) {
-        case 64: return launch<T, 64, PNW, PQB>(a, stream);
-        case 96: return launch<T, 96, PNW, PQB>(a, stream);
-        case 128: return launch<T, 128, PNW, PQB>(a, stream);
-        default: return launch<T, 256, 4, 1>(a, stream);
+        case 64: return launch_groups<T, 64>(a, stream);
+        case 96: return launch_groups<T, 96>(a, stream);
+        case 128: return launch_groups<T, 128>(a, stream);
+        default: return launch<T, 256, 4, 1, 1>(a, stream);           // two groups' tiles do not fit LDS
     }
 }
 
