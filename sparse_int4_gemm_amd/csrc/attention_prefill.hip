@@ -321,10 +321,8 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             qf[q][i] = u4{0, 0, 0, 0};
-            if (live[q] && a.scale != 0.0f) {
+            if (live[q] && a.scale != 0.0f)
                 qf[q][i] = *reinterpret_cast<const u4*>(a.q + token[q] * a.sq + (int64_t)head[q] * D + 16 * i + 8 * half);
-                qf[q][i] ^= flip;
-            }
         }
 
     float m[QB], l[QB];
@@ -539,6 +537,10 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
         advance(t);
         load_all(t);
         const uint32_t k_buf = ((t + 1 - first) & 1) * 2 * kTileBytes;
+#pragma unroll
+        for (int q = 0; q < QB; ++q)
+#pragma unroll
+            for (int i = 0; i < kK; ++i) qf[q][i] ^= flip;        // (their first use: not waited for before the tiles' loads)
         read_k(k_buf);
         score(s0);
         read_k(k_buf + kHalf);
