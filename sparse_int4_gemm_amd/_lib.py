@@ -296,64 +296,72 @@ def slim_linear_hybrid(X, values, meta, scales, dvalues, dense, Lt, Rt, Y, works
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _rows(name, t, heads, dim, dtype, device):
     """(pointer, row stride) of a [tokens, heads, dim] tensor whose rows are
     dense; the rows themselves may lie apart (a slice of a joint array)."""
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     sr, sh, sd = t.stride()
-    if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
+    if sd != 1 or (sh != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     return t.data_ptr(), sr if t.shape[0] > 1 else heads * dim
 
 
 def _ints(name, t, device, dims):
-    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous() or t.device != device:
+    if t.dtype is not torch.int32 or t.dim() != dims or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dims}-dimensional int32 tensor on {device}")
     return t.data_ptr()
 
 
 def _pools(kpool, vpool, dims):
-    if kpool.device.type != "cuda":
+    """Device and shape of a pair of pools."""
+    device, shape = kpool.device, kpool.shape
+    if device.type != "cuda":
         raise ValueError("tensors must live on the GPU (a ROCm 'cuda' device)")
     if kpool.dtype not in _DTYPES:
         raise TypeError("the pools must be float16 or bfloat16")
-    if kpool.dim() != dims or kpool.shape != vpool.shape or kpool.dtype != vpool.dtype or kpool.device != vpool.device:
+    if len(shape) != dims or shape != vpool.shape or kpool.dtype is not vpool.dtype or device != vpool.device:
         raise ValueError(f"the pools must be two {dims}-dimensional tensors of one shape, type and device")
     if not (kpool.is_contiguous() and vpool.is_contiguous()):
         raise ValueError("the pools must be contiguous")
-    return kpool.device
+    return device, shape
 
 
 def _stream_on(stream, device):
     """The HIP stream of a call on `device`, and a check that launches go there."""
     if device.index != torch.cuda.current_device():
         raise ValueError(f"the current device must be the tensors' {device}")
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # (The public way to the current stream's handle costs as much as the launch.)
+    return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
 
 
 def _batch(table, lens, starts, tokens, device):
-    seqs = lens.shape[0] if lens.dim() == 1 else -1
     p_table, p_lens = _ints("table", table, device, 2), _ints("lens", lens, device, 1)
+    seqs = lens.shape[0]
     if table.shape[0] != seqs:
         raise ValueError(f"table has {table.shape[0]} rows for {seqs} sequences")
     if starts is None:
         if tokens != seqs:
             raise ValueError(f"{tokens} new tokens for {seqs} sequences without starts")
         return p_table, p_lens, None, seqs
-    if starts.dim() == 1 and starts.shape[0] != seqs + 1:
+    p_starts = _ints("starts", starts, device, 1)
+    if starts.shape[0] != seqs + 1:
         raise ValueError(f"starts must hold {seqs + 1} values, got {starts.shape[0]}")
-    return p_table, p_lens, _ints("starts", starts, device, 1), seqs
+    return p_table, p_lens, p_starts, seqs
 
 
 def slim_kv_append(K, V, kpool, vpool, table, lens, starts=None, stream=None) -> None:
     """K, V [tokens, kv_heads, head_dim] to the pages of their positions; pools [pages, kv_heads, page_size, head_dim]."""
-    dev = _pools(kpool, vpool, 4)
-    pages, heads, page, dim = kpool.shape
+    dev, (pages, heads, page, dim) = _pools(kpool, vpool, 4)
     pk, sk = _rows("K", K, heads, dim, kpool.dtype, dev)
     pv, sv = _rows("V", V, heads, dim, kpool.dtype, dev)
     tokens = K.shape[0]
@@ -366,11 +374,11 @@ def slim_kv_append(K, V, kpool, vpool, table, lens, starts=None, stream=None) ->
 
 def slim_kv_copy_pages(kpool, vpool, src, dst, stream=None) -> None:
     """Pages src[i] to dst[i] of every layer; pools [layers, pages, ...] or one layer's [pages, kv_heads, page_size, head_dim]."""
-    dev = _pools(kpool, vpool, kpool.dim())
-    if kpool.dim() not in (4, 5):
+    dev, shape = _pools(kpool, vpool, kpool.dim())
+    if len(shape) not in (4, 5):
         raise ValueError("the pools must be [layers, pages, kv_heads, page_size, head_dim] or one layer of it")
-    layers = kpool.shape[0] if kpool.dim() == 5 else 1
-    pages, heads, page, dim = kpool.shape[-4:]
+    layers = shape[0] if len(shape) == 5 else 1
+    pages, heads, page, dim = shape[-4:]
     ps, pd = _ints("src", src, dev, 1), _ints("dst", dst, dev, 1)
     if src.shape != dst.shape:
         raise ValueError(f"{src.shape[0]} sources and {dst.shape[0]} destinations")
@@ -384,8 +392,7 @@ def slim_attention_workspace_bytes(tokens: int, seqs: int, q_heads: int, kv_head
 
 
 def _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace):
-    dev = _pools(kpool, vpool, 4)
-    pages, kv_heads, page, dim = kpool.shape
+    dev, (pages, kv_heads, page, dim) = _pools(kpool, vpool, 4)
     if Q.dim() != 3:
         raise ValueError(f"Q must be [tokens, q_heads, {dim}], got {tuple(Q.shape)}")
     tokens, q_heads = Q.shape[0], Q.shape[1]

@@ -231,8 +231,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
     }
 }
 
-// Splits: kSplitTarget workgroups in all, each with at least kMinTiles tiles.
-constexpr int kSplitTarget = 2048, kMinTiles = 16;
+// Splits: two workgroups a CU, each with at least kMinTiles tiles.  More of
+// them cost more in partial results than they gain (131071 keys of 8 key heads: 512
+// workgroups 100 us, 1024 103, 2048 111; 64 sequences of up to 900 at head size
+// 256: 61 us unsplit, 87 in two), fewer tiles too (4 sequences of up to 8000, 8 key heads:
+// 16 tiles 20.7 us, 8 tiles 24.1).
+constexpr int kSplitTarget = 512, kMinTiles = 16;
 
 template <class T, int D>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {

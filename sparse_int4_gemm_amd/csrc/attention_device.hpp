@@ -69,8 +69,7 @@ __device__ __forceinline__ void load_words(uint32_t (&to)[N], const uint16_t* p)
 // The keys that positions p0 .. p1 of one sequence see, as a run of tiles:
 // those that hold sinks, then those from the first window's start on.
 struct Span {
-    int p;                // (last) position; -1 or less: nothing is seen
-    int end;              // keys below min(p + 1, capacity of the table)
+    int end;              // keys below min(p + 1, capacity of the table); 0 or less: nothing is seen
     int start;            // first key of the (first position's) window
     int sinks;
 
@@ -105,7 +104,6 @@ __device__ __forceinline__ int page_of(const AttnArgs& a, int b, int key, int ke
 __device__ __forceinline__ Span key_span(const AttnArgs& a, int p) {
     const int64_t capacity = (int64_t)a.kv.width << a.kv.page_shift;      // at most 2^30
     Span s;
-    s.p = p;
     s.end = (int)min((int64_t)p + 1, capacity);
     s.start = a.window ? max(0, p - a.window + 1) : 0;
     s.sinks = a.window ? a.sinks : 0;

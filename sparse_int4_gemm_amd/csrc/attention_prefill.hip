@@ -29,6 +29,9 @@ namespace {
 
 constexpr int kKeys = 64;            // keys of a tile
 constexpr float kLazy = 8.0f;        // weights stay at or below 2^kLazy
+// Query rows of a workgroup: 32 for each of its row waves.
+constexpr int kRowWaves = 4, kRowsLog = 7, kRows = 1 << kRowsLog;
+
 // Splits: kSplitTarget workgroups in all, each with at least kMinTiles tiles.
 constexpr int kSplitTarget = 256, kMinTiles = 4;
 
@@ -109,17 +112,15 @@ __device__ void plain_row(const AttnArgs& a, const Span& tiles, int first, int l
     }
 }
 
-template <class T, int D, int NW, int QB, int KG>
-__global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && KG == 1 ? 3 : 2) void attention_prefill_kernel(
+template <class T, int D, int KG>
+__global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG == 1 ? 3 : 2) void attention_prefill_kernel(
     AttnArgs a, int slots, int slot0, int splits, int chunk) {
-    constexpr int kWaveRows = 32 * QB, kRows = kWaveRows * NW, kRowsLog = kRows == 128 ? 7 : 8;
-    static_assert(kRows == 1 << kRowsLog, "rows of a workgroup");
     constexpr int kTileBytes = kKeys * D * 2, kC = D / 8;      // chunks of a row
     constexpr int kLoads = D / 32;                       // 64-lane loads of a 16-row block
     __shared__ __align__(1024) unsigned char lds[KG][2][2][kTileBytes];         // [group][buffer][K, V]
     // Waves in KG groups: each group has all the rows, and every KG-th tile.
     const int lane = threadIdx.x & 63, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int group = any_wave / NW, wave = any_wave % NW;
+    const int group = any_wave / kRowWaves, wave = any_wave % kRowWaves;
     const int half = lane >> 5, col = lane & 31;
 
     // Head fastest (a workgroup's XCD is its index mod 8: with 8 or more key
@@ -181,44 +182,34 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
     constexpr int first = 0;
     const int last = tiles_before(end), steps = (end - begin + KG - 1) / KG;
 
-    // This lane's queries, one of each of the wave's QB blocks of 32 rows.
-    bool live[QB];
-    int token[QB], head[QB];
-    Span mine[QB];
-    u4 qf[QB][D / 16];
+    // This lane's query.
+    const bool live = 32 * wave + col < rows;
+    const int row_in = live ? 32 * wave + col : 0, past = token_of(row_in);
+    const int token = row_first + token0 + past, head = kvh * share + skip + row_in - past * share;
+    const Span mine = key_span(a, live ? p_first + past : -1);
     // Scores are compared before they are scaled, so the scale's sign goes into the queries (exact).
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     const float scale = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f;
-#pragma unroll
-    for (int q = 0; q < QB; ++q) {
-        const int r = kWaveRows * wave + 32 * q + col;
-        live[q] = r < rows;
-        const int past = token_of(live[q] ? r : 0);
-        token[q] = row_first + token0 + past;
-        head[q] = kvh * share + skip + (live[q] ? r : 0) - past * share;
-        mine[q] = key_span(a, live[q] ? p_first + past : -1);
-    }
     // The wave's own tiles [w_begin, w_end): its rows see none of the others.
     // Every row sees all of a 32-key half that begins in [all_from, all_to],
     // and of one that holds sinks only, up to all_to.
-    const int w_rows = min(kWaveRows, rows - kWaveRows * wave);
-    const int w_first = p_first + __builtin_amdgcn_readfirstlane(token_of(kWaveRows * wave));
-    const int w_last = w_rows > 0 ? p_first + __builtin_amdgcn_readfirstlane(token_of(kWaveRows * wave + w_rows - 1)) : -1;
+    const int w_rows = min(32, rows - 32 * wave);
+    const int w_first = p_first + __builtin_amdgcn_readfirstlane(token_of(32 * wave));
+    const int w_last = w_rows > 0 ? p_first + __builtin_amdgcn_readfirstlane(token_of(32 * wave + w_rows - 1)) : -1;
     const int sinks = span.sinks, sink_tiles = span.sink_tiles(kKeys), window_tile = span.start / kKeys - sink_tiles;
     const int w_end = w_last < 0 ? 0 : min(last, tiles_before(w_last / kKeys - window_tile + 1));
     const int w_begin = a.window && sinks == 0
                             ? min(w_end, tiles_before(max(0, w_first - a.window + 1) / kKeys - window_tile)) : 0;
-    const int all_to = w_rows == kWaveRows ? min(w_first + 1, keys) - kKeys / 2 : -1;
+    const int all_to = w_rows == 32 ? min(w_first + 1, keys) - kKeys / 2 : -1;
     const int all_from = a.window ? w_last - a.window + 1 : 0;
 
     // Bookkeeping of a tile: its first key, which of its four 16-key blocks have
     // a page, and of the block that this wave loads its place in the pool
-    // and its rows (those before the sequence's end).  A wave loads the K and V
-    // rows of the blocks wave, wave + NW, ...  Lane j holds it for tile from + j: a table entry looked up for
+    // and its rows (those before the sequence's end).  Wave w of a group loads
+    // block w of K and of V.  Lane j holds it for tile from + j: a table entry looked up for
     // each tile would be waited for each time.
-    constexpr int kOwn = 4 / NW;                  // blocks of a wave
     const int row_mask = (1 << a.kv.page_shift) - 1;
-    int at_lo[kOwn] = {}, at_hi[kOwn] = {}, blocks = 0, from = first;
+    int at_lo = 0, at_hi = 0, blocks = 0, from = first;
     auto base_of = [&](int t) {
         t = begin + group + KG * t;
         return (t < sink_tiles ? t : t + window_tile) * kKeys;
@@ -237,26 +228,23 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
         for (int i = 0; i < 4; ++i) {
             const bool is = page[i] >= 0 && page[i] < a.kv.pages;
             blocks |= is ? 1 << i : 0;
-            if (i % NW == wave) {
+            if (i == wave) {
                 const int key = base + 16 * i;
                 const int64_t at = ((((int64_t)(is ? page[i] : 0) * a.kv_heads + kvh) << a.kv.page_shift) +
                                     (key & row_mask)) * (D * 2);
-                at_lo[i / NW] = (int)at;
-                at_hi[i / NW] = (int)(at >> 32);
-                blocks |= is ? max(0, min(16, keys - key)) << (4 + 8 * (i / NW)) : 0;
+                at_lo = (int)at;
+                at_hi = (int)(at >> 32);
+                blocks |= is ? max(0, min(16, keys - key)) << 4 : 0;
             }
         }
     };
-    struct Place { int base, blocks, lo[kOwn], hi[kOwn]; };
+    struct Place { int base, blocks, lo, hi; };
     auto place = [&](int t) {
         Place x;
         x.base = base_of(t);
         x.blocks = __builtin_amdgcn_readlane(blocks, t - from);
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            x.lo[i] = __builtin_amdgcn_readlane(at_lo[i], t - from);
-            x.hi[i] = __builtin_amdgcn_readlane(at_hi[i], t - from);
-        }
+        x.lo = __builtin_amdgcn_readlane(at_lo, t - from);
+        x.hi = __builtin_amdgcn_readlane(at_hi, t - from);
         return x;
     };
     // Of a 16-row block's 16-byte chunks, load j takes 64 j + lane in LDS order.
@@ -281,27 +269,23 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
         return is_v ? (v_from[0] ^ (uint32_t)(v_place<D>(r, 0) * 16)) + 1024 * j
                     : (k_from[0] ^ (uint32_t)(k_place<D>(r, 0) * 16)) + 1024 * j;
     };
-    // The wave's loads of a tile of K or V, one by one: n of kOwn * kLoads.
-    struct Source { u4 rsrc[kOwn]; uint32_t to; };
+    // The wave's loads of a tile of K or V, kLoads of them, one by one.
+    struct Source { u4 rsrc; uint32_t to; };
     auto source_of = [&](bool is_v, int buf, const Place& x, bool any) {
         const unsigned char* pool = reinterpret_cast<const unsigned char*>(is_v ? a.kv.v : a.kv.k);
         Source s;
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-            s.rsrc[i] = rsrc_words(pool + (int64_t)((uint64_t)(uint32_t)x.lo[i] | (uint64_t)(uint32_t)x.hi[i] << 32),
-                                   any ? (x.blocks >> (4 + 8 * i) & 31) * (D * 2) : 0);
+        s.rsrc = rsrc_words(pool + (int64_t)((uint64_t)(uint32_t)x.lo | (uint64_t)(uint32_t)x.hi << 32),
+                            any ? (x.blocks >> 4) * (D * 2) : 0);
         s.to = lds0 + (2 * buf + is_v) * kTileBytes + wave * 16 * (D * 2);
         return s;
     };
-    constexpr int kPieces = kOwn * kLoads;
-    auto load_piece = [&](bool is_v, const Source& s, int n) {
-        const int i = n / kLoads, j = n % kLoads;
-        lds_load16_at(s.rsrc[i], s.to + NW * i * 16 * (D * 2) + 1024 * j, from_of(is_v, j), 0);
+    auto load_piece = [&](bool is_v, const Source& s, int j) {
+        lds_load16_at(s.rsrc, s.to + 1024 * j, from_of(is_v, j), 0);
     };
     auto load = [&](bool is_v, int buf, const Place& x) {
         const Source s = source_of(is_v, buf, x, true);
 #pragma unroll
-        for (int n = 0; n < kPieces; ++n) load_piece(is_v, s, n);
+        for (int n = 0; n < kLoads; ++n) load_piece(is_v, s, n);
     };
 
     // Where this lane reads a tile: K row col, chunk 2 i + half; V rows
@@ -316,134 +300,96 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
 
     // The queries are asked for after the first tile's pages, which are needed first.
     if (first < last) look_up(first);
+    u4 qf[D / 16];
 #pragma unroll
-    for (int q = 0; q < QB; ++q)
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            qf[q][i] = u4{0, 0, 0, 0};
-            if (live[q] && a.scale != 0.0f)
-                qf[q][i] = *reinterpret_cast<const u4*>(a.q + token[q] * a.sq + (int64_t)head[q] * D + 16 * i + 8 * half);
-        }
+    for (int i = 0; i < D / 16; ++i) {
+        qf[i] = u4{0, 0, 0, 0};
+        if (live && a.scale != 0.0f)
+            qf[i] = *reinterpret_cast<const u4*>(a.q + token * a.sq + (int64_t)head * D + 16 * i + 8 * half);
+    }
 
-    float m[QB], l[QB];
-    f16v o[QB][D / 32];
+    float m = -INFINITY, l = 0.0f;
+    f16v o[D / 32];
     // Software pipeline over 32-key halves j of the tiles.  While the softmax
     // of half j runs on the vector unit, the matrix unit has the scores of half
     // j + 1 and the values of half j - 1 to work on, whose operands were read
     // from LDS during half j - 1; so K is needed a tile ahead of V.
-    f16v s0[QB], s1[QB];
-    u4 kf[D / 16], vf[2][D / 32], w[QB][2];
+    f16v s0, s1;
+    u4 kf[D / 16], vf[2][D / 32], w[2] = {};
 #pragma unroll
-    for (int q = 0; q < QB; ++q) {
-        m[q] = -INFINITY;
-        l[q] = 0.0f;
+    for (int i = 0; i < D / 32; ++i) {
+        vf[0][i] = vf[1][i] = u4{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[q][i][e] = 0.0f;
-        w[q][0] = w[q][1] = u4{0, 0, 0, 0};
+        for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
     }
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) vf[0][i] = vf[1][i] = u4{0, 0, 0, 0};
     auto read_k = [&](uint32_t off) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) kf[i] = lds_ld<u4>(k_read(k_at + off, i));
     };
-    auto score = [&](f16v (&s)[QB]) {
+    auto score = [&](f16v& s) {
 #pragma unroll
-        for (int q = 0; q < QB; ++q)
+        for (int e = 0; e < 16; ++e) s[e] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[q][e] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int q = 0; q < QB; ++q) s[q] = T::mfma32(kf[i], qf[q][i], s[q]);
+        for (int i = 0; i < D / 16; ++i) s = T::mfma32(kf[i], qf[i], s);
     };
     constexpr int kV = D / 32, kK = D / 16;       // matrix operands of 16 keys of V, of 32 keys of K
-    // With two blocks of rows the operands that no vector instruction touches go
-    // to the accumulation registers.
-    auto put_away = [](u4& x) {
-        if constexpr (QB == 2) asm("" : "+a"(x));
-    };
     auto add_value = [&](int n) {                 // n of the 2 kV operands of a half
-        put_away(vf[n / kV][n % kV]);
-#pragma unroll
-        for (int q = 0; q < QB; ++q) o[q][n % kV] = T::mfma32(vf[n / kV][n % kV], w[q][n / kV], o[q][n % kV]);
+        o[n % kV] = T::mfma32(vf[n / kV][n % kV], w[n / kV], o[n % kV]);
     };
     // A half of the tile, from key `base` on: `cur` holds its scores, `nxt` takes the next half's.
     // The order of the code is the order of issue (the empty barriers hold the
     // compiler to it): vector work between any two matrix instructions, so
     // that neither unit waits for the other.
-    auto half_step = [&](f16v (&cur)[QB], f16v (&nxt)[QB], int base, int blocks_of, uint32_t k_next, uint32_t v_cur,
+    auto half_step = [&](f16v& cur, f16v& nxt, int base, int blocks_of, uint32_t k_next, uint32_t v_cur,
                          auto&& between) {
         const bool all = (blocks_of & 3) == 3 && base <= all_to && (base >= all_from || base <= sinks - kKeys / 2);
         if (!all) {
 #pragma unroll
-            for (int q = 0; q < QB; ++q)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int j = base + 8 * (e >> 2) + 4 * half + (e & 3);
-                    const bool seen = mine[q].seen(j) && (blocks_of >> (e >> 3) & 1);
-                    cur[q][e] = seen ? cur[q][e] : -INFINITY;
-                }
+            for (int e = 0; e < 16; ++e) {
+                const int j = base + 8 * (e >> 2) + 4 * half + (e & 3);
+                const bool seen = mine.seen(j) && (blocks_of >> (e >> 3) & 1);
+                cur[e] = seen ? cur[e] : -INFINITY;
+            }
         }
-#pragma unroll
-        for (int q = 0; q < QB; ++q) asm("" : "+v"(cur[q]));      // one set of registers for both paths
+        asm("" : "+v"(cur));      // one set of registers for both paths
         // A quarter of the products with V: the rows' maxima.
         constexpr int kFirst = kV / 2;
-        float was[QB], ms[QB], sum[QB], top[QB];
-        u4 wn[QB][2];
+        float top = cur[0];
 #pragma unroll
         for (int n = 0; n < kFirst; ++n) {
             __builtin_amdgcn_sched_barrier(0);
             add_value(n);
 #pragma unroll
-            for (int q = 0; q < QB; ++q)
-#pragma unroll
-                for (int e = n * 16 / kFirst; e < (n + 1) * 16 / kFirst; ++e) top[q] = e == 0 ? cur[q][0] : __builtin_elementwise_maximum(top[q], cur[q][e]);
+            for (int e = max(1, n * 16 / kFirst); e < (n + 1) * 16 / kFirst; ++e) top = __builtin_elementwise_maximum(top, cur[e]);
         }
         __builtin_amdgcn_sched_barrier(0);
         add_value(kFirst);
-        bool over = false;
-#pragma unroll
-        for (int q = 0; q < QB; ++q) {
-            const Halves tops = halves(top[q]);
-            top[q] = fmaxf(tops.lo, tops.hi) * scale;
-            over = over || top[q] > m[q] + kLazy;
-        }
-        const bool raise = __any(over);
-#pragma unroll
-        for (int q = 0; q < QB; ++q) {
-            was[q] = m[q];
-            m[q] = raise ? fmaxf(m[q], top[q]) : m[q];
-            ms[q] = m[q] == -INFINITY ? 0.0f : m[q];
-            sum[q] = 0.0f;
-        }
+        const Halves tops = halves(top);
+        top = fmaxf(tops.lo, tops.hi) * scale;
+        const bool raise = __any(top > m + kLazy);
+        const float was = m;
+        m = raise ? fmaxf(m, top) : m;
+        const float ms = m == -INFINITY ? 0.0f : m;
         // The others, then the scores of the next half: the weights.  Operands are
         // read for the next half as soon as their registers are free.
 #pragma unroll
-        for (int q = 0; q < QB; ++q)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) nxt[q][e] = 0.0f;
+        for (int e = 0; e < 16; ++e) nxt[e] = 0.0f;
         constexpr int kRest = 2 * kV - kFirst - 1 + kK;
         // Weight pair p of a lane's 8 passes through three chunks: its
         // exponents, the exponentials, their sum and rounding, so that none waits
         // for the one before.
-        float ex[QB][16];
+        float ex[16], sum = 0.0f;
+        u4 wn[2];
         auto exponents = [&](int n) {
 #pragma unroll
-            for (int e = n * 8 / kRest * 2; e < (n + 1) * 8 / kRest * 2; ++e)
-#pragma unroll
-                for (int q = 0; q < QB; ++q) ex[q][e] = fmaf(cur[q][e], scale, -ms[q]);
+            for (int e = n * 8 / kRest * 2; e < (n + 1) * 8 / kRest * 2; ++e) ex[e] = fmaf(cur[e], scale, -ms);
         };
         auto weights = [&](int n) {
 #pragma unroll
-            for (int p = n * 8 / kRest; p < (n + 1) * 8 / kRest; ++p)
-#pragma unroll
-                for (int q = 0; q < QB; ++q) {
-                    sum[q] += ex[q][2 * p] + ex[q][2 * p + 1];
-                    wn[q][p >> 2][p & 3] = T::pack(ex[q][2 * p], ex[q][2 * p + 1]);
-                }
+            for (int p = n * 8 / kRest; p < (n + 1) * 8 / kRest; ++p) {
+                sum += ex[2 * p] + ex[2 * p + 1];
+                wn[p >> 2][p & 3] = T::pack(ex[2 * p], ex[2 * p + 1]);
+            }
         };
         exponents(0);
 #pragma unroll
@@ -454,12 +400,7 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
             if (k < 0) {
                 add_value(kFirst + 1 + n);
             } else {
-                put_away(kf[k]);
-#pragma unroll
-                for (int q = 0; q < QB; ++q) {
-                    put_away(qf[q][k]);
-                    nxt[q] = T::mfma32(kf[k], qf[q][k], nxt[q]);
-                }
+                nxt = T::mfma32(kf[k], qf[k], nxt);
                 const int g = k / kV, i = k % kV;                 // kK == 2 kV
                 const uint32_t at = v_read(v_at + v_cur, i) + g * 16 * D * 2;
                 const u2 x = lds_tr(at), y = lds_tr(at + 8 * D * 2);            // v_place repeats every 8 rows
@@ -467,31 +408,22 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
                 kf[k] = lds_ld<u4>(k_read(k_at + k_next, k));
             }
 #pragma unroll
-            for (int e = n * 8 / kRest * 2; e < (n + 1) * 8 / kRest * 2; ++e)
-#pragma unroll
-                for (int q = 0; q < QB; ++q) ex[q][e] = exp2_fast(ex[q][e]);
+            for (int e = n * 8 / kRest * 2; e < (n + 1) * 8 / kRest * 2; ++e) ex[e] = exp2_fast(ex[e]);
             if (n + 1 < kRest) exponents(n + 1);
             if (n > 0) weights(n - 1);
         }
         __builtin_amdgcn_sched_barrier(0);
         weights(kRest - 1);
-#pragma unroll
-        for (int q = 0; q < QB; ++q) {
-            w[q][0] = wn[q][0];
-            w[q][1] = wn[q][1];
-            asm volatile("" : "+v"(w[q][0]), "+v"(w[q][1]), "+v"(sum[q]));      // made among the products above
-        }
+        w[0] = wn[0];
+        w[1] = wn[1];
+        asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(sum));      // made among the products above
         if (raise) {
+            const float f = m == -INFINITY ? 1.0f : exp2_fast(was - m);
+            l *= f;
 #pragma unroll
-            for (int q = 0; q < QB; ++q) {
-                const float f = m[q] == -INFINITY ? 1.0f : exp2_fast(was[q] - m[q]);
-                l[q] *= f;
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) o[q][i] *= f;
-            }
+            for (int i = 0; i < kV; ++i) o[i] *= f;
         }
-#pragma unroll
-        for (int q = 0; q < QB; ++q) l[q] += sum[q];
+        l += sum;
     };
 
     // Every wave takes part in every step t of the loads, from first - 1 to
@@ -512,9 +444,9 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
             next = after;
             wait_vmem_below<0>();
         } else if (first + 1 < last) {
-            wait_vmem_below<2 * kPieces>();
+            wait_vmem_below<2 * kLoads>();
         } else {
-            wait_vmem_below<kPieces>();
+            wait_vmem_below<kLoads>();
         }
         __syncthreads();
         if (t >= first && t + 2 < last) {
@@ -538,9 +470,7 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
         load_all(t);
         const uint32_t k_buf = ((t + 1 - first) & 1) * 2 * kTileBytes;
 #pragma unroll
-        for (int q = 0; q < QB; ++q)
-#pragma unroll
-            for (int i = 0; i < kK; ++i) qf[q][i] ^= flip;        // (their first use: not waited for before the tiles' loads)
+        for (int i = 0; i < kK; ++i) qf[i] ^= flip;        // (their first use: not waited for before the tiles' loads)
         read_k(k_buf);
         score(s0);
         read_k(k_buf + kHalf);
@@ -555,9 +485,9 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
             const Source v_source = source_of(true, odd ^ 1, next, t + 1 < last);
             half_step(s0, s1, cur.base, cur.blocks & 15, other, buf, [&](int n, int of) {
 #pragma unroll
-                for (int i = n * 2 * kPieces / of; i < (n + 1) * 2 * kPieces / of; ++i) {
-                    if (i < kPieces) load_piece(true, v_source, i);
-                    else load_piece(false, k_source, i - kPieces);
+                for (int i = n * 2 * kLoads / of; i < (n + 1) * 2 * kLoads / of; ++i) {
+                    if (i < kLoads) load_piece(true, v_source, i);
+                    else load_piece(false, k_source, i - kLoads);
                 }
             });
             half_step(s1, s0, cur.base + kKeys / 2, cur.blocks >> 2 & 3, other + kHalf, buf + kHalf, [](int, int) {});
@@ -574,87 +504,81 @@ __global__ __launch_bounds__(64 * NW * KG, QB == 2 || D == 256 ? 1 : D == 64 && 
     if constexpr (KG == 2) {
         // The second group leaves its results in LDS, the first joins them.  One
         // group at most has seen nothing (m = -inf), or both.
-        constexpr int kRegs = QB * (D / 32) * 16;
-        static_assert(NW * kRegs * 64 * 4 <= (int)sizeof lds && QB == 1, "room for the second group's results");
+        constexpr int kRegs = (D / 32) * 16;
+        static_assert(kRowWaves * kRegs * 64 * 4 <= (int)sizeof lds, "room for the second group's results");
         float* const at = reinterpret_cast<float*>(lds) + wave * kRegs * 64 + lane;
         __syncthreads();
         if (group == 1) {
 #pragma unroll
-            for (int i = 0; i < kRegs; ++i) at[i * 64] = o[0][i / 16][i % 16];
+            for (int i = 0; i < kRegs; ++i) at[i * 64] = o[i / 16][i % 16];
         }
-        __shared__ float stats[NW][2][64];
+        __shared__ float stats[kRowWaves][2][64];
         if (group == 1) {
-            stats[wave][0][lane] = m[0];
-            stats[wave][1][lane] = l[0];
+            stats[wave][0][lane] = m;
+            stats[wave][1][lane] = l;
         }
         __syncthreads();
         if (group == 1) return;
-        const float m1 = stats[wave][0][lane], l1 = stats[wave][1][lane], mn = fmaxf(m[0], m1);
-        const float f0 = mn == -INFINITY ? 1.0f : exp2_fast(m[0] - mn), f1 = mn == -INFINITY ? 0.0f : exp2_fast(m1 - mn);
-        m[0] = mn;
-        l[0] = l[0] * f0 + l1 * f1;
+        const float m1 = stats[wave][0][lane], l1 = stats[wave][1][lane], mn = fmaxf(m, m1);
+        const float f0 = mn == -INFINITY ? 1.0f : exp2_fast(m - mn), f1 = mn == -INFINITY ? 0.0f : exp2_fast(m1 - mn);
+        m = mn;
+        l = l * f0 + l1 * f1;
 #pragma unroll
-        for (int i = 0; i < kRegs; ++i) o[0][i / 16][i % 16] = o[0][i / 16][i % 16] * f0 + at[i * 64] * f1;
+        for (int i = 0; i < kRegs; ++i) o[i / 16][i % 16] = o[i / 16][i % 16] * f0 + at[i * 64] * f1;
     }
 
+    // Lane and the one 32 away hold the two halves of a row's sum.
+    const Halves sums = halves(l);
+    l = sums.lo + sums.hi;
     const Partials parts(a, D, splits);
+    float probe = 0.0f;
 #pragma unroll
-    for (int q = 0; q < QB; ++q) {
-        // Lane and the one 32 away hold the two halves of a row's sum.
-        const Halves sums = halves(l[q]);
-        l[q] = sums.lo + sums.hi;
-        float probe = 0.0f;
+    for (int i = 0; i < kV; ++i)
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) probe = fmaf(o[q][i][e], 0.0f, probe);
-        if (__any(live[q] && !(probe == 0.0f))) {
-            for (int i = 0; i < min(32, w_rows - 32 * q); ++i) {
-                const int r = kWaveRows * wave + 32 * q + i, past = token_of(r);
-                const int tk = row_first + token0 + past, hd = kvh * share + skip + r - past * share;
-                float x[4], mx, lx;
-                plain_row<D>(a, span, begin, end, key_span(a, p_first + past), table, kvh,
-                             a.q + tk * a.sq + (int64_t)hd * D, x, mx, lx);
-                const int64_t row = (int64_t)tk * a.q_heads + hd;
-                for (int k = 0; k < 4; ++k) {
-                    const int d = lane + 64 * k;
-                    if (d >= D) continue;
-                    if (splits > 1) {
-                        parts.o[(row * splits + split) * D + d] = x[k];
-                    } else {
-                        a.o[tk * a.so + (int64_t)hd * D + d] = (uint16_t)T::pack(lx == 0.0f ? 0.0f : x[k] / lx, 0.0f);
-                        if (d == 0 && a.lse)
-                            a.lse[row] = lx == 0.0f ? -INFINITY : mx * 0.6931471805599453f + logf(lx);
-                    }
+        for (int e = 0; e < 16; ++e) probe = fmaf(o[i][e], 0.0f, probe);
+    if (__any(live && !(probe == 0.0f))) {
+        for (int r = 32 * wave; r < 32 * wave + w_rows; ++r) {
+            const int p = token_of(r), tk = row_first + token0 + p, hd = kvh * share + skip + r - p * share;
+            float x[4], mx, lx;
+            plain_row<D>(a, span, begin, end, key_span(a, p_first + p), table, kvh, a.q + tk * a.sq + (int64_t)hd * D, x,
+                         mx, lx);
+            const int64_t row = (int64_t)tk * a.q_heads + hd;
+            for (int k = 0; k < 4; ++k) {
+                const int d = lane + 64 * k;
+                if (d >= D) continue;
+                if (splits > 1) {
+                    parts.o[(row * splits + split) * D + d] = x[k];
+                } else {
+                    a.o[tk * a.so + (int64_t)hd * D + d] = (uint16_t)T::pack(lx == 0.0f ? 0.0f : x[k] / lx, 0.0f);
+                    if (d == 0 && a.lse) a.lse[row] = lx == 0.0f ? -INFINITY : mx * 0.6931471805599453f + logf(lx);
                 }
-                if (splits > 1 && lane == 0) parts.mark(row, split, mx, lx);
             }
-            continue;
+            if (splits > 1 && lane == 0) parts.mark(row, split, mx, lx);
         }
-        if (!live[q]) continue;
-        const int64_t row = (int64_t)token[q] * a.q_heads + head[q];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const f4 x = {o[q][i][4 * e], o[q][i][4 * e + 1], o[q][i][4 * e + 2], o[q][i][4 * e + 3]};
-                const int d = 32 * i + 8 * e + 4 * half;
-                if (splits > 1) parts.put4(row, split, d, x);
-                else store_row4<T>(a, token[q], head[q], D, d, x, m[q], l[q]);
-            }
-        if (splits > 1 && half == 0) parts.mark(row, split, m[q], l[q]);
+        return;
     }
+    if (!live) return;
+    const int64_t row = (int64_t)token * a.q_heads + head;
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f4 x = {o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
+            const int d = 32 * i + 8 * e + 4 * half;
+            if (splits > 1) parts.put4(row, split, d, x);
+            else store_row4<T>(a, token, head, D, d, x, m, l);
+        }
+    if (splits > 1 && half == 0) parts.mark(row, split, m, l);
 }
 
-// Slots of `rows` query rows, enough for every sequence's.
-int64_t slots_of(const AttnArgs& a, int rows) {
-    return (int64_t)a.tokens * (a.q_heads / a.kv_heads) / rows + a.kv.seqs;
+// Slots of kRows query rows, enough for every sequence's.
+int64_t slots_of(const AttnArgs& a) {
+    return (int64_t)a.tokens * (a.q_heads / a.kv_heads) / kRows + a.kv.seqs;
 }
 
-template <class T, int D, int NW, int QB, int KG>
+template <class T, int D, int KG>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-    constexpr int kRows = 32 * QB * NW;
-    const int64_t slots = slots_of(a, kRows);
+    const int64_t slots = slots_of(a);
     int64_t most = a.max_len;
     if (a.window && (int64_t)a.window + a.sinks + kRows < most) most = (int64_t)a.window + a.sinks + kRows;
     const int64_t tiles = (most + kKeys - 1) / kKeys, units = slots * a.kv_heads;
@@ -662,11 +586,11 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     const int64_t splits = max((int64_t)1, min(want, kAttnSplitRows / ((int64_t)a.tokens * a.q_heads)));
     const int chunk = (int)max((int64_t)1, (tiles + splits - 1) / splits);
     // A grid holds fewer than 2^32 threads; slots past it go into further launches.
-    const int64_t per_slot = a.kv_heads * splits, at_once = ((int64_t(1) << 32) / (64 * NW * KG) - 1) / per_slot;
+    const int64_t per_slot = a.kv_heads * splits, at_once = ((int64_t(1) << 32) / (64 * kRowWaves * KG) - 1) / per_slot;
     for (int64_t s = 0; s < slots; s += at_once) {
         const int64_t n = min(at_once, slots - s);
-        hipLaunchKernelGGL((attention_prefill_kernel<T, D, NW, QB, KG>), dim3((unsigned)(n * per_slot)), dim3(64 * NW * KG), 0, stream,
-                           a, (int)slots, (int)s, (int)splits, chunk);
+        hipLaunchKernelGGL((attention_prefill_kernel<T, D, KG>), dim3((unsigned)(n * per_slot)), dim3(64 * kRowWaves * KG), 0,
+                           stream, a, (int)slots, (int)s, (int)splits, chunk);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -675,12 +599,12 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
 
 // Two groups of waves on every other tile where one round of workgroups (one
 // a CU) holds all rows: half the tiles one after another (61 tokens on 24576:
-// @KG2@).  With more, two workgroups of one group share a CU and
-// hide each other's beginnings and ends (2048 tokens: @KG1@).
+// 73 us in one group, 55 in two).  With more, two workgroups of one group share a CU and
+// hide each other's beginnings and ends (8192 windowed tokens: 427 us in one group, 476 in two).
 template <class T, int D>
 hipError_t launch_groups(const AttnArgs& a, hipStream_t stream) {
-    if (slots_of(a, 128) * a.kv_heads <= kSplitTarget) return launch<T, D, 4, 1, 2>(a, stream);
-    return launch<T, D, 4, 1, 1>(a, stream);
+    if (slots_of(a) * a.kv_heads <= kSplitTarget) return launch<T, D, 2>(a, stream);
+    return launch<T, D, 1>(a, stream);
 }
 
 template <class T>
@@ -689,7 +613,7 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
         case 64: return launch_groups<T, 64>(a, stream);
         case 96: return launch_groups<T, 96>(a, stream);
         case 128: return launch_groups<T, 128>(a, stream);
-        default: return launch<T, 256, 4, 1, 1>(a, stream);           // two groups' tiles do not fit LDS
+        default: return launch<T, 256, 1>(a, stream);           // two groups' tiles do not fit LDS
     }
 }
 

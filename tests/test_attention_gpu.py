@@ -386,3 +386,54 @@ def test_offsets_past_32_bits(env):
     slim.kv_copy_pages(kpool, vpool, src, dst)
     assert torch.equal(kpool[11], kpool[far[0]]) and torch.equal(vpool[11], vpool[far[0]])
     assert (kpool[far[0] - 1] == 3).all() and (vpool[far[0] - 1] == 4).all()
+
+
+# ------------------------------------------------------------ larger grids
+@pytest.mark.parametrize("dtype,dim", [("fp16", 64), ("bf16", 96), ("fp16", 128), ("bf16", 256)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 5), (500, 0)])
+def test_prefill_more_row_blocks_than_a_round_of_workgroups(env, dtype, dim, window, sinks):
+    """Many short sequences with one behind a prefix of more than 64 tiles, unsplit."""
+    new = [3] + [int(n) for n in np.random.default_rng(71).integers(0, 9, 70)]
+    pre = [9000] + [int(n) for n in np.random.default_rng(72).integers(0, 150, 70)]
+    c = case(env[0], 71, dtype, [n + p for n, p in zip(new, pre)], 8, 4, dim, 32, new=new)
+    y, lse = run(env, c, window, sinks, lse=True)
+    check(c, y, lse, window, sinks)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prefill_long_unsplit_walk_of_both_wave_groups(env, dim):
+    """As few row blocks as one round holds, unsplit: each group of waves walks more than 64 tiles."""
+    new = [2] + [1] * 45
+    pre = [9500] + [int(n) for n in np.random.default_rng(73).integers(0, 200, 45)]
+    c = case(env[0], 73, "fp16", [n + p for n, p in zip(new, pre)], 4, 4, dim, 16, new=new)
+    y, lse = run(env, c, lse=True)
+    check(c, y, lse)
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,new,pre", [(12, 4, 700, 0), (4, 4, 600, 333), (64, 8, 130, 40), (7, 7, 129, 1)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 3)])
+def test_prefill_row_blocks_cross_tokens_and_heads(env, q_heads, kv_heads, new, pre, window, sinks):
+    c = case(env[0], 74, "bf16", [new + pre, 5], q_heads, kv_heads, 64, 64, new=[new, 2])
+    y, lse = run(env, c, window, sinks, lse=True)
+    check(c, y, lse, window, sinks)
+
+
+def test_seen_infinities_give_what_the_formula_gives(env):
+    """An infinite value reaches the rows that see it, in its element only; an infinite score gives NaN."""
+    torch, slim = env
+    for new in (None, [90]):
+        c = case(torch, 75, "bf16", [90], 2, 1, 64, 16, new=new)
+        k, v = host(c["k"]), host(c["v"])
+        want, _, mass = reference(c, k=k, v=v)
+        page = int(c["table"][0, 4])
+        c["v"][page, 0, 6, 3] = float("inf")                      # key 70
+        got = host(run(env, c))
+        assert np.isposinf(got[-1, :, 3]).all()
+        rows = np.arange(got.shape[0]) if new else np.asarray([89])
+        for t, p in enumerate(rows):
+            keep = np.arange(64) != 3 if p >= 70 else np.ones(64, dtype=bool)
+            over = np.abs(got[t][:, keep] - want[t][:, keep]) - bound(c, want[t], mass[t])[:, keep]
+            assert over.max() <= 0, (p, over.max())
+        c["v"][page, 0, 6, 3] = 0.0
+        c["q"][-1, 0, 0] = float("inf")
+        assert np.isnan(host(run(env, c))[-1, 0]).all()
