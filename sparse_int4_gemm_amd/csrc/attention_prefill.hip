@@ -342,13 +342,25 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     // that neither unit waits for the other.
     auto half_step = [&](f16v& cur, f16v& nxt, int base, int blocks_of, uint32_t k_next, uint32_t v_cur,
                          auto&& between) {
-        const bool all = (blocks_of & 3) == 3 && base <= all_to && (base >= all_from || base <= sinks - kKeys / 2);
-        if (!all) {
+        // Keys that some row does not see: element e's is c + base + 4 half, c a
+        // constant, so a limit is compared with constants.  Mostly only one of the two ends cuts.
+        if (base > all_to || blocks_of != 3) {
+            const int lim = mine.end - base - 4 * half;
+            const int lims[2] = {blocks_of & 1 ? lim : -1, blocks_of & 2 ? lim : -1};
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int j = base + 8 * (e >> 2) + 4 * half + (e & 3);
-                const bool seen = mine.seen(j) && (blocks_of >> (e >> 3) & 1);
-                cur[e] = seen ? cur[e] : -INFINITY;
+            for (int e = 0; e < 16; ++e) cur[e] = 8 * (e >> 2) + (e & 3) < lims[e >> 3] ? cur[e] : -INFINITY;
+        }
+        if (base < all_from && base > sinks - kKeys / 2) {
+            const int lim = mine.start - base - 4 * half, sink = mine.sinks - base - 4 * half;
+            if (base >= sinks) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) cur[e] = 8 * (e >> 2) + (e & 3) >= lim ? cur[e] : -INFINITY;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int c = 8 * (e >> 2) + (e & 3);
+                    cur[e] = c >= lim || c < sink ? cur[e] : -INFINITY;
+                }
             }
         }
         asm("" : "+v"(cur));      // one set of registers for both paths
@@ -483,7 +495,7 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
             // Past the last tile they read nothing (and write zeros nobody reads).
             const Source k_source = source_of(false, odd, after, t + 2 < last);
             const Source v_source = source_of(true, odd ^ 1, next, t + 1 < last);
-            half_step(s0, s1, cur.base, cur.blocks & 15, other, buf, [&](int n, int of) {
+            half_step(s0, s1, cur.base, cur.blocks & 3, other, buf, [&](int n, int of) {
 #pragma unroll
                 for (int i = n * 2 * kLoads / of; i < (n + 1) * 2 * kLoads / of; ++i) {
                     if (i < kLoads) load_piece(true, v_source, i);
