@@ -298,15 +298,25 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     auto k_read = [&](uint32_t at, int i) { return D == 96 ? (at ^ (32u * (i & 1))) + 64 * (i >> 1) : at ^ (32u * i); };
     auto v_read = [&](uint32_t at, int i) { return D == 96 ? at + 64 * i : at ^ (64u * i); };
 
-    // The queries are asked for after the first tile's pages, which are needed first.
     if (first < last) look_up(first);
-    u4 qf[D / 16];
+    // The wave's queries go through LDS as a key tile does (waves 0 and 1 of the
+    // group to K of buffer 1, 2 and 3 to V of it, not in use yet): read straight
+    // into the operand layout, every 32 bytes of a load would be another row's.
+    // The rows' elements in global memory from the block's first token and head on:
+    auto element = [&](int r, int64_t stride) {
+        const int p = token_of(r);
+        return (int)(p * stride) + (skip + r - p * share) * D;
+    };
+    auto load_queries = [&] {
+        const u4 rsrc = rsrc_words(a.q + (int64_t)(row_first + token0) * a.sq + (int64_t)kvh * share * D, kOOB);
+        const uint32_t to = lds0 + 2 * kTileBytes + wave * 32 * D * 2;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-        qf[i] = u4{0, 0, 0, 0};
-        if (live && a.scale != 0.0f)
-            qf[i] = *reinterpret_cast<const u4*>(a.q + token * a.sq + (int64_t)head * D + 16 * i + 8 * half);
-    }
+        for (int j = 0; j < 2 * kLoads; ++j) {
+            const int c = 64 * j + lane, r = c / kC, chunk = k_place<D>(r, c - r * kC), in = 32 * wave + r;
+            lds_load16_at(rsrc, to + 1024 * j, in < rows ? (element(in, a.sq) + chunk * 8) * 2 : kOOB, 0);
+        }
+    };
+    u4 qf[D / 16];
 
     float m = -INFINITY, l = 0.0f;
     f16v o[D / 32];
@@ -440,23 +450,22 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
 
     // Every wave takes part in every step t of the loads, from first - 1 to
     // last - 1: at the end of `advance` K of tile t + 1 and V of tile t have
-    // landed for all waves, and all are done with K of tile t and V of tile t - 1, so
-    // the loads of K of tile t + 2 and V of tile t + 1 may begin.
+    // landed for all waves (in step first - 1 K only), and all are done with K of
+    // tile t and V of tile t - 1 (or the queries), so the loads of K of tile t + 2 and
+    // V of tile t + 1 may begin.
     Place cur, next, after;                       // of tiles t, t + 1 and t + 2
     if (first < last) {
         cur = next = place(first);
         after = place(min(first + 1, last - 1));
         load(false, 0, next);
+        load_queries();
         load(true, 0, next);
-        if (first + 1 < last) load(false, 1, after);
     }
     auto advance = [&](int t) {
         if (t >= first) {
             cur = next;
             next = after;
             wait_vmem_below<0>();
-        } else if (first + 1 < last) {
-            wait_vmem_below<2 * kLoads>();
         } else {
             wait_vmem_below<kLoads>();
         }
@@ -467,10 +476,18 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         }
     };
     auto load_all = [&](int t) {
-        if (t >= first && t + 2 < last) load(false, (t - first) & 1, after);
+        if (t + 2 < last) load(false, (t - first) & 1, after);
         if (t >= first && t + 1 < last) load(true, (t + 1 - first) & 1, next);
     };
     constexpr uint32_t kHalf = kKeys / 2 * D * 2;
+    if (first < last) {
+        wait_vmem_below<kLoads>();                // the queries; V of the first tile may still be on its way
+#pragma unroll
+        for (int i = 0; i < kK; ++i) {
+            qf[i] = lds_ld<u4>(k_read(k_at + 2 * kTileBytes + wave * 32 * D * 2, i)) ^ flip;
+            if (a.scale == 0.0f) qf[i] = u4{0, 0, 0, 0};
+        }
+    }
     // (A group without tiles, or with one fewer, only takes part in the barriers.)
     int t = begin < end ? first - 1 : steps;
     for (; t < w_begin - 1; ++t) {
@@ -481,8 +498,6 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         advance(t);
         load_all(t);
         const uint32_t k_buf = ((t + 1 - first) & 1) * 2 * kTileBytes;
-#pragma unroll
-        for (int i = 0; i < kK; ++i) qf[i] ^= flip;        // (their first use: not waited for before the tiles' loads)
         read_k(k_buf);
         score(s0);
         read_k(k_buf + kHalf);
@@ -513,13 +528,14 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     }
     wait_vmem_below<0>();                         // no load may write LDS from here on
 
+    constexpr int kRegs = (D / 32) * 16;          // 32-bit results of a lane
+    static_assert(kRowWaves * kRegs * 64 * 4 <= (int)sizeof lds, "room for a group's results");
+    unsigned char* const mine_lds = &lds[0][0][0][0] + wave * kRegs * 64 * 4;
+    __syncthreads();                              // LDS is free
     if constexpr (KG == 2) {
         // The second group leaves its results in LDS, the first joins them.  One
         // group at most has seen nothing (m = -inf), or both.
-        constexpr int kRegs = (D / 32) * 16;
-        static_assert(kRowWaves * kRegs * 64 * 4 <= (int)sizeof lds, "room for the second group's results");
-        float* const at = reinterpret_cast<float*>(lds) + wave * kRegs * 64 + lane;
-        __syncthreads();
+        float* const at = reinterpret_cast<float*>(mine_lds) + lane;
         if (group == 1) {
 #pragma unroll
             for (int i = 0; i < kRegs; ++i) at[i * 64] = o[i / 16][i % 16];
@@ -537,6 +553,7 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         l = l * f0 + l1 * f1;
 #pragma unroll
         for (int i = 0; i < kRegs; ++i) o[i / 16][i % 16] = o[i / 16][i % 16] * f0 + at[i * 64] * f1;
+        asm volatile("" ::: "memory");            // read before the rows go to the same place
     }
 
     // Lane and the one 32 away hold the two halves of a row's sum.
@@ -569,18 +586,38 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         }
         return;
     }
-    if (!live) return;
     const int64_t row = (int64_t)token * a.q_heads + head;
+    if (splits > 1) {
+        if (!live) return;
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                parts.put4(row, split, 32 * i + 8 * e + 4 * half,
+                           f4{o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]});
+        if (half == 0) parts.mark(row, split, m, l);
+        return;
+    }
+    // The rows leave through LDS too (each wave in its own part, in the order of
+    // key rows), whole rows at a time.
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (a.lse && live && half == 0) a.lse[row] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+    const uint32_t out = lds_u32(mine_lds);
+    typedef __attribute__((address_space(3))) u2* LdsPair;
 #pragma unroll
     for (int i = 0; i < kV; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const f4 x = {o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
-            const int d = 32 * i + 8 * e + 4 * half;
-            if (splits > 1) parts.put4(row, split, d, x);
-            else store_row4<T>(a, token, head, D, d, x, m, l);
-        }
-    if (splits > 1 && half == 0) parts.mark(row, split, m, l);
+        for (int e = 0; e < 4; ++e)
+            *(LdsPair)(size_t)(out + col * (D * 2) + k_place<D>(col, 4 * i + e) * 16 + half * 8) =
+                u2{T::pack(o[i][4 * e] * inv, o[i][4 * e + 1] * inv), T::pack(o[i][4 * e + 2] * inv, o[i][4 * e + 3] * inv)};
+    asm volatile("" ::: "memory");                // a wave's LDS accesses are served in their order
+    uint16_t* const to = a.o + (int64_t)(row_first + token0) * a.so + (int64_t)kvh * share * D;
+#pragma unroll
+    for (int j = 0; j < 2 * kLoads; ++j) {
+        const int c = 64 * j + lane, r = c / kC, chunk = k_place<D>(r, c - r * kC), in = 32 * wave + r;
+        const u4 x = lds_ld<u4>(out + 1024 * j + lane * 16);
+        if (in < rows) *reinterpret_cast<u4*>(to + element(in, a.so) + chunk * 8) = x;
+    }
 }
 
 // Slots of kRows query rows, enough for every sequence's.
