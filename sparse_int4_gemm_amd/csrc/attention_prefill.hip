@@ -647,12 +647,16 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
 }
 
 // Two groups of waves on every other tile where one round of workgroups (one
-// a CU) holds all rows: half the tiles one after another (61 tokens on 24576:
-// 73 us in one group, 55 in two).  With more, two workgroups of one group share a CU and
-// hide each other's beginnings and ends (8192 windowed tokens: 427 us in one group, 476 in two).
+// a CU) holds all row blocks: half the tiles one after another (61 tokens on
+// 24576: 73 us in one group, 55 in two; 1024 tokens of 32 heads 28.9 and 25.9).
+// With more, two workgroups of one group share a CU and hide each other's
+// beginnings and ends (8192 windowed tokens: 427 us in one group, 476 in two;
+// 2048 tokens of 32 heads 56.9 and 58.3).
 template <class T, int D>
 hipError_t launch_groups(const AttnArgs& a, hipStream_t stream) {
-    if (slots_of(a) * a.kv_heads <= kSplitTarget) return launch<T, D, 2>(a, stream);
+    const int64_t rows = (int64_t)a.tokens * (a.q_heads / a.kv_heads);
+    const int64_t blocks = a.kv.seqs == 1 ? (rows + kRows - 1) / kRows : slots_of(a);
+    if (blocks * a.kv_heads <= kSplitTarget) return launch<T, D, 2>(a, stream);
     return launch<T, D, 1>(a, stream);
 }
 
