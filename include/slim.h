@@ -432,10 +432,9 @@ slim_status slim_kv_copy_pages(void* Kpool, void* Vpool, int64_t layers, int64_t
  * Workspace of slim_attention_decode (tokens == seqs) and
  * slim_attention_prefill in bytes, 0 for a rejected shape.  It does not depend
  * on the lengths, and one made for some tokens and sequences serves any other
- * number of the same heads.  Caller-owned device memory with the rules of
- * slim_linear_workspace_bytes: zero its first 16384 bytes before the first
- * use; every call leaves it valid for the next of any shape that it is large
- * enough for; calls that share it must be ordered on one stream.
+ * number of the same heads.  Caller-owned device memory; what it holds before
+ * a call does not matter, and calls that share it must be ordered on one
+ * stream.
  */
 size_t slim_attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t q_heads, int64_t kv_heads,
                                       int64_t head_dim);

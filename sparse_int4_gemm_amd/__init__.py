@@ -229,13 +229,13 @@ def kv_copy_pages(kpool: torch.Tensor, vpool: torch.Tensor, src: torch.Tensor, d
 
 def workspace_attention(tokens: int, seqs: int, q_heads: int, kv_heads: int, head_dim: int,
                         device="cuda") -> torch.Tensor:
-    """A zero-filled workspace for attention_decode (tokens == seqs) and
-    attention_prefill; its size does not depend on the lengths."""
+    """A workspace for attention_decode (tokens == seqs) and attention_prefill;
+    one serves any number of tokens and sequences of these heads."""
     nbytes = slim_attention_workspace_bytes(tokens, seqs, q_heads, kv_heads, head_dim)
     if nbytes == 0:
         raise ValueError(f"no attention of this shape: {tokens} tokens, {seqs} sequences, {q_heads} query heads, "
                          f"{kv_heads} key heads, head size {head_dim}")
-    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _attention_buffers(q, seqs, kpool, ws, out, stream):

@@ -95,7 +95,7 @@ hipError_t launch_attention_join(const AttnArgs& a, int splits, hipStream_t stre
 // one workspace serves every batch of its heads.
 size_t attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
     const size_t parts = (size_t)kAttnSplitRows * (size_t)(head_dim + 2) * sizeof(float);
-    return kAttnReserved + ((parts + 255) & ~size_t(255));
+    return (parts + 255) & ~size_t(255);
 }
 
 }  // namespace slim

@@ -39,10 +39,9 @@ struct AppendArgs {
     int32_t tokens, kv_heads, head_dim;
 };
 
-// Workspace: kAttnReserved bytes, then the partial results of split key axes,
-// for at most kAttnSplitRows (row, split) pairs: a call splits its rows
-// no further than that, whatever its plan would be.
-constexpr size_t kAttnReserved = 256;
+// Workspace: the partial results of split key axes, for at most
+// kAttnSplitRows (row, split) pairs: a call splits its rows no further than
+// that, whatever its plan would be.
 constexpr int64_t kAttnSplitRows = 32768;
 
 size_t attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim);

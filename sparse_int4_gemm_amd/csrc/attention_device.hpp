@@ -88,9 +88,7 @@ struct Span {
 };
 
 // Page of a sequence's key `key` (the same in all lanes), -1 if it has none
-// (from `keys` on, or an entry out of range).  Read through the scalar cache: a
-// vector load would be waited for behind every key and value load in flight,
-// since those return in order.
+// (from `keys` on, or an entry out of range), through the scalar cache.
 typedef const __attribute__((address_space(4))) int32_t* ScalarInts;
 __device__ __forceinline__ int page_of(const AttnArgs& a, int b, int key, int keys) {
     key = __builtin_amdgcn_readfirstlane(key);
@@ -135,7 +133,7 @@ struct Partials {
     float* ml;            // [rows][splits][2]
     int D, splits;
     __host__ __device__ Partials(const AttnArgs& a, int D_, int splits_) : D(D_), splits(splits_) {
-        o = reinterpret_cast<float*>(a.ws + kAttnReserved);
+        o = reinterpret_cast<float*>(a.ws);
         ml = o + (int64_t)a.tokens * a.q_heads * splits * D;
     }
     __device__ __forceinline__ void mark(int64_t row, int split, float top, float sum) const {

@@ -35,14 +35,4 @@ __device__ __forceinline__ int find_seq(const PagedKV& kv, int t) {
     return kv.starts[lo] <= t && t < kv.starts[lo + 1] ? lo : -1;
 }
 
-// First row and number of rows of sequence b's new tokens, within [0, tokens].
-__device__ __forceinline__ void new_rows(const PagedKV& kv, int b, int tokens, int& first, int& count) {
-    if (!kv.starts) { first = b; count = 1; return; }
-    int s0 = kv.starts[b], s1 = kv.starts[b + 1];
-    s0 = s0 < 0 ? 0 : (s0 > tokens ? tokens : s0);
-    s1 = s1 < s0 ? s0 : (s1 > tokens ? tokens : s1);
-    first = s0;
-    count = s1 - s0;
-}
-
 }  // namespace slim
