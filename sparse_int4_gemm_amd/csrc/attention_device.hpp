@@ -100,9 +100,10 @@ __device__ __forceinline__ int page_of(const AttnArgs& a, int b, int key, int ke
 
 // Of a single position p.
 __device__ __forceinline__ Span key_span(const AttnArgs& a, int p) {
-    const int64_t capacity = (int64_t)a.kv.width << a.kv.page_shift;      // at most 2^30
+    // (32-bit: a 64-bit comparison goes to the vector unit, and what follows
+    // from it with it.  The capacity is at most 2^30.)
     Span s;
-    s.end = (int)min((int64_t)p + 1, capacity);
+    s.end = min(p + 1, a.kv.width << a.kv.page_shift);
     s.start = a.window ? max(0, p - a.window + 1) : 0;
     s.sinks = a.window ? a.sinks : 0;
     return s;

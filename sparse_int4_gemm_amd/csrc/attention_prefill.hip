@@ -151,24 +151,22 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     // Sequence b's slots begin at starts[b] * share / kRows + b: at least as
     // many as its rows fill.  Found as find_seq finds a token's sequence; the
     // last step has its starts and length in the lanes already.
-    int lo = 0, n = a.kv.seqs, from_row = 0, to_row = 0, len = 0;
-    for (;;) {
+    int lo = 0, n = a.kv.seqs, found, starts, ends, lens;
+    do {
         const int step = (n + 63) >> 6, i = lo + min(lane * step, n - 1);
-        from_row = a.kv.starts[i];
-        to_row = a.kv.starts[i + 1];
-        len = a.kv.lens[i];
-        const uint64_t ok = __ballot(lane * step < n && (((int64_t)from_row * share) >> kRowsLog) + i <= slot);
+        starts = a.kv.starts[i];
+        ends = a.kv.starts[i + 1];
+        lens = a.kv.lens[i];
+        const uint64_t ok = __ballot(lane * step < n && (((int64_t)starts * share) >> kRowsLog) + i <= slot);
         if (ok == 0) return;
-        const int c = 63 - __builtin_clzll(ok);
-        lo += c * step;
-        n = min(step, n - c * step);
-        if (n == 1) {
-            from_row = __builtin_amdgcn_readlane(from_row, c);
-            to_row = __builtin_amdgcn_readlane(to_row, c);
-            len = min(max(__builtin_amdgcn_readlane(len, c), 0), kMaxLen);
-            break;
-        }
-    }
+        found = 63 - __builtin_clzll(ok);
+        lo += found * step;
+        n = min(step, n - found * step);
+    } while (n > 1);
+    // Of one value for all lanes from here on, in variables that never held
+    // another: else every branch and loop below would run under a lane mask.
+    const int from_row = __builtin_amdgcn_readlane(starts, found), to_row = __builtin_amdgcn_readlane(ends, found);
+    const int len = min(max(__builtin_amdgcn_readlane(lens, found), 0), kMaxLen);
     const int b = __builtin_amdgcn_readfirstlane(lo);
     const int64_t tile = slot - ((((int64_t)from_row * share) >> kRowsLog) + b);
     const int row_first = min(max(from_row, 0), a.tokens), count = max(min(to_row, a.tokens) - row_first, 0);
@@ -178,15 +176,17 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     // divisions, of small numbers by a product with the reciprocal (exact:
     // (x + 1/2) / share is at least 1 / 2048 away from a whole number).
     const uint32_t r0 = (uint32_t)(tile * kRows);
-    const int rows = (int)min((int64_t)kRows, (int64_t)count * share - r0);
+    const int64_t left = (int64_t)count * share - r0;
+    const int rows = left >> kRowsLog ? kRows : (int)left;
     const int token0 = (int)(r0 / (uint32_t)share), skip = (int)(r0 - (uint32_t)token0 * (uint32_t)share);
     const float per_share = 1.0f / (float)share;
     auto token_of = [&](int r) { return (int)(((float)(skip + r) + 0.5f) * per_share); };
     const int before = len - count;                                     // position of new token 0
-    const int p_first = before + token0, p_last = before + token0 + token_of(rows - 1);
+    const int p_first = before + token0;
+    const int p_last = p_first + __builtin_amdgcn_readfirstlane(token_of(rows - 1));
     Span span = key_span(a, p_last);
     span.start = a.window ? max(0, p_first - a.window + 1) : 0;
-    const int keys = min(len, (int)min((int64_t)a.kv.width << a.kv.page_shift, (int64_t)kMaxLen));
+    const int keys = min(len, a.kv.width << a.kv.page_shift);
     const int32_t* table = a.kv.table + (int64_t)b * a.kv.width;
 
     const int tiles = span.tiles(kKeys);
