@@ -127,9 +127,27 @@ __device__ void plain_row(const AttnArgs& a, const Span& tiles, int first, int l
     }
 }
 
+// Division by a number that the launch knows: a product with m = (2^32 - 1) / d
+// (rounded down) gives the quotient or one less.  (The compiler's own takes some 30
+// instructions, and the kernel's beginning is bound by their number.)
+struct Divisor {
+    uint32_t d, m;
+    explicit Divisor(int64_t by) : d((uint32_t)by), m(0xFFFFFFFFu / (uint32_t)by) {}
+    __device__ __forceinline__ int quotient(uint32_t n) const {
+        const uint32_t q = __umulhi(n, m);
+        return (int)(n - q * d >= d ? q + 1 : q);
+    }
+};
+
+// What the launch knows of the grid: key heads x splits x slots (from slot0 on).
+struct Grid {
+    Divisor kv_heads, splits, share;
+    int32_t slots, slot0, chunk, round;
+};
+
 template <class T, int D, int KG>
 __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG == 1 ? 3 : 2) void attention_prefill_kernel(
-    AttnArgs a, int slots, int slot0, int splits, int chunk) {
+    AttnArgs a, Grid grid) {
     constexpr int kTileBytes = kKeys * D * 2, kC = D / 8;      // chunks of a row
     constexpr int kLoads = D / 32;                       // 64-lane loads of a 16-row block
     __shared__ __align__(1024) unsigned char lds[KG][2][2][kTileBytes];         // [group][buffer][K, V]
@@ -141,12 +159,18 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     // Head fastest (a workgroup's XCD is its index mod 8: with 8 or more key
     // heads an XCD's L2 serves its own heads only), then the split, then the
     // slot of rows, last ones first: under the causal mask they have the most keys.
-    const int share = a.q_heads / a.kv_heads;
-    int id = blockIdx.x;
-    const int kvh = id % a.kv_heads;
-    id /= a.kv_heads;
-    const int split = id % splits;
-    const int slot = slots - 1 - (slot0 + id / splits);
+    const int share = grid.share.d, splits = grid.splits.d;
+    const int units = grid.kv_heads.quotient(blockIdx.x), kvh = blockIdx.x - units * a.kv_heads;
+    const int in_order = grid.splits.quotient(units), split = units - in_order * splits;
+    int order = grid.slot0 + in_order;
+    if constexpr (KG == 1 && (D == 96 || D == 128)) {
+        // Two workgroups share a CU from the start (at D = 64 three, at 256 one): the
+        // second 256 in reverse, the shortest of them beside the longest of the first
+        // (2048 tokens of 32 heads of 128: 55.8 us in plain order, 54.4 so; of 64: 40.7 and 41.6).
+        if (order >= grid.round && order < 2 * grid.round)
+            order = grid.round + min(2 * grid.round, grid.slots) - 1 - order;
+    }
+    const int slot = grid.slots - 1 - order;
 
     // Sequence b's slots begin at starts[b] * share / kRows + b: at least as
     // many as its rows fill.  Found as find_seq finds a token's sequence; the
@@ -178,7 +202,7 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     const uint32_t r0 = (uint32_t)(tile * kRows);
     const int64_t left = (int64_t)count * share - r0;
     const int rows = left >> kRowsLog ? kRows : (int)left;
-    const int token0 = (int)(r0 / (uint32_t)share), skip = (int)(r0 - (uint32_t)token0 * (uint32_t)share);
+    const int token0 = grid.share.quotient(r0), skip = (int)(r0 - (uint32_t)(token0 * share));
     const float per_share = 1.0f / (float)share;
     auto token_of = [&](int r) { return (int)(((float)(skip + r) + 0.5f) * per_share); };
     const int before = len - count;                                     // position of new token 0
@@ -190,7 +214,7 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     const int32_t* table = a.kv.table + (int64_t)b * a.kv.width;
 
     const int tiles = span.tiles(kKeys);
-    const int per = max(chunk, (tiles + splits - 1) / splits);
+    const int per = max(grid.chunk, grid.splits.quotient(tiles + splits - 1));
     // Tiles [begin, end) of the list are this workgroup's; its group's t-th is begin + group + KG t.
     const int begin = min(tiles, split * per), end = min(tiles, begin + per);
     auto tiles_before = [&](int i) { return max(0, (i - begin - group + KG - 1) / KG); };      // of the group's, below i
@@ -204,6 +228,8 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     const Span mine = key_span(a, live ? p_first + past : -1);
     // Scores are compared before they are scaled, so the scale's sign goes into the queries (exact).
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+    uint32_t keep = a.scale == 0.0f ? 0u : ~0u;
+    asm("" : "+v"(keep));                         // one operation with the flip, not a selection after it
     const float scale = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f;
     // The wave's own tiles [w_begin, w_end): its rows see none of the others.
     // Every row sees all of a 32-key half that begins in [all_from, all_to],
@@ -229,19 +255,18 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         t = begin + group + KG * t;
         return (t < sink_tiles ? t : t + window_tile) * kKeys;
     };
-    auto look_up = [&](int t0) {
+    auto look_up = [&](int t0, auto&& meanwhile) {
         from = t0;
         const int base = base_of(min(t0 + lane, last - 1));
         int page[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = base + 16 * i;
-            page[i] = key < keys ? table[key >> a.kv.page_shift] : -1;
-        }
+        for (int i = 0; i < 4; ++i)
+            page[i] = table[min(base + 16 * i, keys - 1) >> a.kv.page_shift];       // keys > 0 where there is a tile
+        meanwhile();
         blocks = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const bool is = page[i] >= 0 && page[i] < a.kv.pages;
+            const bool is = base + 16 * i < keys && page[i] >= 0 && page[i] < a.kv.pages;
             blocks |= is ? 1 << i : 0;
             if (i == wave) {
                 const int key = base + 16 * i;
@@ -313,22 +338,20 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     auto k_read = [&](uint32_t at, int i) { return D == 96 ? (at ^ (32u * (i & 1))) + 64 * (i >> 1) : at ^ (32u * i); };
     auto v_read = [&](uint32_t at, int i) { return D == 96 ? at + 64 * i : at ^ (64u * i); };
 
-    if (first < last) look_up(first);
     // The wave's queries go through LDS as a key tile does (waves 0 and 1 of the
     // group to K of buffer 1, 2 and 3 to V of it, not in use yet): read straight
     // into the operand layout, every 32 bytes of a load would be another row's.
     // The rows' elements in global memory from the block's first token and head on:
-    auto element = [&](int r, int64_t stride) {
-        const int p = token_of(r);
-        return (int)(p * stride) + (skip + r - p * share) * D;
-    };
+    auto element = [&](int r, int64_t stride) { return token_of(r) * ((int)stride - share * D) + (skip + r) * D; };
     auto load_queries = [&] {
         const u4 rsrc = rsrc_words(a.q + (int64_t)(row_first + token0) * a.sq + (int64_t)kvh * share * D, kOOB);
         const uint32_t to = lds0 + 2 * kTileBytes + wave * 32 * D * 2;
 #pragma unroll
         for (int j = 0; j < 2 * kLoads; ++j) {
             const int c = 64 * j + lane, r = c / kC, chunk = k_place<D>(r, c - r * kC), in = 32 * wave + r;
-            lds_load16_at(rsrc, to + 1024 * j, in < rows ? (element(in, a.sq) + chunk * 8) * 2 : kOOB, 0);
+            int at = (element(in, a.sq) + chunk * 8) * 2;
+            asm("" : "+v"(at));                   // without a branch around it
+            lds_load16_at(rsrc, to + 1024 * j, in < rows ? at : kOOB, 0);
         }
     };
     u4 qf[D / 16];
@@ -470,10 +493,10 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     // V of tile t + 1 may begin.
     Place cur, next, after;                       // of tiles t, t + 1 and t + 2
     if (first < last) {
+        look_up(first, load_queries);
         cur = next = place(first);
         after = place(min(first + 1, last - 1));
         load(false, 0, next);
-        load_queries();
         load(true, 0, next);
     }
     auto advance = [&](int t) {
@@ -486,7 +509,7 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         }
         __syncthreads();
         if (t >= first && t + 2 < last) {
-            if (t + 2 - from == 64) look_up(t + 2);
+            if (t + 2 - from == 64) look_up(t + 2, [] {});
             after = place(t + 2);
         }
     };
@@ -498,10 +521,8 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     if (first < last) {
         wait_vmem_below<kLoads>();                // the queries; V of the first tile may still be on its way
 #pragma unroll
-        for (int i = 0; i < kK; ++i) {
-            qf[i] = lds_ld<u4>(k_read(k_at + 2 * kTileBytes + wave * 32 * D * 2, i)) ^ flip;
-            if (a.scale == 0.0f) qf[i] = u4{0, 0, 0, 0};
-        }
+        for (int i = 0; i < kK; ++i)
+            qf[i] = (lds_ld<u4>(k_read(k_at + 2 * kTileBytes + wave * 32 * D * 2, i)) ^ flip) & keep;
     }
     // (A group without tiles, or with one fewer, only takes part in the barriers.)
     int t = begin < end ? first - 1 : steps;
@@ -650,11 +671,13 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     const int64_t splits = max((int64_t)1, min(want, kAttnSplitRows / ((int64_t)a.tokens * a.q_heads)));
     const int chunk = (int)max((int64_t)1, (tiles + splits - 1) / splits);
     // A grid holds fewer than 2^32 threads; slots past it go into further launches.
-    const int64_t per_slot = a.kv_heads * splits, at_once = ((int64_t(1) << 32) / (64 * kRowWaves * KG) - 1) / per_slot;
+    const int64_t per_slot = a.kv_heads * splits, round = max((int64_t)1, kSplitTarget / per_slot), at_once = ((int64_t(1) << 32) / (64 * kRowWaves * KG) - 1) / per_slot;
     for (int64_t s = 0; s < slots; s += at_once) {
         const int64_t n = min(at_once, slots - s);
         hipLaunchKernelGGL((attention_prefill_kernel<T, D, KG>), dim3((unsigned)(n * per_slot)), dim3(64 * kRowWaves * KG), 0,
-                           stream, a, (int)slots, (int)s, (int)splits, chunk);
+                           stream, a,
+                           Grid{Divisor(a.kv_heads), Divisor(splits), Divisor(a.q_heads / a.kv_heads), (int)slots, (int)s,
+                                chunk, (int)round});
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
