@@ -10,9 +10,9 @@
 // head (row r is token r / share, head r % share of the group, so grouped heads
 // read each key tile once) and walks the key tiles that any of them sees.
 //  - Keys and values go from the pages straight into LDS, 64 keys a tile, two
-//    tiles deep, 16 bytes a lane, no registers between.  The 16-byte chunks of
-//    a row are permuted by the row on the way in, so that no LDS read below
-//    meets a bank twice (counted: none).  Rows past the sequence's end, and
+//    tiles deep, 16 bytes a lane, no registers between, laid out there
+//    (kQuad) so that no LDS read below meets a bank twice (counted: none) and
+//    nearly all of its address is the instruction's constant.  Rows past the sequence's end, and
 //    pages that are none, arrive as zeros.
 //  - A wave owns 32 rows.  S^T = K Q^T on 32 x 32 x 16 matrix instructions: a
 //    lane holds one query (column lane % 32) and 16 keys of every 32, the lane
@@ -50,21 +50,13 @@ constexpr int kRowWaves = 4, kRowsLog = 7, kRows = 1 << kRowsLog;
 // least kMinTiles tiles.
 constexpr int kSplitTarget = 256, kMinTiles = 4;
 
-// LDS position of 16-byte chunk c of row r (of a tile's rows of D/8 chunks).
-// K: 16 consecutive rows' same chunk lie in 16 different bank groups.
-template <int D>
-__device__ __forceinline__ int k_place(int r, int c) {
-    if constexpr (D == 64) return c ^ ((r >> 1) & 7);
-    if constexpr (D == 96) return c ^ ((r >> 2) & 3);
-    return c ^ (r & 15);
-}
-// V: 4 consecutive rows' same 64 bytes lie in different bank groups.
-template <int D>
-__device__ __forceinline__ int v_place(int r, int c) {
-    if constexpr (D == 64) return c ^ (((r >> 1) & 1) << 2);
-    if constexpr (D == 96) return c;
-    return c ^ ((r & 3) << 2);
-}
+// A tile lies in LDS as [row of 64 bytes' quads][its rows][64 bytes]: a load of
+// 64 lanes brings a quad of 16 rows, and a lane that reads another quad or
+// another row of the same residue only changes the instruction's offset.  Of a
+// row's four 16-byte chunks of a quad, chunk c of K (and of queries and outputs) is at
+// place c ^ k_turn(row), so that 16 consecutive rows' same chunk lie in 16 different bank groups.
+constexpr int kQuad = 64;
+__device__ __forceinline__ int k_turn(int row) { return (row >> 2) & 3; }
 
 typedef short s4v __attribute__((ext_vector_type(4)));
 
@@ -148,8 +140,8 @@ struct Grid {
 template <class T, int D, int KG>
 __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG == 1 ? 3 : 2) void attention_prefill_kernel(
     AttnArgs a, Grid grid) {
-    constexpr int kTileBytes = kKeys * D * 2, kC = D / 8;      // chunks of a row
-    constexpr int kLoads = D / 32;                       // 64-lane loads of a 16-row block
+    constexpr int kTileBytes = kKeys * D * 2;
+    constexpr int kLoads = D / 32;                       // quads of a row, 64-lane loads of a 16-row block
     __shared__ __align__(1024) unsigned char lds[KG][2][2][kTileBytes];         // [group][buffer][K, V]
     // Waves in KG groups: each group has all the rows, and every KG-th tile.
     const int lane = threadIdx.x & 63, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -287,28 +279,10 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         x.hi = __builtin_amdgcn_readlane(at_hi, t - from);
         return x;
     };
-    // Of a 16-row block's 16-byte chunks, load j takes 64 j + lane in LDS order.
-    // Load j's rows differ from load 0's in bits that the permutation moves
-    // through unchanged, so one register gives all (not at D = 96, where a load
-    // ends inside a row).
+    // Load j takes quad j of a 16-row block, 4 lanes a row.
     const uint32_t lds0 = lds_u32(&lds[group][0][0][0]);
-    auto source = [&](bool is_v, int j) {
-        const int c = 64 * j + lane, r = c / kC, at = c - r * kC;
-        return (uint32_t)(r * (D * 2) + (is_v ? v_place<D>(r, at) : k_place<D>(r, at)) * 16);
-    };
-    constexpr int kKept = D == 96 ? kLoads : 1;
-    uint32_t k_from[kKept], v_from[kKept];
-#pragma unroll
-    for (int j = 0; j < kKept; ++j) {
-        k_from[j] = source(false, j);
-        v_from[j] = source(true, j);
-    }
-    auto from_of = [&](bool is_v, int j) {
-        if constexpr (D == 96) return is_v ? v_from[j] : k_from[j];
-        const int r = 64 / kC * j;                // load j's first row
-        return is_v ? (v_from[0] ^ (uint32_t)(v_place<D>(r, 0) * 16)) + 1024 * j
-                    : (k_from[0] ^ (uint32_t)(k_place<D>(r, 0) * 16)) + 1024 * j;
-    };
+    const int load_row = lane >> 2, load_chunk = (lane & 3) ^ k_turn(load_row);
+    const uint32_t k_from = load_row * (D * 2) + load_chunk * 16, v_from = load_row * (D * 2) + (lane & 3) * 16;
     // The wave's loads of a tile of K or V, kLoads of them, one by one.
     struct Source { u4 rsrc; uint32_t to; };
     auto source_of = [&](bool is_v, int buf, const Place& x, bool any) {
@@ -316,11 +290,11 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         Source s;
         s.rsrc = rsrc_words(pool + (int64_t)((uint64_t)(uint32_t)x.lo | (uint64_t)(uint32_t)x.hi << 32),
                             any ? (x.blocks >> 4) * (D * 2) : 0);
-        s.to = lds0 + (2 * buf + is_v) * kTileBytes + wave * 16 * (D * 2);
+        s.to = lds0 + (2 * buf + is_v) * kTileBytes + wave * 16 * kQuad;
         return s;
     };
     auto load_piece = [&](bool is_v, const Source& s, int j) {
-        lds_load16_at(s.rsrc, s.to + 1024 * j, from_of(is_v, j), 0);
+        lds_load16_at(s.rsrc, s.to + j * kKeys * kQuad, is_v ? v_from : k_from, j * kQuad);
     };
     auto load = [&](bool is_v, int buf, const Place& x) {
         const Source s = source_of(is_v, buf, x, true);
@@ -328,15 +302,12 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         for (int n = 0; n < kLoads; ++n) load_piece(is_v, s, n);
     };
 
-    // Where this lane reads a tile: K row col, chunk 2 i + half; V rows
-    // 4 half + lane % 16 / 4 (+ 8, + 16 g), elements 32 i + 16 (col / 16) + 4 (lane % 4).
-    // The chunk's i enters as an exclusive or (at D = 96 in part as a sum).
-    const uint32_t k_at = lds0 + col * (D * 2) + k_place<D>(col, half) * 16;
-    const int v_row = 4 * half + ((lane & 15) >> 2);
-    const uint32_t v_at = lds0 + kTileBytes + v_row * (D * 2) +
-                          v_place<D>(v_row, 2 * (col >> 4) + ((lane & 3) >> 1)) * 16 + (lane & 1) * 8;
-    auto k_read = [&](uint32_t at, int i) { return D == 96 ? (at ^ (32u * (i & 1))) + 64 * (i >> 1) : at ^ (32u * i); };
-    auto v_read = [&](uint32_t at, int i) { return D == 96 ? at + 64 * i : at ^ (64u * i); };
+    // Where this lane reads a tile: K row col, chunk 2 i + half (places 0 or 1, 2 or 3
+    // of a quad by i's low bit, turned); V rows 4 half + lane % 16 / 4 (+ 8, + 16 g),
+    // elements 32 i + 16 (col / 16) + 4 (lane % 4).
+    const uint32_t k_at = lds0 + col * kQuad + (half ^ k_turn(col)) * 16;
+    const uint32_t v_at = lds0 + kTileBytes + (4 * half + ((lane & 15) >> 2)) * kQuad + 32 * (col >> 4) + (lane & 3) * 8;
+    auto k_read = [&](uint32_t at, int i, int rows_of) { return (at ^ (32u * (i & 1))) + (i >> 1) * rows_of * kQuad; };
 
     // The wave's queries go through LDS as a key tile does (waves 0 and 1 of the
     // group to K of buffer 1, 2 and 3 to V of it, not in use yet): read straight
@@ -348,8 +319,8 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         const uint32_t to = lds0 + 2 * kTileBytes + wave * 32 * D * 2;
 #pragma unroll
         for (int j = 0; j < 2 * kLoads; ++j) {
-            const int c = 64 * j + lane, r = c / kC, chunk = k_place<D>(r, c - r * kC), in = 32 * wave + r;
-            int at = (element(in, a.sq) + chunk * 8) * 2;
+            const int in = 32 * wave + 16 * (j & 1) + load_row;
+            int at = (element(in, a.sq) + load_chunk * 8) * 2 + (j >> 1) * kQuad;
             asm("" : "+v"(at));                   // without a branch around it
             lds_load16_at(rsrc, to + 1024 * j, in < rows ? at : kOOB, 0);
         }
@@ -372,7 +343,7 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     }
     auto read_k = [&](uint32_t off) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) kf[i] = lds_ld<u4>(k_read(k_at + off, i));
+        for (int i = 0; i < D / 16; ++i) kf[i] = lds_ld<u4>(k_read(k_at + off, i, kKeys));
     };
     auto score = [&](f16v& s) {
 #pragma unroll
@@ -383,6 +354,20 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     constexpr int kV = D / 32, kK = D / 16;       // matrix operands of 16 keys of V, of 32 keys of K
     auto add_value = [&](int n) {                 // n of the 2 kV operands of a half
         o[n % kV] = T::mfma32(vf[n / kV][n % kV], w[n / kV], o[n % kV]);
+    };
+    // Keeps the scores whose key is seen, `seen(e, c)` with element e's c (below).
+    // Four comparisons, then four selections: one right after the other would wait.
+    auto select = [&](f16v& s, auto&& seen) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            bool is[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) is[e] = seen(4 * g + e, 8 * g + e);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[4 * g + e] = is[e] ? s[4 * g + e] : -INFINITY;
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     // A half of the tile, from key `base` on: `cur` holds its scores, `nxt` takes the next half's.
     // The order of the code is the order of issue (the empty barriers hold the
@@ -395,20 +380,14 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         if (base > all_to || blocks_of != 3) {
             const int lim = mine.end - base - 4 * half;
             const int lims[2] = {blocks_of & 1 ? lim : -1, blocks_of & 2 ? lim : -1};
-#pragma unroll
-            for (int e = 0; e < 16; ++e) cur[e] = 8 * (e >> 2) + (e & 3) < lims[e >> 3] ? cur[e] : -INFINITY;
+            select(cur, [&](int e, int c) { return c < lims[e >> 3]; });
         }
         if (base < all_from && base > sinks - kKeys / 2) {
             const int lim = mine.start - base - 4 * half, sink = mine.sinks - base - 4 * half;
             if (base >= sinks) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) cur[e] = 8 * (e >> 2) + (e & 3) >= lim ? cur[e] : -INFINITY;
+                select(cur, [&](int, int c) { return c >= lim; });
             } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int c = 8 * (e >> 2) + (e & 3);
-                    cur[e] = c >= lim || c < sink ? cur[e] : -INFINITY;
-                }
+                select(cur, [&](int, int c) { return c >= lim || c < sink; });
             }
         }
         asm("" : "+v"(cur));      // one set of registers for both paths
@@ -462,10 +441,10 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
             } else {
                 nxt = T::mfma32(kf[k], qf[k], nxt);
                 const int g = k / kV, i = k % kV;                 // kK == 2 kV
-                const uint32_t at = v_read(v_at + v_cur, i) + g * 16 * D * 2;
-                const u2 x = lds_tr(at), y = lds_tr(at + 8 * D * 2);            // v_place repeats every 8 rows
+                const uint32_t at = v_at + v_cur + (i * kKeys + g * 16) * kQuad;
+                const u2 x = lds_tr(at), y = lds_tr(at + 8 * kQuad);
                 vf[g][i] = u4{x[0], x[1], y[0], y[1]};
-                kf[k] = lds_ld<u4>(k_read(k_at + k_next, k));
+                kf[k] = lds_ld<u4>(k_read(k_at + k_next, k, kKeys));
             }
 #pragma unroll
             for (int e = n * 8 / kRest * 2; e < (n + 1) * 8 / kRest * 2; ++e) ex[e] = exp2_fast(ex[e]);
@@ -517,12 +496,12 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         if (t + 2 < last) load(false, (t - first) & 1, after);
         if (t >= first && t + 1 < last) load(true, (t + 1 - first) & 1, next);
     };
-    constexpr uint32_t kHalf = kKeys / 2 * D * 2;
+    constexpr uint32_t kHalf = kKeys / 2 * kQuad;
     if (first < last) {
         wait_vmem_below<kLoads>();                // the queries; V of the first tile may still be on its way
 #pragma unroll
         for (int i = 0; i < kK; ++i)
-            qf[i] = (lds_ld<u4>(k_read(k_at + 2 * kTileBytes + wave * 32 * D * 2, i)) ^ flip) & keep;
+            qf[i] = (lds_ld<u4>(k_read(k_at + 2 * kTileBytes + wave * 32 * D * 2, i, 32)) ^ flip) & keep;
     }
     // (A group without tiles, or with one fewer, only takes part in the barriers.)
     int t = begin < end ? first - 1 : steps;
@@ -644,15 +623,15 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     for (int i = 0; i < kV; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            *(LdsPair)(size_t)(out + col * (D * 2) + k_place<D>(col, 4 * i + e) * 16 + half * 8) =
+            *(LdsPair)(size_t)(out + (32 * i + col) * kQuad + (e ^ k_turn(col)) * 16 + half * 8) =
                 u2{T::pack(o[i][4 * e] * inv, o[i][4 * e + 1] * inv), T::pack(o[i][4 * e + 2] * inv, o[i][4 * e + 3] * inv)};
     asm volatile("" ::: "memory");                // a wave's LDS accesses are served in their order
     uint16_t* const to = a.o + (int64_t)(row_first + token0) * a.so + (int64_t)kvh * share * D;
 #pragma unroll
     for (int j = 0; j < 2 * kLoads; ++j) {
-        const int c = 64 * j + lane, r = c / kC, chunk = k_place<D>(r, c - r * kC), in = 32 * wave + r;
+        const int in = 32 * wave + 16 * (j & 1) + load_row;
         const u4 x = lds_ld<u4>(out + 1024 * j + lane * 16);
-        if (in < rows) *reinterpret_cast<u4*>(to + element(in, a.so) + chunk * 8) = x;
+        if (in < rows) *reinterpret_cast<u4*>(to + element(in, a.so) + load_chunk * 8 + (j >> 1) * (kQuad / 2)) = x;
     }
 }
 
