@@ -668,13 +668,19 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
 // 24576: 73 us in one group, 55 in two; 1024 tokens of 32 heads 28.9 and 25.9).
 // With more, two workgroups of one group share a CU and hide each other's
 // beginnings and ends (8192 windowed tokens: 427 us in one group, 476 in two;
-// 2048 tokens of 32 heads 56.9 and 58.3).
+// 1536 tokens behind 800 50.3 and 52.7, in a window of 1024 27.7 and 30.4) - unless
+// the blocks' lengths run from one tile to all of them, as a whole prompt's do: the longest
+// is then alone on its CU for most of its time (1100 tokens of 32 heads on 8
+// 26.1 us in one group, 23.7 in two; 1536 33.3 and 30.8; 1900 44.2 and 41.3; 1280 behind 320 34.3
+// and 33.1; head size 64, 1900 tokens 33.6 and 28.6), up to nearly two rounds (2048 tokens 48.6 and 50.2).
 template <class T, int D>
 hipError_t launch_groups(const AttnArgs& a, hipStream_t stream) {
     const int64_t rows = (int64_t)a.tokens * (a.q_heads / a.kv_heads);
     const int64_t blocks = a.kv.seqs == 1 ? (rows + kRows - 1) / kRows : slots_of(a);
-    if (blocks * a.kv_heads <= kSplitTarget) return launch<T, D, 2>(a, stream);
-    return launch<T, D, 1>(a, stream);
+    const bool uneven = a.kv.seqs == 1 && 4 * (int64_t)a.max_len <= 5 * (int64_t)a.tokens &&
+                        (a.window == 0 || a.window >= a.tokens);
+    const int64_t most = uneven ? 2 * kSplitTarget - kSplitTarget / 8 : kSplitTarget;
+    return blocks * a.kv_heads <= most ? launch<T, D, 2>(a, stream) : launch<T, D, 1>(a, stream);
 }
 
 template <class T>
