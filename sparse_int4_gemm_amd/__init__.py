@@ -238,16 +238,16 @@ def workspace_attention(tokens: int, seqs: int, q_heads: int, kv_heads: int, hea
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _attention_buffers(q, seqs, kpool, ws, out, stream):
+def _attention_buffers(q, lens, kpool, ws, out, stream):
     """Output and workspace of a call that was not given them, made on the
     stream that the call runs on (so that it, not the current one, owns them)."""
-    if out is not None and ws is not None:
-        return out, ws
+    if q.dim() != 3 or kpool.dim() != 4:
+        raise ValueError("q must be [tokens, q_heads, head_dim], the pools [pages, kv_heads, page_size, head_dim]")
     with torch.cuda.stream(stream):            # None: no change
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if ws is None:
-            ws = workspace_attention(q.shape[0], seqs, q.shape[1], kpool.shape[1], kpool.shape[3], device=q.device)
+            ws = workspace_attention(q.shape[0], lens.shape[0], q.shape[1], kpool.shape[1], kpool.shape[3], device=q.device)
     return out, ws
 
 
@@ -263,12 +263,9 @@ def attention_decode(q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor, 
     ones; max_len: the longest length expected (None: the table's capacity),
     which only plans how the work is split; scale: 1 / sqrt(head_dim) if None;
     lse: float32 [seqs, q_heads], receives the log of the softmax sums."""
-    if q.dim() != 3 or kpool.dim() != 4:
-        raise ValueError("q must be [seqs, q_heads, head_dim], the pools [pages, kv_heads, page_size, head_dim]")
-    out, ws = _attention_buffers(q, lens.shape[0], kpool, ws, out, stream)
-    slim_attention_decode(q, out, kpool, vpool, table, lens, ws,
-                          table.shape[1] * kpool.shape[2] if max_len is None else max_len, window, sinks,
-                          q.shape[2] ** -0.5 if scale is None else scale, lse, stream=stream)
+    if out is None or ws is None:
+        out, ws = _attention_buffers(q, lens, kpool, ws, out, stream)
+    slim_attention_decode(q, out, kpool, vpool, table, lens, ws, max_len, window, sinks, scale, lse, stream)
     return out
 
 
@@ -280,10 +277,7 @@ def attention_prefill(q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor,
     cache (whole prompts, or chunks behind what is cached): q [tokens, q_heads,
     head_dim], starts int32 [seqs + 1] as for kv_append, the tokens' keys and
     values already appended.  Other arguments as attention_decode."""
-    if q.dim() != 3 or kpool.dim() != 4:
-        raise ValueError("q must be [tokens, q_heads, head_dim], the pools [pages, kv_heads, page_size, head_dim]")
-    out, ws = _attention_buffers(q, lens.shape[0], kpool, ws, out, stream)
-    slim_attention_prefill(q, out, kpool, vpool, table, lens, starts, ws,
-                           table.shape[1] * kpool.shape[2] if max_len is None else max_len, window, sinks,
-                           q.shape[2] ** -0.5 if scale is None else scale, lse, stream=stream)
+    if out is None or ws is None:
+        out, ws = _attention_buffers(q, lens, kpool, ws, out, stream)
+    slim_attention_prefill(q, out, kpool, vpool, table, lens, starts, ws, max_len, window, sinks, scale, lse, stream)
     return out

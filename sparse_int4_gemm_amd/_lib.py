@@ -299,39 +299,47 @@ _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+# (Each attribute of a tensor costs some 50 ns, a call's checks as much as its
+# launch: every one is read once.)
 def _rows(name, t, heads, dim, dtype, device):
-    """(pointer, row stride) of a [tokens, heads, dim] tensor whose rows are
-    dense; the rows themselves may lie apart (a slice of a joint array)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    """(pointer, row stride, tokens, heads) of a [tokens, heads, dim] tensor whose
+    rows are dense; the rows themselves may lie apart (a slice of a joint
+    array).  heads None: any number."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {dim}], got {tuple(shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
+    tokens, heads, _ = shape
     sr, sh, sd = t.stride()
     if sd != 1 or (sh != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), sr if t.shape[0] > 1 else heads * dim
+    return t.data_ptr(), sr if tokens > 1 else heads * dim, tokens, heads
 
 
 def _ints(name, t, device, dims):
-    if t.dtype is not torch.int32 or t.dim() != dims or not t.is_contiguous() or t.device != device:
+    """Pointer and shape."""
+    shape = t.shape
+    if t.dtype is not torch.int32 or len(shape) != dims or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dims}-dimensional int32 tensor on {device}")
-    return t.data_ptr()
+    return t.data_ptr(), shape
 
 
 def _pools(kpool, vpool, dims):
-    """Device and shape of a pair of pools."""
-    device, shape = kpool.device, kpool.shape
-    if device.type != "cuda":
+    """Device, shape, type and pointers of a pair of pools."""
+    if not kpool.is_cuda:
         raise ValueError("tensors must live on the GPU (a ROCm 'cuda' device)")
-    if kpool.dtype not in _DTYPES:
+    device, shape, dtype = kpool.device, kpool.shape, kpool.dtype
+    if dtype not in _DTYPES:
         raise TypeError("the pools must be float16 or bfloat16")
-    if len(shape) != dims or shape != vpool.shape or kpool.dtype is not vpool.dtype or device != vpool.device:
-        raise ValueError(f"the pools must be two {dims}-dimensional tensors of one shape, type and device")
+    if len(shape) not in dims or shape != vpool.shape or dtype is not vpool.dtype or device != vpool.device:
+        raise ValueError(f"the pools must be two {' or '.join(map(str, dims))}-dimensional tensors of one shape, type "
+                         "and device")
     if not (kpool.is_contiguous() and vpool.is_contiguous()):
         raise ValueError("the pools must be contiguous")
-    return device, shape
+    return device, shape, dtype, kpool.data_ptr(), vpool.data_ptr()
 
 
 def _stream_on(stream, device):
@@ -345,45 +353,42 @@ def _stream_on(stream, device):
 
 
 def _batch(table, lens, starts, tokens, device):
-    p_table, p_lens = _ints("table", table, device, 2), _ints("lens", lens, device, 1)
-    seqs = lens.shape[0]
-    if table.shape[0] != seqs:
-        raise ValueError(f"table has {table.shape[0]} rows for {seqs} sequences")
+    """Pointers of table, lens and starts, the number of sequences and the table's width."""
+    p_table, (rows, width) = _ints("table", table, device, 2)
+    p_lens, (seqs,) = _ints("lens", lens, device, 1)
+    if rows != seqs:
+        raise ValueError(f"table has {rows} rows for {seqs} sequences")
     if starts is None:
         if tokens != seqs:
             raise ValueError(f"{tokens} new tokens for {seqs} sequences without starts")
-        return p_table, p_lens, None, seqs
-    p_starts = _ints("starts", starts, device, 1)
-    if starts.shape[0] != seqs + 1:
-        raise ValueError(f"starts must hold {seqs + 1} values, got {starts.shape[0]}")
-    return p_table, p_lens, p_starts, seqs
+        return p_table, p_lens, None, seqs, width
+    p_starts, (bounds,) = _ints("starts", starts, device, 1)
+    if bounds != seqs + 1:
+        raise ValueError(f"starts must hold {seqs + 1} values, got {bounds}")
+    return p_table, p_lens, p_starts, seqs, width
 
 
 def slim_kv_append(K, V, kpool, vpool, table, lens, starts=None, stream=None) -> None:
     """K, V [tokens, kv_heads, head_dim] to the pages of their positions; pools [pages, kv_heads, page_size, head_dim]."""
-    dev, (pages, heads, page, dim) = _pools(kpool, vpool, 4)
-    pk, sk = _rows("K", K, heads, dim, kpool.dtype, dev)
-    pv, sv = _rows("V", V, heads, dim, kpool.dtype, dev)
-    tokens = K.shape[0]
-    if V.shape[0] != tokens:
-        raise ValueError(f"K has {tokens} rows and V {V.shape[0]}")
-    pt, pl, ps, seqs = _batch(table, lens, starts, tokens, dev)
-    _check(load().slim_kv_append(pk, sk, pv, sv, tokens, seqs, heads, dim, _DTYPES[kpool.dtype], pt, table.shape[1], pl,
-                                 ps, kpool.data_ptr(), vpool.data_ptr(), pages, page, _stream_on(stream, dev)))
+    dev, (pages, heads, page, dim), dtype, pkp, pvp = _pools(kpool, vpool, (4,))
+    pk, sk, tokens, _ = _rows("K", K, heads, dim, dtype, dev)
+    pv, sv, v_tokens, _ = _rows("V", V, heads, dim, dtype, dev)
+    if v_tokens != tokens:
+        raise ValueError(f"K has {tokens} rows and V {v_tokens}")
+    pt, pl, ps, seqs, width = _batch(table, lens, starts, tokens, dev)
+    _check(load().slim_kv_append(pk, sk, pv, sv, tokens, seqs, heads, dim, _DTYPES[dtype], pt, width, pl, ps, pkp, pvp,
+                                 pages, page, _stream_on(stream, dev)))
 
 
 def slim_kv_copy_pages(kpool, vpool, src, dst, stream=None) -> None:
     """Pages src[i] to dst[i] of every layer; pools [layers, pages, ...] or one layer's [pages, kv_heads, page_size, head_dim]."""
-    dev, shape = _pools(kpool, vpool, kpool.dim())
-    if len(shape) not in (4, 5):
-        raise ValueError("the pools must be [layers, pages, kv_heads, page_size, head_dim] or one layer of it")
+    dev, shape, _, pkp, pvp = _pools(kpool, vpool, (4, 5))
     layers = shape[0] if len(shape) == 5 else 1
     pages, heads, page, dim = shape[-4:]
-    ps, pd = _ints("src", src, dev, 1), _ints("dst", dst, dev, 1)
-    if src.shape != dst.shape:
-        raise ValueError(f"{src.shape[0]} sources and {dst.shape[0]} destinations")
-    _check(load().slim_kv_copy_pages(kpool.data_ptr(), vpool.data_ptr(), layers, pages,
-                                     heads * page * dim * kpool.element_size(), ps, pd, src.shape[0],
+    (ps, (count,)), (pd, (to,)) = _ints("src", src, dev, 1), _ints("dst", dst, dev, 1)
+    if count != to:
+        raise ValueError(f"{count} sources and {to} destinations")
+    _check(load().slim_kv_copy_pages(pkp, pvp, layers, pages, heads * page * dim * 2, ps, pd, count,
                                      _stream_on(stream, dev)))
 
 
@@ -391,15 +396,14 @@ def slim_attention_workspace_bytes(tokens: int, seqs: int, q_heads: int, kv_head
     return load().slim_attention_workspace_bytes(tokens, seqs, q_heads, kv_heads, head_dim)
 
 
-def _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace):
-    dev, (pages, kv_heads, page, dim) = _pools(kpool, vpool, 4)
-    if Q.dim() != 3:
-        raise ValueError(f"Q must be [tokens, q_heads, {dim}], got {tuple(Q.shape)}")
-    tokens, q_heads = Q.shape[0], Q.shape[1]
-    pq, sq = _rows("Q", Q, q_heads, dim, kpool.dtype, dev)
-    po, so = _rows("O", O, q_heads, dim, kpool.dtype, dev)
-    if O.shape[0] != tokens:
-        raise ValueError(f"Q has {tokens} rows and O {O.shape[0]}")
+def _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace, max_len, window, sinks, scale, stream):
+    """What both attention calls pass on: before seqs' place, from it to lens',
+    and after.  max_len None: the table's capacity; scale None: 1 / sqrt(head_dim)."""
+    dev, (pages, kv_heads, page, dim), dtype, pk, pv = _pools(kpool, vpool, (4,))
+    pq, sq, tokens, q_heads = _rows("Q", Q, None, dim, dtype, dev)
+    po, so, o_tokens, _ = _rows("O", O, q_heads, dim, dtype, dev)
+    if o_tokens != tokens:
+        raise ValueError(f"Q has {tokens} rows and O {o_tokens}")
     p_lse = None
     if lse is not None:
         if lse.dtype != torch.float32 or lse.shape != (tokens, q_heads) or not lse.is_contiguous() or lse.device != dev:
@@ -407,27 +411,26 @@ def _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace):
         p_lse = lse.data_ptr()
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"the workspace must be a contiguous tensor on {dev}")
-    pt, pl, ps, seqs = _batch(table, lens, starts, tokens, dev)
-    return (dev, pq, sq, po, so, p_lse, tokens, seqs, q_heads, kv_heads, dim, pages, page, pt, pl, ps,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    pt, pl, ps, seqs, width = _batch(table, lens, starts, tokens, dev)
+    if max_len is None:
+        max_len = width * page
+    if scale is None:
+        scale = dim ** -0.5
+    return ((pq, sq, po, so, p_lse), tokens, (seqs, q_heads, kv_heads, dim, _DTYPES[dtype], pk, pv, pages, page, pt, width,
+            pl), ps, (max_len, window, sinks, scale, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev)))
 
 
 def slim_attention_decode(Q, O, kpool, vpool, table, lens, workspace, max_len: int, window: int = 0, sinks: int = 0,
                           scale: float = 1.0, lse=None, stream=None) -> None:
     """Attention of one new token per sequence: Q, O [seqs, q_heads, head_dim]."""
-    (dev, pq, sq, po, so, p_lse, _, seqs, q_heads, kv_heads, dim, pages, page, pt, pl, _, ws,
-     ws_bytes) = _attention_args(Q, O, lse, kpool, vpool, table, lens, None, workspace)
-    _check(load().slim_attention_decode(pq, sq, po, so, p_lse, seqs, q_heads, kv_heads, dim, _DTYPES[kpool.dtype],
-                                        kpool.data_ptr(), vpool.data_ptr(), pages, page, pt, table.shape[1], pl, max_len,
-                                        window, sinks, scale, ws, ws_bytes, _stream_on(stream, dev)))
+    rows, _, cache, _, rest = _attention_args(Q, O, lse, kpool, vpool, table, lens, None, workspace, max_len, window,
+                                              sinks, scale, stream)
+    _check(load().slim_attention_decode(*rows, *cache, *rest))
 
 
 def slim_attention_prefill(Q, O, kpool, vpool, table, lens, starts, workspace, max_len: int, window: int = 0,
                            sinks: int = 0, scale: float = 1.0, lse=None, stream=None) -> None:
     """Attention of any number of new tokens per sequence: Q, O [tokens, q_heads, head_dim]."""
-    (dev, pq, sq, po, so, p_lse, tokens, seqs, q_heads, kv_heads, dim, pages, page, pt, pl, ps, ws,
-     ws_bytes) = _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace)
-    _check(load().slim_attention_prefill(pq, sq, po, so, p_lse, tokens, seqs, q_heads, kv_heads, dim,
-                                         _DTYPES[kpool.dtype], kpool.data_ptr(), vpool.data_ptr(), pages, page, pt,
-                                         table.shape[1], pl, ps, max_len, window, sinks, scale, ws, ws_bytes,
-                                         _stream_on(stream, dev)))
+    rows, tokens, cache, ps, rest = _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace, max_len,
+                                                    window, sinks, scale, stream)
+    _check(load().slim_attention_prefill(*rows, tokens, *cache, ps, *rest))
