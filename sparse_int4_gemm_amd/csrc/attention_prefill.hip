@@ -12,8 +12,8 @@
 //  - Keys and values go from the pages straight into LDS, 64 keys a tile, two
 //    tiles deep, 16 bytes a lane, no registers between, laid out there
 //    (kQuad) so that no LDS read below meets a bank twice (counted: none) and
-//    nearly all of its address is the instruction's constant.  Rows past the sequence's end, and
-//    pages that are none, arrive as zeros.
+//    nearly all of its address is the instruction's constant.  Rows past the
+//    sequence's end, and pages that are none, arrive as zeros.
 //  - A wave owns 32 rows.  S^T = K Q^T on 32 x 32 x 16 matrix instructions: a
 //    lane holds one query (column lane % 32) and 16 keys of every 32, the lane
 //    32 away the other 16, so a row's maximum is 8 instructions and an exchange.
@@ -34,8 +34,8 @@
 //    wave whose output is not finite is computed again key by key (plain_row),
 //    which gives only the rows that do see such a value theirs.
 // Measured: 8192 tokens, window 4096, 32 query heads on 8 key heads of 128,
-// bf16: 411 us, 1.0 PFLOP/s (a library product of 8192^3: 1.45); matrix unit
-// busy 51%, vector unit 69% of the cycles, at 2.0 GHz (power).
+// bf16: 391 us, 1.05 PFLOP/s (a library product of 8192^3: 1.45); matrix unit
+// busy 57%, vector unit 55% of the cycles, at 2.0 GHz (power).
 #include "attention_device.hpp"
 
 namespace slim {
