@@ -26,9 +26,9 @@
 //    they would be waited for behind the keys in flight (131071 keys: 128 us
 //    against 124).
 // Measured (a 1 GiB copy moves 4.8 TB/s, read and write together): 64 sequences
-// of 4096 tokens, 32 heads of 128: 720 us, 6.0 TB/s; of 1 to 4096: 436 us, 4.9
-// TB/s (the last long sequences run alone); one of 131071, 8 key heads: 96 us,
-// 5.6 TB/s; one of 33: 5 us, launch and the chain lens -> table -> keys -> join.
+// of 4096 tokens, 32 heads of 128: 720 us, 6.0 TB/s; of 1 to 4096: 365 us, 5.9
+// TB/s (longest first; the last long ones alone: 436); one of 131071, 8 key heads:
+// 96 us, 5.6 TB/s; one of 33: 5 us, launch and the chain lens -> table -> keys -> join.
 #include "attention_device.hpp"
 
 namespace slim {
@@ -67,17 +67,49 @@ __device__ __forceinline__ void load_tile(Tile<D>& x, const AttnArgs& a, int kvh
     }
 }
 
+// The sequence in place `rank` when those of every 64 are taken longest first,
+// in sixteen classes of length up to `most` (a class's in their own order): a
+// load, and a ballot for each class down to the answer's.
+__device__ __forceinline__ int longest_first(const PagedKV& kv, int rank, int most) {
+    const int lane = threadIdx.x & 63, base = rank & ~63;
+    const int len = seq_len(kv, min(base + lane, kv.seqs - 1));
+    const int of = min((int)((float)len * (16.0f / (float)most)), 15);
+    int left = rank & 63;
+    uint64_t found = 0;
+    for (int c = 15; c >= 0; --c) {
+        found = __ballot(base + lane < kv.seqs && of == c);
+        const int n = __builtin_popcountll(found);
+        if (left < n) break;
+        left -= n;
+    }
+    // The left-th of the class.
+    const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(found >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)found, 0));
+    const uint64_t at = __ballot((found >> lane & 1) && before == left);
+    return base + (at == 0 ? 0 : __builtin_ctzll(at));
+}
+
 template <class T, int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnArgs a, int splits, int chunk,
-                                                                          int groups) {
+                                                                          int groups, int sort_most) {
     constexpr int VE = D / 16;
     __shared__ float o_join[kWaves][16][D + 4];
     __shared__ float m_join[kWaves][16], l_join[kWaves][16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int split = blockIdx.x % splits, b = blockIdx.x / splits;
-    const int kvh = blockIdx.y / groups, share = a.q_heads / a.kv_heads;
-    const int h0 = kvh * share + (blockIdx.y - kvh * groups) * 16;             // this workgroup's query heads
+    int split, b, unit;                  // unit: key head and group of 16 query heads
+    if (sort_most) {
+        // Longest sequences first, with all their heads (not split: see launch).
+        const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x, rank = id / gridDim.y;
+        unit = (int)(id - rank * gridDim.y);
+        split = 0;
+        b = __builtin_amdgcn_readfirstlane(longest_first(a.kv, (int)rank, sort_most));
+    } else {
+        split = blockIdx.x % splits;
+        b = blockIdx.x / splits;
+        unit = blockIdx.y;
+    }
+    const int kvh = unit / groups, share = a.q_heads / a.kv_heads;
+    const int h0 = kvh * share + (unit - kvh * groups) * 16;                   // this workgroup's query heads
     const int heads = min(16, (kvh + 1) * share - h0);
 
     const Span span = key_span(a, seq_len(a.kv, b) - 1);
@@ -244,7 +276,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
 // workgroups 100 us, 1024 103, 2048 111; 64 sequences of up to 900 at head size
 // 256: 61 us unsplit, 87 in two), fewer tiles too (4 sequences of up to 8000, 8 key heads:
 // 16 tiles 20.7 us, 8 tiles 24.1).
-constexpr int kSplitTarget = 512, kMinTiles = 16;
+constexpr int kSplitTarget = 512, kMinTiles = 16, kSortFrom = 512;
 
 template <class T, int D>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
@@ -257,7 +289,15 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     const int splits = (int)max((int64_t)1, min(want, kAttnSplitRows / ((int64_t)a.tokens * a.q_heads)));
     const int chunk = max(kWaves, (tiles + splits - 1) / splits);
     dim3 grid((unsigned)(a.tokens * splits), (unsigned)(a.kv_heads * groups));
-    hipLaunchKernelGGL((attention_decode_kernel<T, D>), grid, dim3(64 * kWaves), 0, stream, a, splits, chunk, groups);
+    // More than one round of workgroups, so that none is split: the longest
+    // sequences first, or the last ones to begin end alone (64 sequences of 1 to
+    // 4096, 32 key heads: 436 us in their order, 365 so; 128 of up to 8000, 8 key
+    // heads 426 and 377; 64 of up to 900 at head size 256 207 and 170).  Not for
+    // short ones, where finding a place costs more (512 of up to 100: 40.3 and
+    // 45.6; 256 of up to 250 33.8 and 35.4, of up to 500 58.9 and 59.3).
+    const int sort_most = units > kSplitTarget && most >= kSortFrom ? (int)most : 0;
+    hipLaunchKernelGGL((attention_decode_kernel<T, D>), grid, dim3(64 * kWaves), 0, stream, a, splits, chunk, groups,
+                       sort_most);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || splits == 1 ? e : launch_attention_join(a, splits, stream);
 }
