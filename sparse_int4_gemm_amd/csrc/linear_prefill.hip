@@ -192,14 +192,15 @@ __global__ __launch_bounds__(kMThreads) void prefill_main_kernel(LinearArgs a, P
                   : lane < 32 ? (int)((lane >> 1) * 16 * (K / kGroup) * 2 + 16 * (lane & 1))
                               : kOOB;
     // (The lambdas below are forced inline: every load index and stage must be
-    // a compile-time constant where it is used.)
+    // a compile-time constant where it is used.  The descriptors do not all fit the scalar registers:
+    // the loads wait for one that has just come back.)
     auto dma = [&](unsigned char* st, int ch, int i) __attribute__((always_inline)) {   // load i of chunk ch into st
         ch = c0 + (ch < nchunks ? ch : nchunks - 1);       // past the end: a repeat of the last chunk
-        if (i < 4)         lds_load16(rx, st + kSXOff + (4 * wave + i) * 1024, dxo[i], ch * kXLRow);
-        else if (i == 4)   lds_load16(rl, st + kSLOff + wave * 1024, dlo, ch * kXLRow);
-        else if (i == 5)   lds_load16(rv, st + kSVOff + wave * 1024, dvo, ch * 512);
-        else if (aux_meta) lds_load16(rm, st + kSMOff + wave * 1024, dao, ch * 256);
-        else               lds_load16(rs, st + kSSOff, dao, ch * 32);
+        if (i < 4)         lds_load16<4>(rx, st + kSXOff + (4 * wave + i) * 1024, dxo[i], ch * kXLRow);
+        else if (i == 4)   lds_load16<4>(rl, st + kSLOff + wave * 1024, dlo, ch * kXLRow);
+        else if (i == 5)   lds_load16<4>(rv, st + kSVOff + wave * 1024, dvo, ch * 512);
+        else if (aux_meta) lds_load16<4>(rm, st + kSMOff + wave * 1024, dao, ch * 256);
+        else               lds_load16<4>(rs, st + kSSOff, dao, ch * 32);
     };
 
     f4 acc[4][4];

@@ -110,12 +110,26 @@ __device__ __forceinline__ h8 buffer_load_h8(__amdgpu_buffer_rsrc_t r, int voff)
 // Written as asm: the compiler cannot tell which LDS bytes such a load writes
 // and would wait for every load in flight before any LDS read; callers order
 // them with wait_vmem_below.  No register outputs.
-__device__ __forceinline__ void lds_load16(u4 rsrc, const unsigned char* lds, int voff, int soff) {
-    const uint32_t l = (uint32_t)(size_t)(const __attribute__((address_space(3))) unsigned char*)lds;
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+//
+// The compiler keeps the machine's wait states between instructions that it
+// issues itself, but not before one inside an asm block.  Two concern this
+// load: one between the write of M0 and the load, and five between a vector
+// instruction that writes a scalar register (v_readfirstlane, or v_readlane
+// where a spilled one comes back) and the load that reads it.  kStates are spent
+// here, behind the write of M0 (itself a state): 1 for a kernel whose
+// descriptors stay in scalar registers, 4 (five in all) for one that spills
+// them.  The assembly of every source is held to both (test_lds_load_waits.py).
+template <int kStates = 1>
+__device__ __forceinline__ void lds_load16_to(u4 rsrc, uint32_t lds, int voff, int soff) {
+    static_assert(kStates >= 1 && kStates <= 16, "s_nop's range");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(l)), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc), "s"(soff), "i"(kStates - 1)
                  : "memory", "m0");
+}
+template <int kStates = 1>
+__device__ __forceinline__ void lds_load16(u4 rsrc, const unsigned char* lds, int voff, int soff) {
+    lds_load16_to<kStates>(rsrc, (uint32_t)(size_t)(const __attribute__((address_space(3))) unsigned char*)lds, voff, soff);
 }
 
 // LDS byte addresses as 32-bit integers: the address of a __shared__ object,
@@ -130,10 +144,7 @@ __device__ __forceinline__ T lds_ld(uint32_t a) {
     return *(const __attribute__((address_space(3))) T*)(size_t)a;
 }
 __device__ __forceinline__ void lds_load16_at(u4 rsrc, uint32_t lds, int voff, int soff) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory", "m0");
+    lds_load16_to(rsrc, lds, voff, soff);
 }
 
 // Raw buffer descriptor words (gfx9 family) over [base, base + bytes); see make_rsrc.
