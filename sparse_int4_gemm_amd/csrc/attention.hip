@@ -25,6 +25,9 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a, in
     __shared__ float part_sum[kGroups];
     __shared__ float red[kThreads / 64];
     const int64_t row = blockIdx.x;
+    const int token = (int)(blockIdx.x / (uint32_t)a.q_heads);
+    // Rows of no sequence have no partial results, and their outputs are not this call's.
+    if (a.kv.starts && (token < a.kv.starts[0] || token >= a.kv.starts[a.kv.seqs])) return;
     const Partials parts(a, D, splits);
     const float* ml = parts.ml + 2 * row * splits;
     if (ml[1] == kWhole) return;
@@ -58,8 +61,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a, in
             acc += *reinterpret_cast<const f4*>(&part[i][c]);
             sum += part_sum[i];
         }
-        const int64_t token = row / a.q_heads;
-        store_row4<T>(a, token, (int)(row - token * a.q_heads), D, d, acc, top, sum);
+        store_row4<T>(a, token, (int)blockIdx.x - token * a.q_heads, D, d, acc, top, sum);
     }
 }
 

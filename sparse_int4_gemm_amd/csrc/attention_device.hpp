@@ -124,7 +124,7 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, int64_t token, int
 
 // Partial results of rows whose keys are split over workgroups: for each row
 // (token * q_heads + head) and split the unscaled fp32 output, its maximum (in
-// units of log2) and sum.  Every split of a row is marked, also one without
+// units of log2) and sum.  Every split of a sequence's row is marked, also one without
 // keys (sum 0, no output stored), so attention_join_kernel needs no knowledge of
 // how the row was cut; a row that needed no join is marked kWhole in its split 0.
 constexpr float kWhole = -1.0f;
