@@ -18,7 +18,9 @@
 //    per operand register: V is never transposed through LDS.
 //  - Weights enter the product as two halves (high and low part of the fp32
 //    value): the matrix unit idles anyway, and the result then keeps fp32
-//    weights' accuracy.
+//    weights' accuracy.  An infinite value meets a low half of 0 or of the other
+//    sign there: rows that are not finite at the end are computed again, each
+//    weight whole (plain_row).
 //  - A sequence's tiles are cut into chunks, one workgroup each; its 4 waves
 //    take every fourth tile and join through LDS; the chunks of a row are joined
 //    by attention_join_kernel.
@@ -94,6 +96,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
     constexpr int VE = D / 16;
     __shared__ float o_join[kWaves][16][D + 4];
     __shared__ float m_join[kWaves][16], l_join[kWaves][16];
+    __shared__ uint32_t bad_join[kWaves];        // a bit for each row that is not finite
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
     int split, b, unit;                  // unit: key head and group of 16 query heads
@@ -246,9 +249,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
 #pragma unroll
             for (int e = 0; e < VE; ++e) o_join[wave][c][VE * (4 * g + r) + e] = o[e][r];
     }
+    f4 probe = f4{0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < VE; ++e) probe += o[e] * 0.0f;
+    const uint64_t odd = __ballot(c < heads && !(probe[0] + probe[1] + probe[2] + probe[3] == 0.0f));
+    if (lane == 0) bad_join[wave] = (uint32_t)(odd | odd >> 16 | odd >> 32 | odd >> 48) & 0xFFFFu;
     __syncthreads();
+    static_assert(kWaves == 4, "the waves' rows below");
+    const uint32_t bad = __builtin_amdgcn_readfirstlane(bad_join[0] | bad_join[1] | bad_join[2] | bad_join[3]);
     for (int at = threadIdx.x; at < heads * (D / 4); at += 64 * kWaves) {
         const int r = at / (D / 4), d = (at - r * (D / 4)) * 4;
+        if (bad >> r & 1) continue;
         float top = m_join[0][r];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) top = fmaxf(top, m_join[w][r]);
@@ -268,6 +279,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
             parts.put4(row0 + r, split, d, acc);
             if (d == 0) parts.mark(row0 + r, split, top, sum);
         }
+    }
+    for (int r = wave; r < heads; r += kWaves) {
+        if (!(bad >> r & 1)) continue;
+        float x[4], top, sum;
+        plain_row<D, kTile>(a, span, first, last, span, a.kv.table + (int64_t)b * a.kv.width, kvh,
+                            a.q + b * a.sq + (int64_t)(h0 + r) * D, x, top, sum);
+        store_plain_row<T, D>(a, parts, active > 1, b, h0 + r, split, x, top, sum);
+        if (active == 1 && splits > 1 && lane == 0) parts.mark(row0 + r, 0, top, kWhole);
     }
 }
 

@@ -109,6 +109,56 @@ __device__ __forceinline__ Span key_span(const AttnArgs& a, int p) {
     return s;
 }
 
+__device__ __forceinline__ float half_value(const AttnArgs& a, uint16_t x) {
+    return a.dtype == 0 ? (float)__builtin_bit_cast(_Float16, x) : __builtin_bit_cast(float, (uint32_t)x << 16);
+}
+
+// One row over tiles [first, last) of `tiles` (KEYS keys each, at most 64) by
+// the whole wave, straight from the formula: lane j scores key j of each tile, then owns
+// the output elements lane + 64 i.  For rows that an infinity or NaN has
+// reached in the matrix products, where it also meets weights of 0 and of
+// either sign: here only keys that the row sees, and each with its weight.  A key
+// at a time: some hundred times slower than the products.
+template <int D, int KEYS>
+__device__ void plain_row(const AttnArgs& a, const Span& tiles, int first, int last, const Span& row_span,
+                          const int32_t* table, int kvh, const uint16_t* q, float (&o)[4], float& m, float& l) {
+    const int lane = threadIdx.x & 63;
+    const float scale = a.scale * 1.4426950408889634f;
+    m = -INFINITY;
+    l = 0.0f;
+    for (int i = 0; i < 4; ++i) o[i] = 0.0f;
+    for (int t = first; t < last; ++t) {
+        const int j = tiles.base(t, KEYS) + lane;
+        bool seen = lane < KEYS && row_span.seen(j);
+        int page = -1;
+        if (seen) page = table[j >> a.kv.page_shift];
+        seen = seen && page >= 0 && page < a.kv.pages;
+        const int64_t at = seen ? ((((int64_t)page * a.kv_heads + kvh) << a.kv.page_shift) +
+                                   (j & ((1 << a.kv.page_shift) - 1))) * D : 0;
+        float s = -INFINITY;
+        if (seen) {
+            s = 0.0f;
+            for (int d = 0; d < D; ++d) s = fmaf(half_value(a, q[d]), half_value(a, a.kv.k[at + d]), s);
+            s *= scale;
+        }
+        float top = s;
+        for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+        const float mn = fmaxf(m, top), ms = mn == -INFINITY ? 0.0f : mn;
+        const float f = exp2_fast(m - ms), w = seen ? exp2_fast(s - ms) : 0.0f;
+        m = mn;
+        l *= f;
+        for (int i = 0; i < 4; ++i) o[i] *= f;
+        for (uint64_t left = __ballot(seen); left; left &= left - 1) {
+            const int k = __builtin_ctzll(left);
+            const float wk = __shfl(w, k);
+            const int64_t r = __shfl(at, k);
+            l += wk;
+            for (int i = 0; i < 4; ++i)
+                if (lane + 64 * i < D) o[i] = fmaf(wk, half_value(a, a.kv.v[r + lane + 64 * i]), o[i]);
+        }
+    }
+}
+
 // Writes four elements of an output row, and lse with the first of them.
 // sum == 0: no key was seen, or none with a score above -inf.
 template <class T>
@@ -146,5 +196,23 @@ struct Partials {
         *reinterpret_cast<f4*>(o + (row * splits + split) * D + d) = acc;
     }
 };
+
+// Writes what plain_row left in its wave's lanes: the output row, or where the
+// keys are cut over workgroups its partial result.
+template <class T, int D>
+__device__ __forceinline__ void store_plain_row(const AttnArgs& a, const Partials& parts, bool cut, int64_t token, int head,
+                                                int split, const float (&o)[4], float m, float l) {
+    const int lane = threadIdx.x & 63;
+    const int64_t row = token * a.q_heads + head;
+    for (int i = 0; i < 4; ++i) {
+        const int d = lane + 64 * i;
+        if (d >= D) continue;
+        if (cut) parts.o[(row * parts.splits + split) * D + d] = o[i];
+        else a.o[token * a.so + (int64_t)head * D + d] = (uint16_t)T::pack(l == 0.0f ? 0.0f : o[i] / l, 0.0f);
+    }
+    if (lane != 0) return;
+    if (cut) parts.mark(row, split, m, l);
+    else if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+}
 
 }  // namespace slim

@@ -73,52 +73,6 @@ __device__ __forceinline__ Halves halves(float x) {
     return {__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
 }
 
-__device__ __forceinline__ float half_value(const AttnArgs& a, uint16_t x) {
-    return a.dtype == 0 ? (float)__builtin_bit_cast(_Float16, x) : __builtin_bit_cast(float, (uint32_t)x << 16);
-}
-
-// One row by the whole wave, straight from the formula: lane j scores key j of
-// each tile, then owns the output elements lane + 64 i.
-template <int D>
-__device__ void plain_row(const AttnArgs& a, const Span& tiles, int first, int last, const Span& row_span,
-                          const int32_t* table, int kvh, const uint16_t* q, float (&o)[4], float& m, float& l) {
-    const int lane = threadIdx.x & 63;
-    const float scale = a.scale * 1.4426950408889634f;
-    m = -INFINITY;
-    l = 0.0f;
-    for (int i = 0; i < 4; ++i) o[i] = 0.0f;
-    for (int t = first; t < last; ++t) {
-        const int j = tiles.base(t, kKeys) + lane;
-        bool seen = row_span.seen(j);
-        int page = -1;
-        if (seen) page = table[j >> a.kv.page_shift];
-        seen = seen && page >= 0 && page < a.kv.pages;
-        const int64_t at = seen ? ((((int64_t)page * a.kv_heads + kvh) << a.kv.page_shift) +
-                                   (j & ((1 << a.kv.page_shift) - 1))) * D : 0;
-        float s = -INFINITY;
-        if (seen) {
-            s = 0.0f;
-            for (int d = 0; d < D; ++d) s = fmaf(half_value(a, q[d]), half_value(a, a.kv.k[at + d]), s);
-            s *= scale;
-        }
-        float top = s;
-        for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-        const float mn = fmaxf(m, top), ms = mn == -INFINITY ? 0.0f : mn;
-        const float f = exp2_fast(m - ms), w = seen ? exp2_fast(s - ms) : 0.0f;
-        m = mn;
-        l *= f;
-        for (int i = 0; i < 4; ++i) o[i] *= f;
-        for (uint64_t left = __ballot(seen); left; left &= left - 1) {
-            const int k = __builtin_ctzll(left);
-            const float wk = __shfl(w, k);
-            const int64_t r = __shfl(at, k);
-            l += wk;
-            for (int i = 0; i < 4; ++i)
-                if (lane + 64 * i < D) o[i] = fmaf(wk, half_value(a, a.kv.v[r + lane + 64 * i]), o[i]);
-        }
-    }
-}
-
 // Division by a number that the launch knows: a product with m = (2^32 - 1) / d
 // (rounded down) gives the quotient or one less.  (The compiler's own takes some 30
 // instructions, and the kernel's beginning is bound by their number.)
@@ -584,20 +538,9 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         for (int r = 32 * wave; r < 32 * wave + w_rows; ++r) {
             const int p = token_of(r), tk = row_first + token0 + p, hd = kvh * share + skip + r - p * share;
             float x[4], mx, lx;
-            plain_row<D>(a, span, begin, end, key_span(a, p_first + p), table, kvh, a.q + tk * a.sq + (int64_t)hd * D, x,
-                         mx, lx);
-            const int64_t row = (int64_t)tk * a.q_heads + hd;
-            for (int k = 0; k < 4; ++k) {
-                const int d = lane + 64 * k;
-                if (d >= D) continue;
-                if (splits > 1) {
-                    parts.o[(row * splits + split) * D + d] = x[k];
-                } else {
-                    a.o[tk * a.so + (int64_t)hd * D + d] = (uint16_t)T::pack(lx == 0.0f ? 0.0f : x[k] / lx, 0.0f);
-                    if (d == 0 && a.lse) a.lse[row] = lx == 0.0f ? -INFINITY : mx * 0.6931471805599453f + logf(lx);
-                }
-            }
-            if (splits > 1 && lane == 0) parts.mark(row, split, mx, lx);
+            plain_row<D, kKeys>(a, span, begin, end, key_span(a, p_first + p), table, kvh, a.q + tk * a.sq + (int64_t)hd * D,
+                                x, mx, lx);
+            store_plain_row<T, D>(a, parts, splits > 1, tk, hd, split, x, mx, lx);
         }
         return;
     }
