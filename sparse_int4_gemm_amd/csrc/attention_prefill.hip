@@ -118,16 +118,18 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     }
     const int slot = grid.slots - 1 - order;
 
-    // Sequence b's slots begin at starts[b] * share / kRows + b: at least as
-    // many as its rows fill.  Found as find_seq finds a token's sequence; the
-    // last step has its starts and length in the lanes already.
+    // Sequence b's slots begin at starts[b] * share / kRows + b (of its start
+    // among the rows there are, [0, tokens]): at least as many as its rows fill.
+    // Found as find_seq finds a token's sequence; the last step has its starts
+    // and length in the lanes already.
     int lo = 0, n = a.kv.seqs, found, starts, ends, lens;
     do {
         const int step = (n + 63) >> 6, i = lo + min(lane * step, n - 1);
         starts = a.kv.starts[i];
         ends = a.kv.starts[i + 1];
         lens = a.kv.lens[i];
-        const uint64_t ok = __ballot(lane * step < n && (((int64_t)starts * share) >> kRowsLog) + i <= slot);
+        const int row = min(max(starts, 0), a.tokens);
+        const uint64_t ok = __ballot(lane * step < n && (((int64_t)row * share) >> kRowsLog) + i <= slot);
         if (ok == 0) return;
         found = 63 - __builtin_clzll(ok);
         lo += found * step;
@@ -138,8 +140,8 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     const int from_row = __builtin_amdgcn_readlane(starts, found), to_row = __builtin_amdgcn_readlane(ends, found);
     const int len = min(max(__builtin_amdgcn_readlane(lens, found), 0), kMaxLen);
     const int b = __builtin_amdgcn_readfirstlane(lo);
-    const int64_t tile = slot - ((((int64_t)from_row * share) >> kRowsLog) + b);
     const int row_first = min(max(from_row, 0), a.tokens), count = max(min(to_row, a.tokens) - row_first, 0);
+    const int64_t tile = slot - ((((int64_t)row_first * share) >> kRowsLog) + b);
     if (tile < 0 || tile * kRows >= (int64_t)count * share) return;
 
     // Row r of the block is token (skip + r) / share past `token0`: 32-bit
@@ -151,7 +153,9 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     const int token0 = grid.share.quotient(r0), skip = (int)(r0 - (uint32_t)(token0 * share));
     const float per_share = 1.0f / (float)share;
     auto token_of = [&](int r) { return (int)(((float)(skip + r) + 0.5f) * per_share); };
-    const int before = len - count;                                     // position of new token 0
+    // Position of the first of them; new tokens before or behind the rows there are
+    // count too (held at where all positions are negative: nothing below overflows).
+    const int before = max(len - (to_row - row_first), -a.tokens);
     const int p_first = before + token0;
     const int p_last = p_first + __builtin_amdgcn_readfirstlane(token_of(rows - 1));
     Span span = key_span(a, p_last);
