@@ -1,7 +1,7 @@
 // slim_attention_decode: attention of one new token per sequence.
 //
 //   s_j = scale q . k_j,  O = sum_j 2^(c s_j - m) v_j / l,  c = log2 e,
-//   m a running maximum of c s_j, l the sum of the weights (all fp32).
+//   m a running maximum of c s_j - T::kTop, l the sum of the weights (all fp32).
 //
 // Bound by the keys and values read once from HBM (1 to 16 flops a byte), so
 // the kernel is built around loads: each wave streams tiles of 32 keys
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
                           fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float mn = fmaxf(m, top);
+        const float mn = fmaxf(m, top - T::kTop);            // the largest weight is 2^kTop
         const float ms = mn == -INFINITY ? 0.0f : mn;        // nothing seen so far: all weights are 2^-inf = 0
         const float f = exp2_fast(m - ms);
         m = mn;

@@ -13,7 +13,13 @@ typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 
 // Operands travel as dwords of two halves; `pack` rounds to nearest even.
+// kTop: log2 of the largest softmax weight that enters a product.  fp16 ends at
+// 2^16 and, downwards, at 2^-24: with weights of 1 at most, those 2^-25 of the
+// row's largest and below would be lost to the output, and not to the sum (a first key 25.5
+// bits above 2^19 others: outputs 0.5% low), so they are taken as high as they
+// go.  bf16 has the range of fp32.
 struct Fp16 {
+    static constexpr float kTop = 15.0f;
     static __device__ __forceinline__ f4 mfma16(u4 a, u4 b, f4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
     }
@@ -27,6 +33,7 @@ struct Fp16 {
     static __device__ __forceinline__ float high(uint32_t x) { return (float)__builtin_bit_cast(h2, x)[1]; }
 };
 struct Bf16 {
+    static constexpr float kTop = 0.0f;
     static __device__ __forceinline__ f4 mfma16(u4 a, u4 b, f4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
     }

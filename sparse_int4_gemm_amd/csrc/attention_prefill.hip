@@ -2,7 +2,7 @@
 // cache.
 //
 //   s_j = scale q . k_j,  O = sum_j 2^(c s_j - m) v_j / l,  c = log2 e,
-//   m within 2^kLazy of the running maximum of c s_j, l the sum of the weights.
+//   m within 2^kLazy of the running maximum of c s_j - kUp, l the sum of the weights.
 //
 // Bound by the matrix unit (4 head_dim flops for each query, head and key it
 // sees) and, nearly as much, by the vector unit (about 6 instructions and an
@@ -42,7 +42,7 @@ namespace slim {
 namespace {
 
 constexpr int kKeys = 64;            // keys of a tile
-constexpr float kLazy = 8.0f;        // weights stay at or below 2^kLazy
+constexpr float kLazy = 8.0f;        // a weight may pass 2^kUp by 2^kLazy
 // Query rows of a workgroup: 32 for each of its row waves.
 constexpr int kRowWaves = 4, kRowsLog = 7, kRows = 1 << kRowsLog;
 
@@ -170,6 +170,8 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     auto tiles_before = [&](int i) { return max(0, (i - begin - group + KG - 1) / KG); };      // of the group's, below i
     constexpr int first = 0;
     const int last = tiles_before(end), steps = (end - begin + KG - 1) / KG;
+
+    constexpr float kUp = T::kTop > kLazy ? T::kTop - kLazy : 0.0f;        // so that no weight passes 2^kTop
 
     // This lane's query.
     const bool live = 32 * wave + col < rows;
@@ -362,7 +364,7 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         __builtin_amdgcn_sched_barrier(0);
         add_value(kFirst);
         const Halves tops = halves(top);
-        top = fmaxf(tops.lo, tops.hi) * scale;
+        top = fmaf(fmaxf(tops.lo, tops.hi), scale, -kUp);
         const bool raise = __any(top > m + kLazy);
         const float was = m;
         m = raise ? fmaxf(m, top) : m;
