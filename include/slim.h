@@ -393,10 +393,10 @@ slim_status slim_pack_transposed(const uint8_t* values, const uint8_t* meta,
  * head_dim 64, 96, 128 or 256; page_size a power of two from 16 to 1024;
  * q_heads a multiple of kv_heads; heads at most 1024; tokens and
  * seqs up to 2^22, pages and table_width up to 2^24, table_width * page_size
- * up to 2^30.  Rows
- * of Q and O are [q_heads][head_dim], rows of the new K and V
- * [kv_heads][head_dim], consecutive rows stride_* elements apart (a multiple of
- * 8, at least a row: a slice of a joint q/k/v array is taken as it is).
+ * up to 2^30.  Rows of Q and O are [q_heads][head_dim], rows of the new K and
+ * V [kv_heads][head_dim], consecutive rows stride_* elements apart (a multiple
+ * of 8, at least a row and at most 2^22: a slice of a joint q/k/v array is
+ * taken as it is).
  * Pointers are 16-byte aligned except table, lens, starts, src, dst and lse
  * (4 bytes).  Errors: SLIM_EINVAL for a broken rule, a NULL pointer or a
  * workspace too small, SLIM_EUNSUPPORTED for a head_dim, page_size or dtype

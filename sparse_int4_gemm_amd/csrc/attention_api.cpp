@@ -9,12 +9,14 @@ namespace {
 using slim::aligned16;
 using slim::fail;
 using slim::kMaxDim;
-using slim::kMaxStride;
 
 constexpr int64_t kMaxHeads = 1024;
 constexpr int64_t kMaxPositions = int64_t(1) << 30;   // table_width * page_size
 constexpr int64_t kMaxTokens = int64_t(1) << 22;      // a workgroup per token stays within a grid's 2^32 threads
 constexpr int64_t kMaxPageBytes = int64_t(1) << 30;
+// Elements between rows: the prompt kernel's offsets from a block's first row, of up to
+// 128 rows, are 32-bit bytes.
+constexpr int64_t kMaxRowStride = int64_t(1) << 22;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -30,9 +32,9 @@ int page_shift(int64_t p) {
 slim_status check_rows(const char* what, const void* p, int64_t stride, int64_t rows, int64_t row) {
     if (!p) return fail(SLIM_EINVAL, "%s is NULL", what);
     if (!aligned16(p)) return fail(SLIM_EINVAL, "%s must be 16-byte aligned", what);
-    if (stride % 8 || (rows > 1 && stride < row) || stride < 0 || stride > kMaxStride / kMaxDim)
+    if (stride % 8 || (rows > 1 && stride < row) || stride < 0 || stride > kMaxRowStride)
         return fail(SLIM_EINVAL, "%s: row stride %lld must be a multiple of 8, at least %lld and at most %lld", what,
-                    (long long)stride, (long long)row, (long long)(kMaxStride / kMaxDim));
+                    (long long)stride, (long long)row, (long long)kMaxRowStride);
     return SLIM_OK;
 }
 

@@ -272,7 +272,8 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     // The wave's queries go through LDS as a key tile does (waves 0 and 1 of the
     // group to K of buffer 1, 2 and 3 to V of it, not in use yet): read straight
     // into the operand layout, every 32 bytes of a load would be another row's.
-    // The rows' elements in global memory from the block's first token and head on:
+    // The rows' elements in global memory from the block's first token and head on
+    // (at most 128 rows of 2^22: 2^30 bytes):
     auto element = [&](int r, int64_t stride) { return token_of(r) * ((int)stride - share * D) + (skip + r) * D; };
     auto load_queries = [&] {
         const u4 rsrc = rsrc_words(a.q + (int64_t)(row_first + token0) * a.sq + (int64_t)kvh * share * D, kOOB);
