@@ -16,6 +16,8 @@ import torch
 
 from . import _lib
 
+PAGE_SIZES = tuple(1 << i for i in range(4, 11))
+
 
 class CacheFull(RuntimeError):
     """Not enough free pages; the cache is as it was before the call."""
@@ -40,8 +42,19 @@ class _Sequence:
 class KVCache:
     def __init__(self, layers: int, pages: int, kv_heads: int, head_dim: int, page_size: int = 64,
                  dtype: torch.dtype = torch.float16, device="cuda"):
-        if layers <= 0 or pages <= 0:
-            raise ValueError("layers and pages must be positive")
+        if min(layers, pages, kv_heads, head_dim, page_size) <= 0:
+            raise ValueError("layers, pages, kv_heads, head_dim and page_size must be positive")
+        if layers > 4096 or pages > 1 << 24:
+            raise ValueError("at most 4096 layers and 2^24 pages")
+        # What the calls on these pools would refuse later, with pages handed
+        # out already.  (Pools on the host serve the bookkeeping alone.)
+        if torch.device(device).type != "cpu":
+            if dtype not in _lib._DTYPES:
+                raise TypeError(f"the pools must be float16 or bfloat16, not {dtype}")
+            if _lib.slim_attention_workspace_bytes(1, 1, kv_heads, kv_heads, head_dim) == 0:
+                raise ValueError(f"no attention with {kv_heads} key heads of size {head_dim}")
+            if page_size not in PAGE_SIZES:
+                raise ValueError(f"page_size must be one of {PAGE_SIZES}, not {page_size}")
         self.page_size = page_size
         self.k = torch.empty((layers, pages, kv_heads, page_size, head_dim), dtype=dtype, device=device)
         self.v = torch.empty_like(self.k)
