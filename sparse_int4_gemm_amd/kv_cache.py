@@ -122,8 +122,8 @@ class KVCache:
 
     def extend(self, seqs: Sequence[int], counts: Sequence[int] | None = None) -> Batch:
         """Make room for counts[i] new tokens of sequence seqs[i] (one each if
-        None) and return the step's batch; raises CacheFull, with nothing
-        changed, if the free pages do not suffice."""
+        None) and return the step's batch; raises CacheFull if the free pages
+        do not suffice.  After any error the cache is as it was."""
         seqs = list(seqs)
         counts = [1] * len(seqs) if counts is None else list(counts)
         if len(counts) != len(seqs) or len(set(seqs)) != len(seqs) or any(c < 0 for c in counts):
@@ -144,20 +144,33 @@ class KVCache:
                     need += 1
         if need > len(self._free):
             raise CacheFull(f"{need} pages needed, {len(self._free)} free")
-        src, dst = [], []
-        for q in copies:
-            s = self._seqs[q]
-            p, s.pages[-1] = s.pages[-1], self._take()
-            src.append(p)
-            dst.append(s.pages[-1])
+        before = [(s, len(s.pages), s.length) for s in (self._seqs[q] for q in seqs)]
+        src = [self._seqs[q].pages[-1] for q in copies]
+        dst = [self._take() for _ in copies]
+        try:
+            self._move(src, dst)
+            for q, p in zip(copies, dst):
+                self._seqs[q].pages[-1] = p
+            for q, c in zip(seqs, counts):
+                s = self._seqs[q]
+                s.length += c
+                while len(s.pages) * size < s.length:
+                    s.pages.append(self._take())
+            batch = self.batch(seqs, counts)
+        except BaseException:
+            for s, n, length in before:
+                for p in s.pages[n:]:
+                    self._release(p)
+                del s.pages[n:]
+                s.length = length
+            for q, p in zip(copies, src):
+                self._seqs[q].pages[-1] = p
+            for p in dst:
+                self._release(p)
+            raise
+        for p in src:
             self._release(p)
-        for q, c in zip(seqs, counts):
-            s = self._seqs[q]
-            s.length += c
-            while len(s.pages) * size < s.length:
-                s.pages.append(self._take())
-        self._move(src, dst)
-        return self.batch(seqs, counts)
+        return batch
 
     def _take(self) -> int:
         p = heapq.heappop(self._free)
@@ -191,11 +204,11 @@ class KVCache:
         live = sum(1 for n in self._owners if n)
         src = [p for p in range(live, len(self._owners)) if self._owners[p]]
         dst = [p for p in range(live) if not self._owners[p]]
+        self._move(src, dst)
         to = dict(zip(src, dst))
         for p, q in to.items():
             self._owners[q], self._owners[p] = self._owners[p], 0
         for s in self._seqs.values():
             s.pages = [to.get(p, p) for p in s.pages]
         self._free = list(range(live, len(self._owners)))
-        self._move(src, dst)
         return len(src)
