@@ -120,7 +120,8 @@ def main(argv=None):
         nonlocal worst
         for i, s in enumerate(seqs):
             want = block.plain(q[i], s)
-            worst = max(worst, float((y[i].float() - want).norm() / want.norm()))
+            off = float((y[i].float() - want).norm() / want.norm())
+            worst = max(worst, off if off == off else float("inf"))
 
     seqs = [cache.add() for _ in prompts]
     block.step(tokens(sum(prompts)), seqs, prompts)
