@@ -66,6 +66,9 @@ class AttentionBlock:
     def step(self, x, seqs, counts):
         """x [tokens, hidden]: counts[i] new tokens of seqs[i].  Returns the block's
         output, the queries and the attention's output (for the check)."""
+        if self.window:                   # (only now: the tokens of the step before saw these pages)
+            for s in seqs:
+                self.cache.drop(s, self.window, self.sinks)
         batch = self.cache.extend(seqs, counts)
         at = [p for s, c in zip(seqs, counts) for p in range(self.cache.length(s) - c, self.cache.length(s))]
         positions = torch.tensor(at, device=x.device)
@@ -79,9 +82,6 @@ class AttentionBlock:
             y = slim.attention_decode(q, *pools, batch.table, batch.lens, **kw)
         else:
             y = slim.attention_prefill(q, *pools, batch.table, batch.lens, batch.starts, **kw)
-        if self.window:
-            for s in seqs:
-                self.cache.drop(s, self.window, self.sinks)
         return self.o(y.reshape(x.shape[0], -1)), q, y
 
     def plain(self, q, seq):
