@@ -374,8 +374,8 @@ slim_status slim_pack_transposed(const uint8_t* values, const uint8_t* meta,
  * so one captured graph serves a cache that grows.  Their values are checked
  * where they are used: a table entry outside [0, pages), and a position past
  * table_width * page_size, holds no key (it is masked; append writes nothing
- * there), rows outside [0, tokens) are left alone, and no value reads or
- * writes out of range.
+ * there), rows outside [0, tokens) are left alone (those inside keep their
+ * positions), and no value reads or writes out of range.
  *
  * What a query at position p sees: key j if j <= p and (window == 0, or
  * j > p - window, or j < sinks): causal, the last `window` positions (its own
@@ -385,9 +385,13 @@ slim_status slim_pack_transposed(const uint8_t* values, const uint8_t* meta,
  *   m = max_j s_j, l = sum_j exp(s_j - m) over the keys seen, lse = m + ln l.
  * A row that sees no key (or only scores of -inf) gives O = 0, lse = -inf.
  * Keys and values that a row does not see do not reach it, whatever they
- * hold, NaN and infinities included.  Scores, m, l and O are held in fp32;
- * the products take fp16 or bf16 operands.  Results do not depend on other
- * sequences' values and repeat bit for bit.
+ * hold, NaN and infinities included; a seen infinite value gives its element of O
+ * that infinity (NaN with one of the other sign).  Rows with such results are
+ * computed again key by key, which makes a call of many of them some hundred times slower.
+ * Scores, m, l and O are held in fp32; the products take fp16 or bf16
+ * operands: weights enter slim_attention_prefill's rounded once to the type,
+ * slim_attention_decode's with the accuracy of fp32.  Results do not depend on
+ * other sequences' values and repeat bit for bit.
  *
  * Arguments of all calls: dtype SLIM_FP16 or SLIM_BF16 (of every half tensor);
  * head_dim 64, 96, 128 or 256; page_size a power of two from 16 to 1024;
@@ -443,9 +447,10 @@ size_t slim_attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t q_he
  * slim_attention_decode — attention of one new token of each sequence (row b
  * of Q at position lens[b] - 1), its key and value already in the cache.
  *   Q, O     [seqs] rows;  lse: fp32 [seqs][q_heads] or NULL
- *   max_len  the longest length expected: it only sets how far the work is split over
- *            the keys (longer sequences are computed as well); it may
- *            change results in their last bits
+ *   max_len  the longest length expected: it only plans the work, how far it is
+ *            split over the keys among others (longer sequences are computed
+ *            as well), and is best near the longest there is: far from it the
+ *            plan may be a slower one.  It may change results in their last bits
  *   window   0 or the number of last positions seen; sinks >= 0
  */
 slim_status slim_attention_decode(const uint16_t* Q, int64_t stride_Q, uint16_t* O, int64_t stride_O, float* lse,
@@ -459,7 +464,8 @@ slim_status slim_attention_decode(const uint16_t* Q, int64_t stride_Q, uint16_t*
  * slim_attention_prefill — the same for any number of new tokens of each
  * sequence (starts), whole prompts or chunks behind a cached prefix, their keys and
  * values already in the cache.  Q, O: [tokens] rows; lse: fp32
- * [tokens][q_heads] or NULL; rows at or past starts[seqs] are not written.
+ * [tokens][q_heads] or NULL; rows before starts[0] and at or past starts[seqs]
+ * are not written.
  * Other arguments as slim_attention_decode.
  */
 slim_status slim_attention_prefill(const uint16_t* Q, int64_t stride_Q, uint16_t* O, int64_t stride_O, float* lse,

@@ -261,7 +261,8 @@ def attention_decode(q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor, 
 
     window: 0, or the number of last positions seen, with the first `sinks`
     ones; max_len: the longest length expected (None: the table's capacity),
-    which only plans how the work is split; scale: 1 / sqrt(head_dim) if None;
+    which only plans the work: far above the lengths the plan may be a slower
+    one; scale: 1 / sqrt(head_dim) if None;
     lse: float32 [seqs, q_heads], receives the log of the softmax sums."""
     if out is None or ws is None:
         out, ws = _attention_buffers(q, lens, kpool, ws, out, stream)

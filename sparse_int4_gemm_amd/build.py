@@ -33,10 +33,11 @@ COMMON_FLAGS = [
 ]
 
 
-# Extra flags per source.  The prompt attention kernels use more than 256
-# registers a lane; this keeps the results of their matrix instructions in
-# registers that vector instructions can read (the other form moved every
-# score through v_accvgpr_read: 12410 such moves in the file against 1984).
+# Extra flags per source.  The prompt attention kernel of head size 256 uses
+# more than 256 registers a lane (the others 155 to 231); this keeps the results
+# of its matrix instructions in registers that vector instructions can read.
+# Without it: 256 accumulation registers instead of 148, 40 vector spills
+# instead of none, 3572 moves between the two kinds in the file instead of 570.
 FILE_FLAGS: dict[str, list[str]] = {
     "attention_prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }

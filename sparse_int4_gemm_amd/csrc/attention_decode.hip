@@ -8,7 +8,9 @@
 // straight into registers, one tile ahead of the one it computes on, and every
 // load is as wide as the layout gives (16 bytes a lane at head size 128).
 //  - One wave serves up to 16 query heads of a key head: the matrix
-//    instruction's 16 columns.  Keys are its rows: S^T = K Q^T leaves a
+//    instruction's 16 columns; more take a workgroup for every 16, which reads
+//    the keys again (64 sequences of 4096, 8 key heads: 183 us with 16 query heads
+//    each, 295 with 20 or 32, 443 with 40).  Keys are its rows: S^T = K Q^T leaves a
 //    lane with one query (column) and the 4 keys 16 t + 4 g + [0, 4) of each
 //    16-key half t (g = lane / 16).
 //  - O^T = V^T P^T then takes these weights as they lie: its 32 contraction
@@ -25,12 +27,12 @@
 //    take every fourth tile and join through LDS; the chunks of a row are joined
 //    by attention_join_kernel.
 //  - Page numbers come through the scalar cache a tile ahead: as vector loads
-//    they would be waited for behind the keys in flight (131071 keys: 128 us
-//    against 124).
-// Measured (a 1 GiB copy moves 4.8 TB/s, read and write together): 64 sequences
-// of 4096 tokens, 32 heads of 128: 720 us, 6.0 TB/s; of 1 to 4096: 365 us, 5.9
+//    they would be waited for behind the keys in flight (131071 keys: 124 us
+//    against 128).
+// Measured (a stream of 4 GiB is read at 6.1 TB/s): 64 sequences
+// of 4096 tokens, 32 heads of 128: 720 us, 6.0 TB/s; of 1 to 4096: 367 us, 5.9
 // TB/s (longest first; the last long ones alone: 436); one of 131071, 8 key heads:
-// 96 us, 5.6 TB/s; one of 33: 5 us, launch and the chain lens -> table -> keys -> join.
+// 97 us, 5.5 TB/s; one of 33: 5.5 us, launch and the chain lens -> table -> keys -> join.
 #include "attention_device.hpp"
 
 namespace slim {
@@ -294,7 +296,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnAr
 // them cost more in partial results than they gain (131071 keys of 8 key heads: 512
 // workgroups 100 us, 1024 103, 2048 111; 64 sequences of up to 900 at head size
 // 256: 61 us unsplit, 87 in two), fewer tiles too (4 sequences of up to 8000, 8 key heads:
-// 16 tiles 20.7 us, 8 tiles 24.1).
+// 16 tiles 20.7 us, 8 tiles 24.1).  One number for the batch, from its size and
+// longest length: a long sequence among enough short ones is not split (63 of
+// 100 tokens and one of 131071, 8 key heads: 2582 us, the long one alone 98).
 constexpr int kSplitTarget = 512, kMinTiles = 16, kSortFrom = 512;
 
 template <class T, int D>
@@ -308,8 +312,8 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     const int splits = (int)max((int64_t)1, min(want, kAttnSplitRows / ((int64_t)a.tokens * a.q_heads)));
     const int chunk = max(kWaves, (tiles + splits - 1) / splits);
     dim3 grid((unsigned)(a.tokens * splits), (unsigned)(a.kv_heads * groups));
-    // More than one round of workgroups, so that none is split: the longest
-    // sequences first, or the last ones to begin end alone (64 sequences of 1 to
+    // More than one round of workgroups, so that none is split: the longest of
+    // every 64 sequences first, or the last ones to begin end alone (64 sequences of 1 to
     // 4096, 32 key heads: 436 us in their order, 365 so; 128 of up to 8000, 8 key
     // heads 426 and 377; 64 of up to 900 at head size 256 207 and 170).  Not for
     // short ones, where finding a place costs more (512 of up to 100: 40.3 and

@@ -34,8 +34,9 @@
 //    wave whose output is not finite is computed again key by key (plain_row),
 //    which gives only the rows that do see such a value theirs.
 // Measured: 8192 tokens, window 4096, 32 query heads on 8 key heads of 128,
-// bf16: 391 us, 1.05 PFLOP/s (a library product of 8192^3: 1.45); matrix unit
-// busy 57%, vector unit 55% of the cycles, at 2.0 GHz (power).
+// bf16: 391 to 403 us on different cards, 1.02 to 1.05 PFLOP/s (a library
+// product of 8192^3: 1.40 to 1.45); 719 thousand cycles, so 1.8 GHz over the call,
+// of which the matrix unit is busy for 57% and the vector unit for 55%.
 #include "attention_device.hpp"
 
 namespace slim {
@@ -47,7 +48,9 @@ constexpr float kLazy = 8.0f;        // a weight may pass 2^kUp by 2^kLazy
 constexpr int kRowWaves = 4, kRowsLog = 7, kRows = 1 << kRowsLog;
 
 // Splits of the keys: kSplitTarget workgroups in all (one a CU), each with at
-// least kMinTiles tiles.
+// least kMinTiles tiles.  One number for the batch, from its rows and the
+// longest length: a long sequence among enough short ones is not split (61
+// tokens on 24576 alone 49 us, beside 40 single tokens on 200 423).
 constexpr int kSplitTarget = 256, kMinTiles = 4;
 
 // A tile lies in LDS as [row of 64 bytes' quads][its rows][64 bytes]: a load of

@@ -14,7 +14,7 @@ constexpr int kThreads = 256;
 // HBM for prompts, by launch and the chain starts -> lens -> table -> store
 // for single tokens.  Each wave finds its sequence itself (find_seq), which
 // costs one load for up to 64 sequences.  Measured, 32 heads of 128: 8763
-// tokens 59 us (4.8 TB/s, what a plain copy moves), 64 tokens 3 us.  U vectors a
+// tokens 59 us (4.8 TB/s; a plain copy of a GiB moves 5.7), 64 tokens 3 us.  U vectors a
 // thread: 4 where there are workgroups enough (more loads in flight), 1 for up to 512
 // tokens.
 template <int U>

@@ -24,7 +24,9 @@ class CacheFull(RuntimeError):
 
 
 class Batch(NamedTuple):
-    """One step's device arrays, as kv_append and the attention calls take them."""
+    """One step's device arrays, as kv_append and the attention calls take them.
+    (New ones each time, as wide as the step's longest sequence: a captured graph
+    has its own and copies these into them.)"""
     table: torch.Tensor      # int32 [seqs, width]; -1 where a sequence owns no page
     lens: torch.Tensor       # int32 [seqs], the new tokens included
     starts: torch.Tensor     # int32 [seqs + 1]
