@@ -476,6 +476,108 @@ slim_status slim_attention_prefill(const uint16_t* Q, int64_t stride_Q, uint16_t
                                    int64_t sinks, float scale, void* workspace, size_t workspace_bytes,
                                    hipStream_t stream);
 
+/*
+ * Rotary positions: element pairs of each head turned by an angle that grows
+ * with the row's position p, pair i by p * freqs[i] radians:
+ *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin).
+ *   freqs        fp64 [rot_dim / 2], device (8-byte aligned): any frequencies,
+ *                so every way of scaling them for long contexts is served
+ *   rot_dim      the first rot_dim elements of a head are turned (a multiple of
+ *                8, at most head_dim), the others are left as they are
+ *   interleaved  0: pair i is elements i and i + rot_dim / 2, 1: 2 i and 2 i + 1
+ *   magnitude    finite; 1 leaves lengths as they are
+ * Angles, cosines and sines are formed in fp64 (position 2^30 is as exact as 1),
+ * half outputs are turned in fp32 and rounded once.  The struct is host memory, read
+ * during the call; freqs is read when the call runs.
+ */
+typedef struct {
+    const double* freqs;
+    int64_t rot_dim;
+    int32_t interleaved;
+    float magnitude;
+} slim_rotation;
+
+/*
+ * slim_rope — X, Y rows [tokens] of [heads][head_dim] (consecutive rows
+ * stride_* elements apart, as those of Q above), row t at position
+ * positions[t] (int32, device; a negative one turns back: the inverse of the
+ * rotation at magnitude 1, and its gradient).  head_dim a multiple of 8 up to 1024.  Y may be
+ * X itself, with the same stride.
+ */
+slim_status slim_rope(const uint16_t* X, int64_t stride_X, uint16_t* Y, int64_t stride_Y, int64_t tokens,
+                      int64_t heads, int64_t head_dim, int dtype, const int32_t* positions,
+                      const slim_rotation* rotation, hipStream_t stream);
+
+/*
+ * slim_kv_append_rope — slim_kv_append with the keys turned to their positions
+ * on the way, and with them the step's queries:
+ *   Q, Qout   rows [tokens] of [q_heads][head_dim], or both NULL (q_heads is
+ *             then ignored); Qout may be Q itself, with the same stride
+ * Rows of Qout that belong to no sequence are not written; those whose
+ * position has no page are (queries need none).  Other arguments as slim_kv_append.
+ */
+slim_status slim_kv_append_rope(const uint16_t* Q, int64_t stride_Q, uint16_t* Qout, int64_t stride_Qout,
+                                int64_t q_heads, const uint16_t* K, int64_t stride_K, const uint16_t* V,
+                                int64_t stride_V, int64_t tokens, int64_t seqs, int64_t kv_heads, int64_t head_dim,
+                                int dtype, const int32_t* table, int64_t table_width, const int32_t* lens,
+                                const int32_t* starts, uint16_t* Kpool, uint16_t* Vpool, int64_t pages,
+                                int64_t page_size, const slim_rotation* rotation, hipStream_t stream);
+
+/*
+ * A cache of 4 bits a value.  A row of one head is cut into groups of 32
+ * elements; a group is 32 codes of 4 bits times 2^e.  Code c stands for 0, 0.5,
+ * 1, 1.5, 2, 3, 4 or 6 by its low three bits, negative if bit 3 is set (the
+ * pairs that this processor turns into two halves in one instruction).
+ *   e is the smallest whole number for which no element of the group exceeds
+ *   7 * 2^e (so none moves by more than 2^e, the half step between 4 and 6), held
+ *   within [-23, 13] in fp16 and [-125, 125] in bf16: half of 2^e is then a
+ *   number of the type, and 6 * 2^e finite.  An element goes to the nearest
+ *   code, ties to the even one, 6 at most.  A group that holds an infinity
+ *   or NaN reads back as 32 NaNs.  Keys that are turned on the way are held
+ *   in fp32 before they are coded.
+ * A page of K or V is slim_q4_page_bytes(kv_heads, page_size, head_dim) =
+ * kv_heads * page_size * head_dim * 17 / 32 bytes (0 for a rejected shape): all codes
+ * [kv_heads][page_size][head_dim / 2] (element 2 i of a row in the low four bits
+ * of byte i), then all scales [kv_heads][page_size / 16][head_dim / 32][16], e + 127 as a
+ * byte each (255: NaN), the 16 of consecutive positions.  A pool is [pages] of
+ * them, 16-byte aligned; slim_kv_copy_pages moves them as any others.
+ *
+ * slim_kv_append_q4   slim_kv_append_rope into such pools.  rotation NULL: keys as they
+ *                     are (Q and Qout must then be NULL)
+ * slim_kv_read_q4     the new tokens' keys and values (rows as those of slim_kv_append)
+ *                     from the pages back to rows of K and V, exact: every value that
+ *                     the codes stand for is one of the type.  Rows whose position has no page
+ *                     are zero, those of no sequence are not written
+ * slim_attention_decode_q4, slim_attention_prefill_q4
+ *                     slim_attention_decode and slim_attention_prefill over
+ *                     such pools, on the values the codes stand for; dtype is that of
+ *                     Q, O and the append.  Workspace: slim_attention_workspace_bytes
+ */
+size_t slim_q4_page_bytes(int64_t kv_heads, int64_t page_size, int64_t head_dim);
+slim_status slim_kv_append_q4(const uint16_t* Q, int64_t stride_Q, uint16_t* Qout, int64_t stride_Qout,
+                              int64_t q_heads, const uint16_t* K, int64_t stride_K, const uint16_t* V,
+                              int64_t stride_V, int64_t tokens, int64_t seqs, int64_t kv_heads, int64_t head_dim,
+                              int dtype, const int32_t* table, int64_t table_width, const int32_t* lens,
+                              const int32_t* starts, uint8_t* Kpool, uint8_t* Vpool, int64_t pages, int64_t page_size,
+                              const slim_rotation* rotation, hipStream_t stream);
+slim_status slim_kv_read_q4(uint16_t* K, int64_t stride_K, uint16_t* V, int64_t stride_V, int64_t tokens, int64_t seqs,
+                            int64_t kv_heads, int64_t head_dim, int dtype, const int32_t* table, int64_t table_width,
+                            const int32_t* lens, const int32_t* starts, const uint8_t* Kpool, const uint8_t* Vpool,
+                            int64_t pages, int64_t page_size, hipStream_t stream);
+slim_status slim_attention_decode_q4(const uint16_t* Q, int64_t stride_Q, uint16_t* O, int64_t stride_O, float* lse,
+                                     int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int dtype,
+                                     const uint8_t* Kpool, const uint8_t* Vpool, int64_t pages, int64_t page_size,
+                                     const int32_t* table, int64_t table_width, const int32_t* lens, int64_t max_len,
+                                     int64_t window, int64_t sinks, float scale, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream);
+slim_status slim_attention_prefill_q4(const uint16_t* Q, int64_t stride_Q, uint16_t* O, int64_t stride_O, float* lse,
+                                      int64_t tokens, int64_t seqs, int64_t q_heads, int64_t kv_heads,
+                                      int64_t head_dim, int dtype, const uint8_t* Kpool, const uint8_t* Vpool,
+                                      int64_t pages, int64_t page_size, const int32_t* table, int64_t table_width,
+                                      const int32_t* lens, const int32_t* starts, int64_t max_len, int64_t window,
+                                      int64_t sinks, float scale, void* workspace, size_t workspace_bytes,
+                                      hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

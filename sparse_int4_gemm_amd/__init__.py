@@ -18,8 +18,11 @@ from ._lib import (SlimError, slim_adapter_codes_bytes, slim_adapter_scales_byte
                    slim_transposed_values_bytes, slim_values_bytes, slim_linear_giveups,
                    slim_set_wait_limit, slim_quantize_input, slim_linear_a8_workspace_bytes, slim_linear_a8,
                    slim_pack_hybrid, slim_linear_hybrid, slim_kv_append, slim_kv_copy_pages,
-                   slim_attention_workspace_bytes, slim_attention_decode, slim_attention_prefill)
+                   slim_attention_workspace_bytes, slim_attention_decode, slim_attention_prefill, slim_rope,
+                   slim_kv_append_rope, slim_q4_page_bytes, slim_kv_append_q4, slim_kv_read_q4,
+                   slim_attention_decode_q4, slim_attention_prefill_q4)
 from .kv_cache import CacheFull, KVCache
+from .rotary import Rope, rope_frequencies
 
 GROUP = 128
 
@@ -35,7 +38,10 @@ __all__ = ["SlimError", "slim_pack", "slim_linear", "slim_linear_batched",
            "HybridWeight", "pack_hybrid", "linear_hybrid",
            "slim_kv_append", "slim_kv_copy_pages", "slim_attention_workspace_bytes", "slim_attention_decode",
            "slim_attention_prefill", "kv_append", "kv_copy_pages", "workspace_attention", "attention_decode",
-           "attention_prefill", "KVCache", "CacheFull"]
+           "attention_prefill", "KVCache", "CacheFull",
+           "slim_rope", "slim_kv_append_rope", "slim_q4_page_bytes", "slim_kv_append_q4", "slim_kv_read_q4",
+           "slim_attention_decode_q4", "slim_attention_prefill_q4", "Rope", "rope_frequencies", "rope",
+           "kv_append_rope", "kv_append_q4", "kv_read_q4", "attention_decode_q4", "attention_prefill_q4"]
 
 GROUP_L = 128          # quantised Lt: groups along K
 GROUP_R = 32           # quantised Rt: groups along r
@@ -238,7 +244,7 @@ def workspace_attention(tokens: int, seqs: int, q_heads: int, kv_heads: int, hea
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _attention_buffers(q, lens, kpool, ws, out, stream):
+def _attention_buffers(q, lens, kpool, ws, out, stream, head_dim=None):
     """Output and workspace of a call that was not given them, made on the
     stream that the call runs on (so that it, not the current one, owns them)."""
     if q.dim() != 3 or kpool.dim() != 4:
@@ -247,7 +253,7 @@ def _attention_buffers(q, lens, kpool, ws, out, stream):
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if ws is None:
-            ws = workspace_attention(q.shape[0], lens.shape[0], q.shape[1], kpool.shape[1], kpool.shape[3], device=q.device)
+            ws = workspace_attention(q.shape[0], lens.shape[0], q.shape[1], kpool.shape[1], head_dim or kpool.shape[3], device=q.device)
     return out, ws
 
 
@@ -281,4 +287,85 @@ def attention_prefill(q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor,
     if out is None or ws is None:
         out, ws = _attention_buffers(q, lens, kpool, ws, out, stream)
     slim_attention_prefill(q, out, kpool, vpool, table, lens, starts, ws, max_len, window, sinks, scale, lse, stream)
+    return out
+
+
+def _empty_like(x, stream):
+    """A tensor of x's shape, made on the stream that the call runs on."""
+    with torch.cuda.stream(stream):            # None: no change
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows x [tokens, heads, head_dim] (fp16 or bf16) turned to positions
+    int32 [tokens]; a negative position turns back.  out: may be x itself."""
+    if out is None:
+        out = _empty_like(x, stream)
+    slim_rope(x, out, positions, rope, stream=stream)
+    return out
+
+
+def kv_append_rope(K: torch.Tensor, V: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor, table: torch.Tensor,
+                   lens: torch.Tensor, rope: Rope, starts: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                   q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """kv_append with the keys turned to their positions on the way, and with
+    them the step's queries q [tokens, q_heads, head_dim], which are returned
+    (in q_out, which may be q itself)."""
+    if q is not None and q_out is None:
+        q_out = _empty_like(q, stream)
+    slim_kv_append_rope(q, q_out, K, V, kpool, vpool, table, lens, rope, starts, stream=stream)
+    return q_out
+
+
+def kv_append_q4(K: torch.Tensor, V: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor, table: torch.Tensor,
+                 lens: torch.Tensor, starts: torch.Tensor | None = None, rope: Rope | None = None,
+                 q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """kv_append_rope into pages of 4 bits a value: uint8 pools [pages, kv_heads,
+    page_size, head_dim * 17 / 32] (slim.h has the format).  rope None: keys as
+    they are, and no queries."""
+    if q is not None and q_out is None:
+        q_out = _empty_like(q, stream)
+    slim_kv_append_q4(q, q_out, K, V, kpool, vpool, table, lens, rope, starts, stream=stream)
+    return q_out
+
+
+def kv_read_q4(kpool: torch.Tensor, vpool: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+               starts: torch.Tensor | None = None, tokens: int | None = None, dtype: torch.dtype = torch.float16,
+               out: tuple[torch.Tensor, torch.Tensor] | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The last tokens of every sequence (starts as for kv_append; None: one
+    each) from pages of 4 bits: keys and values [tokens, kv_heads, head_dim] of
+    `dtype`, the type that they were appended in.  With starts, `tokens` is their number."""
+    if out is None:
+        if tokens is None:
+            if starts is not None:
+                raise ValueError("with starts the number of tokens must be given")
+            tokens = lens.shape[0]
+        if kpool.dim() != 4:
+            raise ValueError("the pools must be [pages, kv_heads, page_size, head_dim * 17 / 32]")
+        with torch.cuda.stream(stream):
+            out = tuple(torch.empty((tokens, kpool.shape[1], kpool.shape[3] // 17 * 32), dtype=dtype, device=kpool.device)
+                        for _ in range(2))
+    slim_kv_read_q4(out[0], out[1], kpool, vpool, table, lens, starts, stream=stream)
+    return out
+
+
+def attention_decode_q4(q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor, table: torch.Tensor,
+                        lens: torch.Tensor, max_len: int | None = None, window: int = 0, sinks: int = 0,
+                        scale: float | None = None, lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """attention_decode over pages of 4 bits (kv_append_q4)."""
+    if out is None or ws is None:
+        out, ws = _attention_buffers(q, lens, kpool, ws, out, stream, kpool.shape[-1] // 17 * 32)
+    slim_attention_decode_q4(q, out, kpool, vpool, table, lens, ws, max_len, window, sinks, scale, lse, stream)
+    return out
+
+
+def attention_prefill_q4(q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor, table: torch.Tensor,
+                         lens: torch.Tensor, starts: torch.Tensor | None, max_len: int | None = None, window: int = 0,
+                         sinks: int = 0, scale: float | None = None, lse: torch.Tensor | None = None,
+                         ws: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """attention_prefill over pages of 4 bits (kv_append_q4)."""
+    if out is None or ws is None:
+        out, ws = _attention_buffers(q, lens, kpool, ws, out, stream, kpool.shape[-1] // 17 * 32)
+    slim_attention_prefill_q4(q, out, kpool, vpool, table, lens, starts, ws, max_len, window, sinks, scale, lse, stream)
     return out

@@ -32,9 +32,17 @@ EXPORTED = (
     "slim_pack_hybrid", "slim_linear_hybrid",
     "slim_kv_append", "slim_kv_copy_pages", "slim_attention_workspace_bytes",
     "slim_attention_decode", "slim_attention_prefill",
+    "slim_rope", "slim_kv_append_rope", "slim_q4_page_bytes", "slim_kv_append_q4", "slim_kv_read_q4",
+    "slim_attention_decode_q4", "slim_attention_prefill_q4",
 )
 
 _lib = None
+
+
+class Rotation(ctypes.Structure):
+    """slim_rotation."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot_dim", ctypes.c_int64), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
 
 
 class SlimError(RuntimeError):
@@ -117,6 +125,21 @@ def load() -> ctypes.CDLL:
     lib.slim_attention_prefill.restype = ctypes.c_int
     lib.slim_attention_prefill.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i32, vp, vp, i64, i64, vp,
                                            i64, vp, vp, i64, i64, i64, f32, vp, sz, vp]
+    rotation = ctypes.POINTER(Rotation)
+    lib.slim_rope.restype = ctypes.c_int
+    lib.slim_rope.argtypes = [vp, i64, vp, i64, i64, i64, i64, i32, vp, rotation, vp]
+    lib.slim_q4_page_bytes.restype = sz
+    lib.slim_q4_page_bytes.argtypes = [i64, i64, i64]
+    for f in ("slim_kv_append_rope", "slim_kv_append_q4"):
+        getattr(lib, f).restype = ctypes.c_int
+        getattr(lib, f).argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, i64, i64, i64, i64, i64, i32, vp, i64, vp, vp, vp,
+                                    vp, i64, i64, rotation, vp]
+    lib.slim_kv_read_q4.restype = ctypes.c_int
+    lib.slim_kv_read_q4.argtypes = lib.slim_kv_append.argtypes
+    lib.slim_attention_decode_q4.restype = ctypes.c_int
+    lib.slim_attention_decode_q4.argtypes = lib.slim_attention_decode.argtypes
+    lib.slim_attention_prefill_q4.restype = ctypes.c_int
+    lib.slim_attention_prefill_q4.argtypes = lib.slim_attention_prefill.argtypes
     _lib = lib
     return lib
 
@@ -294,6 +317,7 @@ def slim_linear_hybrid(X, values, meta, scales, dvalues, dense, Lt, Rt, Y, works
 
 # ------------------------------------- paged key-value cache and attention
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+_PAGE_TYPES = (*_DTYPES, torch.uint8)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -327,12 +351,12 @@ def _ints(name, t, device, dims):
     return t.data_ptr(), shape
 
 
-def _pools(kpool, vpool, dims):
+def _pools(kpool, vpool, dims, dtypes=_DTYPES):
     """Device, shape, type and pointers of a pair of pools."""
     if not kpool.is_cuda:
         raise ValueError("tensors must live on the GPU (a ROCm 'cuda' device)")
     device, shape, dtype = kpool.device, kpool.shape, kpool.dtype
-    if dtype not in _DTYPES:
+    if dtype not in dtypes:
         raise TypeError("the pools must be float16 or bfloat16")
     if len(shape) not in dims or shape != vpool.shape or dtype is not vpool.dtype or device != vpool.device:
         raise ValueError(f"the pools must be two {' or '.join(map(str, dims))}-dimensional tensors of one shape, type "
@@ -380,15 +404,33 @@ def slim_kv_append(K, V, kpool, vpool, table, lens, starts=None, stream=None) ->
                                  pages, page, _stream_on(stream, dev)))
 
 
+def _q4_pools(kpool, vpool):
+    """Device, (pages, kv_heads, page_size, head_dim) and pointers of a pair of 4-bit pools."""
+    if not kpool.is_cuda:
+        raise ValueError("tensors must live on the GPU (a ROCm 'cuda' device)")
+    device, shape = kpool.device, kpool.shape
+    if kpool.dtype is not torch.uint8 or vpool.dtype is not torch.uint8:
+        raise TypeError("the pools must be uint8 [pages, kv_heads, page_size, head_dim * 17 / 32]")
+    if len(shape) != 4 or shape != vpool.shape or device != vpool.device:
+        raise ValueError("the pools must be two 4-dimensional tensors of one shape and device")
+    if not (kpool.is_contiguous() and vpool.is_contiguous()):
+        raise ValueError("the pools must be contiguous")
+    pages, heads, page, row = shape
+    if row % 17:
+        raise ValueError(f"a row of a 4-bit pool holds head_dim * 17 / 32 bytes, not {row}")
+    return device, (pages, heads, page, row // 17 * 32), kpool.data_ptr(), vpool.data_ptr()
+
+
 def slim_kv_copy_pages(kpool, vpool, src, dst, stream=None) -> None:
-    """Pages src[i] to dst[i] of every layer; pools [layers, pages, ...] or one layer's [pages, kv_heads, page_size, head_dim]."""
-    dev, shape, _, pkp, pvp = _pools(kpool, vpool, (4, 5))
+    """Pages src[i] to dst[i] of every layer; pools [layers, pages, ...] or one layer's
+    [pages, kv_heads, page_size, head_dim] (uint8: 4-bit pages)."""
+    dev, shape, dtype, pkp, pvp = _pools(kpool, vpool, (4, 5), _PAGE_TYPES)
     layers = shape[0] if len(shape) == 5 else 1
     pages, heads, page, dim = shape[-4:]
     (ps, (count,)), (pd, (to,)) = _ints("src", src, dev, 1), _ints("dst", dst, dev, 1)
     if count != to:
         raise ValueError(f"{count} sources and {to} destinations")
-    _check(load().slim_kv_copy_pages(pkp, pvp, layers, pages, heads * page * dim * 2, ps, pd, count,
+    _check(load().slim_kv_copy_pages(pkp, pvp, layers, pages, heads * page * dim * dtype.itemsize, ps, pd, count,
                                      _stream_on(stream, dev)))
 
 
@@ -396,10 +438,14 @@ def slim_attention_workspace_bytes(tokens: int, seqs: int, q_heads: int, kv_head
     return load().slim_attention_workspace_bytes(tokens, seqs, q_heads, kv_heads, head_dim)
 
 
-def _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace, max_len, window, sinks, scale, stream):
+def _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace, max_len, window, sinks, scale, stream, q4=False):
     """What both attention calls pass on: before seqs' place, from it to lens',
     and after.  max_len None: the table's capacity; scale None: 1 / sqrt(head_dim)."""
-    dev, (pages, kv_heads, page, dim), dtype, pk, pv = _pools(kpool, vpool, (4,))
+    if q4:
+        dev, (pages, kv_heads, page, dim), pk, pv = _q4_pools(kpool, vpool)
+        dtype = _half(Q, "Q")
+    else:
+        dev, (pages, kv_heads, page, dim), dtype, pk, pv = _pools(kpool, vpool, (4,))
     pq, sq, tokens, q_heads = _rows("Q", Q, None, dim, dtype, dev)
     po, so, o_tokens, _ = _rows("O", O, q_heads, dim, dtype, dev)
     if o_tokens != tokens:
@@ -434,3 +480,102 @@ def slim_attention_prefill(Q, O, kpool, vpool, table, lens, starts, workspace, m
     rows, tokens, cache, ps, rest = _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace, max_len,
                                                     window, sinks, scale, stream)
     _check(load().slim_attention_prefill(*rows, tokens, *cache, ps, *rest))
+
+
+def _half(t, name):
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    return t.dtype
+
+
+def _rotation(rope, device):
+    """slim_rotation of a Rope (kept by it), None of None."""
+    if rope is None:
+        return None
+    if rope.freqs.device != device:
+        raise ValueError(f"the rotation must be on {device}, got {rope.freqs.device}")
+    return rope.params
+
+
+def slim_rope(X, Y, positions, rope, stream=None) -> None:
+    """X, Y [tokens, heads, head_dim], positions int32 [tokens], rope: a Rope."""
+    if not X.is_cuda:
+        raise ValueError("tensors must live on the GPU (a ROCm 'cuda' device)")
+    if X.dim() != 3:
+        raise ValueError(f"X must be [tokens, heads, head_dim], got {tuple(X.shape)}")
+    dev, dtype = X.device, _half(X, "X")
+    px, sx, tokens, heads = _rows("X", X, None, X.shape[2], dtype, dev)
+    py, sy, y_tokens, _ = _rows("Y", Y, heads, X.shape[2], dtype, dev)
+    pp, (count,) = _ints("positions", positions, dev, 1)
+    if y_tokens != tokens or count != tokens:
+        raise ValueError(f"X has {tokens} rows, Y {y_tokens}, and there are {count} positions")
+    _check(load().slim_rope(px, sx, py, sy, tokens, heads, X.shape[2], _DTYPES[dtype], pp, _rotation(rope, dev),
+                            _stream_on(stream, dev)))
+
+
+def _append_args(K, V, heads, dim, dtype, dev):
+    pk, sk, tokens, _ = _rows("K", K, heads, dim, dtype, dev)
+    pv, sv, v_tokens, _ = _rows("V", V, heads, dim, dtype, dev)
+    if v_tokens != tokens:
+        raise ValueError(f"K has {tokens} rows and V {v_tokens}")
+    return pk, sk, pv, sv, tokens
+
+
+def _append(call, Q, Qout, K, V, pkp, pvp, pages, heads, page, dim, dtype, dev, table, lens, rope, starts, stream):
+    pk, sk, pv, sv, tokens = _append_args(K, V, heads, dim, dtype, dev)
+    queries = (None, 0, None, 0, 0)
+    if (Q is None) != (Qout is None):
+        raise ValueError("Q and Qout must both be given, or neither")
+    if Q is not None:
+        pq, sq, q_tokens, q_heads = _rows("Q", Q, None, dim, dtype, dev)
+        po, so, o_tokens, _ = _rows("Qout", Qout, q_heads, dim, dtype, dev)
+        if q_tokens != tokens or o_tokens != tokens:
+            raise ValueError(f"K has {tokens} rows, Q {q_tokens} and Qout {o_tokens}")
+        queries = (pq, sq, po, so, q_heads)
+    pt, pl, ps, seqs, width = _batch(table, lens, starts, tokens, dev)
+    _check(call(*queries, pk, sk, pv, sv, tokens, seqs, heads, dim, _DTYPES[dtype], pt, width, pl, ps, pkp, pvp, pages, page,
+                _rotation(rope, dev), _stream_on(stream, dev)))
+
+
+def slim_kv_append_rope(Q, Qout, K, V, kpool, vpool, table, lens, rope, starts=None, stream=None) -> None:
+    """slim_kv_append with the keys turned by rope, and Q [tokens, q_heads, head_dim] into Qout (or both None)."""
+    dev, (pages, heads, page, dim), dtype, pkp, pvp = _pools(kpool, vpool, (4,))
+    _append(load().slim_kv_append_rope, Q, Qout, K, V, pkp, pvp, pages, heads, page, dim, dtype, dev, table, lens, rope,
+            starts, stream)
+
+
+def slim_q4_page_bytes(kv_heads: int, page_size: int, head_dim: int) -> int:
+    return load().slim_q4_page_bytes(kv_heads, page_size, head_dim)
+
+
+def slim_kv_append_q4(Q, Qout, K, V, kpool, vpool, table, lens, rope=None, starts=None, stream=None) -> None:
+    """slim_kv_append_rope into uint8 pools [pages, kv_heads, page_size, head_dim * 17 / 32]; rope None: keys as they are."""
+    dev, (pages, heads, page, dim), pkp, pvp = _q4_pools(kpool, vpool)
+    _append(load().slim_kv_append_q4, Q, Qout, K, V, pkp, pvp, pages, heads, page, dim, _half(K, "K"), dev, table, lens,
+            rope, starts, stream)
+
+
+def slim_kv_read_q4(K, V, kpool, vpool, table, lens, starts=None, stream=None) -> None:
+    """The new tokens' keys and values from the pages to K, V [tokens, kv_heads, head_dim]."""
+    dev, (pages, heads, page, dim), pkp, pvp = _q4_pools(kpool, vpool)
+    dtype = _half(K, "K")
+    pk, sk, pv, sv, tokens = _append_args(K, V, heads, dim, dtype, dev)
+    pt, pl, ps, seqs, width = _batch(table, lens, starts, tokens, dev)
+    _check(load().slim_kv_read_q4(pk, sk, pv, sv, tokens, seqs, heads, dim, _DTYPES[dtype], pt, width, pl, ps, pkp, pvp,
+                                  pages, page, _stream_on(stream, dev)))
+
+
+def slim_attention_decode_q4(Q, O, kpool, vpool, table, lens, workspace, max_len: int, window: int = 0, sinks: int = 0,
+                             scale: float = 1.0, lse=None, stream=None) -> None:
+    """slim_attention_decode over 4-bit pools."""
+    rows, _, cache, _, rest = _attention_args(Q, O, lse, kpool, vpool, table, lens, None, workspace, max_len, window,
+                                              sinks, scale, stream, True)
+    _check(load().slim_attention_decode_q4(*rows, *cache, *rest))
+
+
+def slim_attention_prefill_q4(Q, O, kpool, vpool, table, lens, starts, workspace, max_len: int, window: int = 0,
+                              sinks: int = 0, scale: float = 1.0, lse=None, stream=None) -> None:
+    """slim_attention_prefill over 4-bit pools."""
+    rows, tokens, cache, ps, rest = _attention_args(Q, O, lse, kpool, vpool, table, lens, starts, workspace, max_len,
+                                                    window, sinks, scale, stream, True)
+    _check(load().slim_attention_prefill_q4(*rows, tokens, *cache, ps, *rest))

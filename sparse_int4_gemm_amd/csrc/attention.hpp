@@ -10,7 +10,7 @@ namespace slim {
 
 // One layer's pool and the sequences' places in it.
 struct PagedKV {
-    const uint16_t* k;       // [pages][kv_heads][1 << page_shift][head_dim]
+    const uint16_t* k;       // [pages][kv_heads][1 << page_shift][head_dim], or pages of 4 bits (kv_q4.hpp)
     const uint16_t* v;
     const int32_t* table;    // [seqs][width]
     const int32_t* lens;     // [seqs]
@@ -39,6 +39,33 @@ struct AppendArgs {
     int32_t tokens, kv_heads, head_dim;
 };
 
+// Rotary positions; half 0: none.
+struct Rotation {
+    const double* freqs;     // [half], radians a position
+    int32_t half;            // pairs of a head
+    int32_t interleaved;
+    double magnitude;
+};
+
+struct RopeArgs {
+    const uint16_t* x;  int64_t sx;
+    uint16_t* y;        int64_t sy;
+    const int32_t* positions;
+    int32_t tokens, heads, head_dim;
+    int32_t dtype;
+    Rotation by;
+};
+
+// New keys (turned on the way) and values to their pages, queries beside them.
+struct AppendRopeArgs {
+    AppendArgs to;
+    const uint16_t* q;  int64_t sq;      // NULL: none
+    uint16_t* q_out;    int64_t sqo;
+    int32_t q_heads;                     // 0 where q is NULL
+    int32_t dtype;
+    Rotation by;
+};
+
 // Workspace: the partial results of split key axes, for at most
 // kAttnSplitRows (row, split) pairs: a call splits its rows no further than
 // that, whatever its plan would be.
@@ -50,6 +77,14 @@ hipError_t launch_attention_prefill(const AttnArgs& a, hipStream_t stream);
 // Joins the partial results of a call's rows, `splits` each.
 hipError_t launch_attention_join(const AttnArgs& a, int splits, hipStream_t stream);
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream);
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
+hipError_t launch_kv_append_rope(const AppendRopeArgs& a, hipStream_t stream);
+// The same calls on pages of 4 bits.
+hipError_t launch_kv_append_q4(const AppendRopeArgs& a, hipStream_t stream);
+// k_new, v_new are written.
+hipError_t launch_kv_read_q4(const AppendArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_attention_decode_q4(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attention_prefill_q4(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_kv_copy_pages(void* k, void* v, int64_t layers, int64_t pages, int64_t page_bytes,
                                 const int32_t* src, const int32_t* dst, int64_t n, hipStream_t stream);
 

@@ -110,6 +110,61 @@ slim_status check_attention(const uint16_t* Q, int64_t stride_Q, uint16_t* O, in
     return slim::check_device();
 }
 
+// A rotation of heads of head_dim elements; fills *to.
+slim_status check_rotation(const slim_rotation* r, int64_t head_dim, slim::Rotation* to) {
+    if (!r) return fail(SLIM_EINVAL, "rotation is NULL");
+    if (r->rot_dim <= 0 || r->rot_dim % 8 || r->rot_dim > head_dim)
+        return fail(SLIM_EINVAL, "rot_dim must be a multiple of 8 from 8 to head_dim (got %lld)", (long long)r->rot_dim);
+    if (!r->freqs) return fail(SLIM_EINVAL, "freqs is NULL");
+    if (reinterpret_cast<uintptr_t>(r->freqs) & 7u) return fail(SLIM_EINVAL, "freqs must be 8-byte aligned");
+    if (r->interleaved != 0 && r->interleaved != 1) return fail(SLIM_EINVAL, "interleaved must be 0 or 1");
+    if (!(r->magnitude - r->magnitude == 0.0f)) return fail(SLIM_EINVAL, "magnitude must be finite");
+    to->freqs = r->freqs;
+    to->half = (int32_t)(r->rot_dim / 2);
+    to->interleaved = r->interleaved;
+    to->magnitude = (double)r->magnitude;
+    return SLIM_OK;
+}
+
+// Output rows that may be the input's.
+slim_status check_in_place(const char* what, const void* x, int64_t sx, const void* y, int64_t sy) {
+    if (x == y && sx != sy) return fail(SLIM_EINVAL, "%s in place needs one row stride", what);
+    return SLIM_OK;
+}
+
+// Everything that both appends with a rotation take; fills *a.
+slim_status check_append_rope(const uint16_t* Q, int64_t stride_Q, uint16_t* Qout, int64_t stride_Qout, int64_t q_heads,
+                              const uint16_t* K, int64_t stride_K, const uint16_t* V, int64_t stride_V, int64_t tokens,
+                              int64_t seqs, int64_t kv_heads, int64_t head_dim, const int32_t* table,
+                              int64_t table_width, const int32_t* lens, const int32_t* starts, const void* Kpool,
+                              const void* Vpool, int64_t pages, int64_t page_size, const slim_rotation* rotation,
+                              int dtype, slim::AppendRopeArgs* a) {
+    if (seqs == 0) return fail(SLIM_EINVAL, "tokens without sequences");
+    if (!Q != !Qout) return fail(SLIM_EINVAL, "Q and Qout must both be given, or neither");
+    slim_status st = check_rows("K", K, stride_K, tokens, kv_heads * head_dim);
+    if (st == SLIM_OK) st = check_rows("V", V, stride_V, tokens, kv_heads * head_dim);
+    if (st == SLIM_OK && Q) {
+        if (!rotation) return fail(SLIM_EINVAL, "Q without a rotation");
+        st = check_rows("Q", Q, stride_Q, tokens, q_heads * head_dim);
+        if (st == SLIM_OK) st = check_rows("Qout", Qout, stride_Qout, tokens, q_heads * head_dim);
+        if (st == SLIM_OK) st = check_in_place("Q", Q, stride_Q, Qout, stride_Qout);
+    }
+    a->by = slim::Rotation{nullptr, 0, 0, 1.0};
+    if (st == SLIM_OK && rotation) st = check_rotation(rotation, head_dim, &a->by);
+    if (st == SLIM_OK)
+        st = check_cache(seqs, kv_heads, head_dim, static_cast<const uint16_t*>(Kpool), static_cast<const uint16_t*>(Vpool),
+                         pages, page_size, table, table_width, lens, starts, &a->to.kv);
+    if (st != SLIM_OK) return st;
+    a->to.k_new = K; a->to.sk = stride_K;
+    a->to.v_new = V; a->to.sv = stride_V;
+    a->to.tokens = (int32_t)tokens; a->to.kv_heads = (int32_t)kv_heads; a->to.head_dim = (int32_t)head_dim;
+    a->q = Q; a->sq = stride_Q;
+    a->q_out = Qout; a->sqo = stride_Qout;
+    a->q_heads = Q ? (int32_t)q_heads : 0;
+    a->dtype = dtype;
+    return slim::check_device();
+}
+
 }  // namespace
 
 extern "C" {
@@ -196,6 +251,126 @@ slim_status slim_attention_prefill(const uint16_t* Q, int64_t stride_Q, uint16_t
                          workspace_bytes, &a);
     if (st != SLIM_OK) return st;
     return slim::launched(slim::launch_attention_prefill(a, stream), "slim_attention_prefill launch");
+}
+
+slim_status slim_rope(const uint16_t* X, int64_t stride_X, uint16_t* Y, int64_t stride_Y, int64_t tokens, int64_t heads,
+                      int64_t head_dim, int dtype, const int32_t* positions, const slim_rotation* rotation,
+                      hipStream_t stream) {
+    if (dtype != SLIM_FP16 && dtype != SLIM_BF16) return fail(SLIM_EUNSUPPORTED, "unknown dtype %d", dtype);
+    if (head_dim <= 0 || head_dim % 8 || head_dim > 1024)
+        return fail(SLIM_EUNSUPPORTED, "slim_rope: head_dim must be a multiple of 8 up to 1024 (got %lld)", (long long)head_dim);
+    if (tokens < 0 || tokens > kMaxTokens) return fail(SLIM_EINVAL, "tokens must be in [0, 2^22] (got %lld)", (long long)tokens);
+    if (heads <= 0 || heads > kMaxHeads) return fail(SLIM_EINVAL, "heads must be in [1, 1024] (got %lld)", (long long)heads);
+    slim::RopeArgs a;
+    slim_status st = check_rotation(rotation, head_dim, &a.by);
+    if (st != SLIM_OK) return st;
+    if (tokens == 0) return slim::done();
+    st = check_rows("X", X, stride_X, tokens, heads * head_dim);
+    if (st == SLIM_OK) st = check_rows("Y", Y, stride_Y, tokens, heads * head_dim);
+    if (st == SLIM_OK) st = check_in_place("X", X, stride_X, Y, stride_Y);
+    if (st != SLIM_OK) return st;
+    if (!positions || !aligned4(positions)) return fail(SLIM_EINVAL, "positions must be given, 4-byte aligned");
+    st = slim::check_device();
+    if (st != SLIM_OK) return st;
+    a.x = X; a.sx = stride_X;
+    a.y = Y; a.sy = stride_Y;
+    a.positions = positions;
+    a.tokens = (int32_t)tokens; a.heads = (int32_t)heads; a.head_dim = (int32_t)head_dim;
+    a.dtype = dtype;
+    return slim::launched(slim::launch_rope(a, stream), "slim_rope launch");
+}
+
+slim_status slim_kv_append_rope(const uint16_t* Q, int64_t stride_Q, uint16_t* Qout, int64_t stride_Qout, int64_t q_heads,
+                                const uint16_t* K, int64_t stride_K, const uint16_t* V, int64_t stride_V, int64_t tokens,
+                                int64_t seqs, int64_t kv_heads, int64_t head_dim, int dtype, const int32_t* table,
+                                int64_t table_width, const int32_t* lens, const int32_t* starts, uint16_t* Kpool,
+                                uint16_t* Vpool, int64_t pages, int64_t page_size, const slim_rotation* rotation,
+                                hipStream_t stream) {
+    slim_status st = check_shape(tokens, seqs, Q ? q_heads : kv_heads, kv_heads, head_dim, dtype);
+    if (st != SLIM_OK) return st;
+    if (!starts && tokens != seqs) return fail(SLIM_EINVAL, "slim_kv_append_rope: without starts tokens must equal seqs");
+    if (!rotation) return fail(SLIM_EINVAL, "rotation is NULL");
+    if (tokens == 0) return slim::done();
+    slim::AppendRopeArgs a;
+    st = check_append_rope(Q, stride_Q, Qout, stride_Qout, q_heads, K, stride_K, V, stride_V, tokens, seqs, kv_heads,
+                           head_dim, table, table_width, lens, starts, Kpool, Vpool, pages, page_size, rotation, dtype, &a);
+    if (st != SLIM_OK) return st;
+    return slim::launched(slim::launch_kv_append_rope(a, stream), "slim_kv_append_rope launch");
+}
+
+size_t slim_q4_page_bytes(int64_t kv_heads, int64_t page_size, int64_t head_dim) {
+    if (kv_heads <= 0 || kv_heads > kMaxHeads || page_shift(page_size) < 0 || !head_dim_ok(head_dim)) return 0;
+    return (size_t)(kv_heads * page_size * head_dim * 17 / 32);
+}
+
+slim_status slim_kv_append_q4(const uint16_t* Q, int64_t stride_Q, uint16_t* Qout, int64_t stride_Qout, int64_t q_heads,
+                              const uint16_t* K, int64_t stride_K, const uint16_t* V, int64_t stride_V, int64_t tokens,
+                              int64_t seqs, int64_t kv_heads, int64_t head_dim, int dtype, const int32_t* table,
+                              int64_t table_width, const int32_t* lens, const int32_t* starts, uint8_t* Kpool,
+                              uint8_t* Vpool, int64_t pages, int64_t page_size, const slim_rotation* rotation,
+                              hipStream_t stream) {
+    slim_status st = check_shape(tokens, seqs, Q ? q_heads : kv_heads, kv_heads, head_dim, dtype);
+    if (st != SLIM_OK) return st;
+    if (!starts && tokens != seqs) return fail(SLIM_EINVAL, "slim_kv_append_q4: without starts tokens must equal seqs");
+    if (tokens == 0) return slim::done();
+    slim::AppendRopeArgs a;
+    st = check_append_rope(Q, stride_Q, Qout, stride_Qout, q_heads, K, stride_K, V, stride_V, tokens, seqs, kv_heads,
+                           head_dim, table, table_width, lens, starts, Kpool, Vpool, pages, page_size, rotation, dtype, &a);
+    if (st != SLIM_OK) return st;
+    return slim::launched(slim::launch_kv_append_q4(a, stream), "slim_kv_append_q4 launch");
+}
+
+slim_status slim_kv_read_q4(uint16_t* K, int64_t stride_K, uint16_t* V, int64_t stride_V, int64_t tokens, int64_t seqs,
+                            int64_t kv_heads, int64_t head_dim, int dtype, const int32_t* table, int64_t table_width,
+                            const int32_t* lens, const int32_t* starts, const uint8_t* Kpool, const uint8_t* Vpool,
+                            int64_t pages, int64_t page_size, hipStream_t stream) {
+    slim_status st = check_shape(tokens, seqs, kv_heads, kv_heads, head_dim, dtype);
+    if (st != SLIM_OK) return st;
+    if (!starts && tokens != seqs) return fail(SLIM_EINVAL, "slim_kv_read_q4: without starts tokens must equal seqs");
+    if (tokens == 0) return slim::done();
+    slim::AppendRopeArgs a;
+    st = check_append_rope(nullptr, 0, nullptr, 0, 0, K, stride_K, V, stride_V, tokens, seqs, kv_heads, head_dim, table,
+                           table_width, lens, starts, Kpool, Vpool, pages, page_size, nullptr, dtype, &a);
+    if (st != SLIM_OK) return st;
+    return slim::launched(slim::launch_kv_read_q4(a.to, dtype, stream), "slim_kv_read_q4 launch");
+}
+
+slim_status slim_attention_decode_q4(const uint16_t* Q, int64_t stride_Q, uint16_t* O, int64_t stride_O, float* lse,
+                                     int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int dtype,
+                                     const uint8_t* Kpool, const uint8_t* Vpool, int64_t pages, int64_t page_size,
+                                     const int32_t* table, int64_t table_width, const int32_t* lens, int64_t max_len,
+                                     int64_t window, int64_t sinks, float scale, void* workspace, size_t workspace_bytes,
+                                     hipStream_t stream) {
+    slim_status st = check_shape(seqs, seqs, q_heads, kv_heads, head_dim, dtype);
+    if (st != SLIM_OK) return st;
+    if (seqs == 0) return slim::done();
+    slim::AttnArgs a;
+    st = check_attention(Q, stride_Q, O, stride_O, lse, seqs, seqs, q_heads, kv_heads, head_dim, dtype,
+                         reinterpret_cast<const uint16_t*>(Kpool), reinterpret_cast<const uint16_t*>(Vpool), pages,
+                         page_size, table, table_width, lens, nullptr, max_len, window, sinks, scale, workspace,
+                         workspace_bytes, &a);
+    if (st != SLIM_OK) return st;
+    return slim::launched(slim::launch_attention_decode_q4(a, stream), "slim_attention_decode_q4 launch");
+}
+
+slim_status slim_attention_prefill_q4(const uint16_t* Q, int64_t stride_Q, uint16_t* O, int64_t stride_O, float* lse,
+                                      int64_t tokens, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                      int dtype, const uint8_t* Kpool, const uint8_t* Vpool, int64_t pages,
+                                      int64_t page_size, const int32_t* table, int64_t table_width, const int32_t* lens,
+                                      const int32_t* starts, int64_t max_len, int64_t window, int64_t sinks, float scale,
+                                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    slim_status st = check_shape(tokens, seqs, q_heads, kv_heads, head_dim, dtype);
+    if (st != SLIM_OK) return st;
+    if (!starts && tokens != seqs)
+        return fail(SLIM_EINVAL, "slim_attention_prefill_q4: without starts tokens must equal seqs");
+    if (tokens == 0) return slim::done();
+    slim::AttnArgs a;
+    st = check_attention(Q, stride_Q, O, stride_O, lse, tokens, seqs, q_heads, kv_heads, head_dim, dtype,
+                         reinterpret_cast<const uint16_t*>(Kpool), reinterpret_cast<const uint16_t*>(Vpool), pages,
+                         page_size, table, table_width, lens, starts, max_len, window, sinks, scale, workspace,
+                         workspace_bytes, &a);
+    if (st != SLIM_OK) return st;
+    return slim::launched(slim::launch_attention_prefill_q4(a, stream), "slim_attention_prefill_q4 launch");
 }
 
 }  // extern "C"

@@ -71,27 +71,6 @@ __device__ __forceinline__ void load_tile(Tile<D>& x, const AttnArgs& a, int kvh
     }
 }
 
-// The sequence in place `rank` when those of every 64 are taken longest first,
-// in sixteen classes of length up to `most` (a class's in their own order): a
-// load, and a ballot for each class down to the answer's.
-__device__ __forceinline__ int longest_first(const PagedKV& kv, int rank, int most) {
-    const int lane = threadIdx.x & 63, base = rank & ~63;
-    const int len = seq_len(kv, min(base + lane, kv.seqs - 1));
-    const int of = min((int)((float)len * (16.0f / (float)most)), 15);
-    int left = rank & 63;
-    uint64_t found = 0;
-    for (int c = 15; c >= 0; --c) {
-        found = __ballot(base + lane < kv.seqs && of == c);
-        const int n = __builtin_popcountll(found);
-        if (left < n) break;
-        left -= n;
-    }
-    // The left-th of the class.
-    const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(found >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)found, 0));
-    const uint64_t at = __ballot((found >> lane & 1) && before == left);
-    return base + (at == 0 ? 0 : __builtin_ctzll(at));
-}
-
 template <class T, int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_kernel(AttnArgs a, int splits, int chunk,
                                                                           int groups, int sort_most) {

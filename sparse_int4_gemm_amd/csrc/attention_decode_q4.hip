@@ -1,0 +1,351 @@
+// slim_attention_decode_q4: attention of one new token per sequence over pages
+// of 4 bits a value (attention_decode.hip has the mathematics; kv_q4.hpp the
+// format).
+//
+//   s_j = scale q . k_j,  O = sum_j 2^(c s_j - m) v_j / l.
+//
+// Each wave streams tiles of 32 keys into registers, codes as they lie in the
+// pages, a tile ahead of the one it computes on, and turns them into halves on
+// the way into the matrix products: one instruction for every two values, with
+// their scale (4.5 cycles a wave and pair, as a byte permute).
+//  - Keys: lane (c, g) = (lane % 16, lane / 16) holds a quarter of key c's
+//    elements, [D/4 g, D/4 (g + 1)), 16 bytes at head size 128, and eight of them
+//    are its slots of one 16 x 16 x 32 product; queries lie the same way.
+//  - Values: lane (c, g) holds D/16 elements of the four keys 4 g + i of each half
+//    tile, whose weights it has already; two keys' elements are paired by a
+//    byte permute as in attention_decode.hip.
+//  - A half tile's scales are 16 bytes for each group of 32 elements: a byte a
+//    lane for the keys, the four keys' dword for the values.
+#include "kv_q4.hpp"
+
+namespace slim {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kTile = 32;            // keys of one wave's step
+
+struct Place {
+    int base, page[2];               // first key, pages of the 16-key halves (-1: none)
+};
+
+// Groups of 32 that a lane's elements of a key (D/4 from D/4 g on) lie in:
+// the first, and where D/4 is no part of 32 (head sizes 96, 256) a second.
+template <int D>
+struct KeyGroups {
+    static constexpr int kTwo = D == 96 || D == 256;
+    static __device__ __forceinline__ int first(int g) { return D / 4 * g / 32; }
+    static __device__ __forceinline__ int last(int g) { return (D / 4 * (g + 1) - 1) / 32; }
+    // Whether chunk i of eight elements lies in the last.
+    static __device__ __forceinline__ bool in_last(int g, int i) { return (D / 4 * g + 8 * i) / 32 != first(g); }
+};
+// The same of its elements of a value (D/16 from D/16 c on).
+template <int D>
+struct ValueGroups {
+    static constexpr int kTwo = D == 96;
+    static __device__ __forceinline__ int first(int c) { return D / 16 * c / 32; }
+    static __device__ __forceinline__ int last(int c) { return (D / 16 * (c + 1) - 1) / 32; }
+    static __device__ __forceinline__ bool in_last(int c, int e) { return (D / 16 * c + e) / 32 != first(c); }
+};
+
+// The registers of one tile.
+template <int D>
+struct Tile {
+    static constexpr int kV = D == 256 ? 2 : 1;          // dwords that hold D/32 bytes
+    uint32_t k[2][D / 32];
+    uint32_t v[2][4][kV];
+    uint32_t ks[2][2], vs[2][2];             // scales: a byte (first, last group); four keys' bytes
+    Place at;
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(Tile<D>& x, const AttnArgs& a, int kvh, const Place& at) {
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    x.at = at;
+    const unsigned char *kp = reinterpret_cast<const unsigned char*>(a.kv.k), *vp = reinterpret_cast<const unsigned char*>(a.kv.v);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const Q4Row row(max(at.page[t], 0), a.kv_heads, a.kv.page_shift, D, kvh,
+                        (at.base + 16 * t) & ((1 << a.kv.page_shift) - 1));
+        const uint32_t* k = reinterpret_cast<const uint32_t*>(kp + row.codes + c * (D / 2) + g * (D / 8));
+        if constexpr (D == 96) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) x.k[t][i] = k[i];
+        } else {
+            load_words<D / 32>(x.k[t], reinterpret_cast<const uint16_t*>(k));
+        }
+        const unsigned char* ks = kp + row.scales + c;
+        x.ks[t][0] = ks[16 * KeyGroups<D>::first(g)];
+        if constexpr (KeyGroups<D>::kTwo) x.ks[t][1] = ks[16 * KeyGroups<D>::last(g)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const unsigned char* v = vp + row.codes + (4 * g + i) * (D / 2) + c * (D / 32);
+            if constexpr (D == 64) x.v[t][i][0] = *reinterpret_cast<const uint16_t*>(v);
+            else if constexpr (D == 96) x.v[t][i][0] = v[0] | v[1] << 8 | v[2] << 16;
+            else load_words<Tile<D>::kV>(x.v[t][i], reinterpret_cast<const uint16_t*>(v));
+        }
+        const unsigned char* vs = vp + row.scales + 4 * g;
+        x.vs[t][0] = *reinterpret_cast<const uint32_t*>(vs + 16 * ValueGroups<D>::first(c));
+        if constexpr (ValueGroups<D>::kTwo) x.vs[t][1] = *reinterpret_cast<const uint32_t*>(vs + 16 * ValueGroups<D>::last(c));
+    }
+}
+
+template <class T, int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_q4_kernel(AttnArgs a, int splits, int chunk, int groups,
+                                                                             int sort_most) {
+    constexpr int VE = D / 16;
+    __shared__ float o_join[kWaves][16][D + 4];
+    __shared__ float m_join[kWaves][16], l_join[kWaves][16];
+    __shared__ uint32_t bad_join[kWaves];        // a bit for each row that is not finite
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    int split, b, unit;                  // unit: key head and group of 16 query heads
+    if (sort_most) {
+        // Longest sequences first, with all their heads (not split: see launch).
+        const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x, rank = id / gridDim.y;
+        unit = (int)(id - rank * gridDim.y);
+        split = 0;
+        b = __builtin_amdgcn_readfirstlane(longest_first(a.kv, (int)rank, sort_most));
+    } else {
+        split = blockIdx.x % splits;
+        b = blockIdx.x / splits;
+        unit = blockIdx.y;
+    }
+    const int kvh = unit / groups, share = a.q_heads / a.kv_heads;
+    const int h0 = kvh * share + (unit - kvh * groups) * 16;                   // this workgroup's query heads
+    const int heads = min(16, (kvh + 1) * share - h0);
+
+    const Span span = key_span(a, seq_len(a.kv, b) - 1);
+    const int tiles = span.tiles(kTile);
+    // At least `chunk` tiles a workgroup, more where the length passes what was planned for.
+    const int per = max(chunk, (tiles + splits - 1) / splits);
+    const int active = max(1, (tiles + per - 1) / per);
+    const int64_t row0 = (int64_t)b * a.q_heads + h0;
+    const Partials parts(a, D, splits);
+    if (split >= active) {
+        if ((int)threadIdx.x < heads) parts.mark(row0 + threadIdx.x, split, -INFINITY, 0.0f);
+        return;
+    }
+    const int first = split * per, last = min(tiles, first + per);
+
+    // Slots of product i: elements D/4 g + 8 i + [0, 8).
+    u4 qf[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        qf[i] = u4{0, 0, 0, 0};
+        if (c < heads) qf[i] = *reinterpret_cast<const u4*>(a.q + b * a.sq + (int64_t)(h0 + c) * D + D / 4 * g + 8 * i);
+    }
+    const float scale = a.scale * 1.4426950408889634f;
+    float m = -INFINITY, l = 0.0f;
+    f4 o[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) o[e] = f4{0, 0, 0, 0};
+
+    auto step = [&](Tile<D>& x) {
+        f4 s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t] = f4{0, 0, 0, 0};
+            const float first_scale = q4_scale(x.ks[t][0]);
+            float last_scale = first_scale;
+            if constexpr (KeyGroups<D>::kTwo) last_scale = q4_scale(x.ks[t][1]);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                s[t] = T::mfma16(q4_values<T>(x.k[t][i], KeyGroups<D>::in_last(g, i) ? last_scale : first_scale), qf[i], s[t]);
+            s[t] *= scale;
+        }
+        // A tile whose every key is seen and owned needs no mask (the same answer in all lanes).
+        if (!(span.all_seen(x.at.base, kTile) && x.at.page[0] >= 0 && x.at.page[1] >= 0)) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool seen = x.at.page[t] >= 0 && span.seen(x.at.base + 16 * t + 4 * g + i);
+                    if (!seen) {
+                        s[t][i] = -INFINITY;
+                        // What lies there must not reach 0 * v: codes of 0, and no scale that makes NaN of them.
+#pragma unroll
+                        for (int e = 0; e < Tile<D>::kV; ++e) x.v[t][i][e] = 0;
+                        x.vs[t][0] &= ~(0xFFu << 8 * i);
+                        if constexpr (ValueGroups<D>::kTwo) x.vs[t][1] &= ~(0xFFu << 8 * i);
+                    }
+                }
+        }
+        float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                          fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top - T::kTop);            // the largest weight is 2^kTop
+        const float ms = mn == -INFINITY ? 0.0f : mn;        // nothing seen so far: all weights are 2^-inf = 0
+        const float f = exp2_fast(m - ms);
+        m = mn;
+        float w[8], sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            w[j] = exp2_fast(s[j >> 2][j & 3] - ms);
+            sum += w[j];
+        }
+        l = l * f + sum;
+        u4 hi, lo;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            hi[j] = T::pack(w[2 * j], w[2 * j + 1]);
+            lo[j] = T::pack(w[2 * j] - T::low(hi[j]), w[2 * j + 1] - T::high(hi[j]));
+        }
+        float vs[8], vs_last[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            vs[j] = q4_scale(x.vs[j >> 2][0] >> 8 * (j & 3) & 0xFFu);
+            if constexpr (ValueGroups<D>::kTwo) vs_last[j] = q4_scale(x.vs[j >> 2][1] >> 8 * (j & 3) & 0xFFu);
+        }
+        // Elements e and e + 1 of a lane's: two keys' pairs, then their low and their high halves side by side.
+        auto two = [&](auto byte, int word) {
+            constexpr int e = 2 * decltype(byte)::value;
+            u4 lows, highs;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t p[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int key = 2 * j + y;
+                    float by = vs[key];
+                    if constexpr (ValueGroups<D>::kTwo) by = ValueGroups<D>::in_last(c, e) ? vs_last[key] : by;
+                    p[y] = q4_pair<T, e / 2>(x.v[key >> 2][key & 3][word], by);
+                }
+                lows[j] = __builtin_amdgcn_perm(p[1], p[0], 0x05040100u);
+                highs[j] = __builtin_amdgcn_perm(p[1], p[0], 0x07060302u);
+            }
+            f4 &even = o[8 * word + e], &odd = o[8 * word + e + 1];
+            even = T::mfma16(lows, lo, T::mfma16(lows, hi, even * f));
+            odd = T::mfma16(highs, lo, T::mfma16(highs, hi, odd * f));
+        };
+#pragma unroll
+        for (int word = 0; word < Tile<D>::kV; ++word) {
+            two(std::integral_constant<int, 0>{}, word);
+            two(std::integral_constant<int, 1>{}, word);
+            if constexpr (VE > 4) two(std::integral_constant<int, 2>{}, word);
+            if constexpr (VE > 6) two(std::integral_constant<int, 3>{}, word);
+        }
+    };
+
+    // Two tiles in flight: the next one's loads are issued before the current
+    // one is used, with the pages of the one after it.
+    const int keys = max(0, span.end);
+    auto place = [&](int i) {
+        Place at;
+        at.base = __builtin_amdgcn_readfirstlane(span.base(min(i, last - 1), kTile));
+        at.page[0] = page_of(a, b, at.base, keys);
+        at.page[1] = page_of(a, b, at.base + 16, keys);
+        return at;
+    };
+    int i = first + wave;
+    if (i < last) {
+        Place next = place(i);
+        Tile<D> x, y;
+        load_tile<D>(x, a, kvh, next);
+        next = place(i + kWaves);
+        for (;;) {
+            load_tile<D>(y, a, kvh, next);
+            next = place(i + 2 * kWaves);
+            step(x);
+            i += kWaves;
+            if (i >= last) break;
+            load_tile<D>(x, a, kvh, next);
+            next = place(i + 2 * kWaves);
+            step(y);
+            i += kWaves;
+            if (i >= last) break;
+        }
+    }
+
+    // Join the waves: a lane's o[e][r] is O^T of query c at d = (D/16)(4 g + r) + e.
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) {
+        m_join[wave][c] = m;
+        l_join[wave][c] = l;
+    }
+    if (c < heads) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) o_join[wave][c][VE * (4 * g + r) + e] = o[e][r];
+    }
+    f4 probe = f4{0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < VE; ++e) probe += o[e] * 0.0f;
+    const uint64_t odd = __ballot(c < heads && !(probe[0] + probe[1] + probe[2] + probe[3] == 0.0f));
+    if (lane == 0) bad_join[wave] = (uint32_t)(odd | odd >> 16 | odd >> 32 | odd >> 48) & 0xFFFFu;
+    __syncthreads();
+    static_assert(kWaves == 4, "the waves' rows below");
+    const uint32_t bad = __builtin_amdgcn_readfirstlane(bad_join[0] | bad_join[1] | bad_join[2] | bad_join[3]);
+    for (int at = threadIdx.x; at < heads * (D / 4); at += 64 * kWaves) {
+        const int r = at / (D / 4), d = (at - r * (D / 4)) * 4;
+        if (bad >> r & 1) continue;
+        float top = m_join[0][r];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, m_join[w][r]);
+        const float ms = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f;
+        f4 acc = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float f = exp2_fast(m_join[w][r] - ms);
+            sum += l_join[w][r] * f;
+            acc += *reinterpret_cast<const f4*>(&o_join[w][r][d]) * f;
+        }
+        if (active == 1) {
+            store_row4<T>(a, b, h0 + r, D, d, acc, top, sum);
+            if (splits > 1 && d == 0) parts.mark(row0 + r, 0, top, kWhole);
+        } else {
+            parts.put4(row0 + r, split, d, acc);
+            if (d == 0) parts.mark(row0 + r, split, top, sum);
+        }
+    }
+    for (int r = wave; r < heads; r += kWaves) {
+        if (!(bad >> r & 1)) continue;
+        float x[4], top, sum;
+        plain_row<D, kTile, Q4Rows<D>>(a, span, first, last, span, a.kv.table + (int64_t)b * a.kv.width, kvh,
+                                       a.q + b * a.sq + (int64_t)(h0 + r) * D, x, top, sum);
+        store_plain_row<T, D>(a, parts, active > 1, b, h0 + r, split, x, top, sum);
+        if (active == 1 && splits > 1 && lane == 0) parts.mark(row0 + r, 0, top, kWhole);
+    }
+}
+
+// As attention_decode.hip's plan.
+constexpr int kSplitTarget = 512, kMinTiles = 16, kSortFrom = 512;
+
+template <class T, int D>
+hipError_t launch(const AttnArgs& a, hipStream_t stream) {
+    const int share = a.q_heads / a.kv_heads, groups = (share + 15) / 16;
+    int64_t most = (int64_t)a.max_len;
+    if (a.window && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;
+    const int tiles = (int)((most + kTile - 1) / kTile);
+    const int64_t units = (int64_t)a.tokens * a.kv_heads * groups;
+    const int64_t want = min(kSplitTarget / units, (int64_t)((tiles + kMinTiles - 1) / kMinTiles));
+    const int splits = (int)max((int64_t)1, min(want, kAttnSplitRows / ((int64_t)a.tokens * a.q_heads)));
+    const int chunk = max(kWaves, (tiles + splits - 1) / splits);
+    dim3 grid((unsigned)(a.tokens * splits), (unsigned)(a.kv_heads * groups));
+    const int sort_most = units > kSplitTarget && most >= kSortFrom ? (int)most : 0;
+    hipLaunchKernelGGL((attention_decode_q4_kernel<T, D>), grid, dim3(64 * kWaves), 0, stream, a, splits, chunk, groups,
+                       sort_most);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || splits == 1 ? e : launch_attention_join(a, splits, stream);
+}
+
+template <class T>
+hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
+    switch (a.head_dim) {
+        case 64: return launch<T, 64>(a, stream);
+        case 96: return launch<T, 96>(a, stream);
+        case 128: return launch<T, 128>(a, stream);
+        default: return launch<T, 256>(a, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_attention_decode_q4(const AttnArgs& a, hipStream_t stream) {
+    return a.dtype == 0 ? launch_dim<Fp16>(a, stream) : launch_dim<Bf16>(a, stream);
+}
+
+}  // namespace slim

@@ -120,13 +120,28 @@ __device__ __forceinline__ float half_value(const AttnArgs& a, uint16_t x) {
     return a.dtype == 0 ? (float)__builtin_bit_cast(_Float16, x) : __builtin_bit_cast(float, (uint32_t)x << 16);
 }
 
+// Rows of halves as plain_row reads them, an element at a time: `at` finds a
+// key's row in both pools, `of_lane` another lane's.
+template <int D>
+struct HalfRows {
+    typedef int64_t At;
+    static __device__ __forceinline__ At at(const AttnArgs& a, int page, int kvh, int r) {
+        return ((((int64_t)page * a.kv_heads + kvh) << a.kv.page_shift) + r) * D;
+    }
+    static __device__ __forceinline__ At none() { return 0; }
+    static __device__ __forceinline__ At of_lane(At at, int lane) { return __shfl(at, lane); }
+    static __device__ __forceinline__ float value(const AttnArgs& a, const uint16_t* pool, At at, int d) {
+        return half_value(a, pool[at + d]);
+    }
+};
+
 // One row over tiles [first, last) of `tiles` (KEYS keys each, at most 64) by
 // the whole wave, straight from the formula: lane j scores key j of each tile, then owns
 // the output elements lane + 64 i.  For rows that an infinity or NaN has
 // reached in the matrix products, where it also meets weights of 0 and of
 // either sign: here only keys that the row sees, and each with its weight.  A key
 // at a time: some hundred times slower than the products.
-template <int D, int KEYS>
+template <int D, int KEYS, class Rows = HalfRows<D>>
 __device__ void plain_row(const AttnArgs& a, const Span& tiles, int first, int last, const Span& row_span,
                           const int32_t* table, int kvh, const uint16_t* q, float (&o)[4], float& m, float& l) {
     const int lane = threadIdx.x & 63;
@@ -140,12 +155,11 @@ __device__ void plain_row(const AttnArgs& a, const Span& tiles, int first, int l
         int page = -1;
         if (seen) page = table[j >> a.kv.page_shift];
         seen = seen && page >= 0 && page < a.kv.pages;
-        const int64_t at = seen ? ((((int64_t)page * a.kv_heads + kvh) << a.kv.page_shift) +
-                                   (j & ((1 << a.kv.page_shift) - 1))) * D : 0;
+        const typename Rows::At at = seen ? Rows::at(a, page, kvh, j & ((1 << a.kv.page_shift) - 1)) : Rows::none();
         float s = -INFINITY;
         if (seen) {
             s = 0.0f;
-            for (int d = 0; d < D; ++d) s = fmaf(half_value(a, q[d]), half_value(a, a.kv.k[at + d]), s);
+            for (int d = 0; d < D; ++d) s = fmaf(half_value(a, q[d]), Rows::value(a, a.kv.k, at, d), s);
             s *= scale;
         }
         float top = s;
@@ -158,12 +172,33 @@ __device__ void plain_row(const AttnArgs& a, const Span& tiles, int first, int l
         for (uint64_t left = __ballot(seen); left; left &= left - 1) {
             const int k = __builtin_ctzll(left);
             const float wk = __shfl(w, k);
-            const int64_t r = __shfl(at, k);
+            const typename Rows::At r = Rows::of_lane(at, k);
             l += wk;
             for (int i = 0; i < 4; ++i)
-                if (lane + 64 * i < D) o[i] = fmaf(wk, half_value(a, a.kv.v[r + lane + 64 * i]), o[i]);
+                if (lane + 64 * i < D) o[i] = fmaf(wk, Rows::value(a, a.kv.v, r, lane + 64 * i), o[i]);
         }
     }
+}
+
+// The sequence in place `rank` when those of every 64 are taken longest first,
+// in sixteen classes of length up to `most` (a class's in their own order): a
+// load, and a ballot for each class down to the answer's.
+__device__ __forceinline__ int longest_first(const PagedKV& kv, int rank, int most) {
+    const int lane = threadIdx.x & 63, base = rank & ~63;
+    const int len = seq_len(kv, min(base + lane, kv.seqs - 1));
+    const int of = min((int)((float)len * (16.0f / (float)most)), 15);
+    int left = rank & 63;
+    uint64_t found = 0;
+    for (int c = 15; c >= 0; --c) {
+        found = __ballot(base + lane < kv.seqs && of == c);
+        const int n = __builtin_popcountll(found);
+        if (left < n) break;
+        left -= n;
+    }
+    // The left-th of the class.
+    const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(found >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)found, 0));
+    const uint64_t at = __ballot((found >> lane & 1) && before == left);
+    return base + (at == 0 ? 0 : __builtin_ctzll(at));
 }
 
 // Writes four elements of an output row, and lse with the first of them.

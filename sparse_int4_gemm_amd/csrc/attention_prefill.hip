@@ -37,7 +37,7 @@
 // bf16: 391 to 403 us on different cards, 1.02 to 1.05 PFLOP/s (a library
 // product of 8192^3: 1.40 to 1.45); 719 thousand cycles, so 1.8 GHz over the call,
 // of which the matrix unit is busy for 57% and the vector unit for 55%.
-#include "attention_device.hpp"
+#include "kv_q4.hpp"
 
 namespace slim {
 namespace {
@@ -94,9 +94,11 @@ struct Grid {
     int32_t slots, slot0, chunk, round;
 };
 
-template <class T, int D, int KG>
+// Q4: keys and values lie in the pages as 4 bits each (kv_q4.hpp).
+template <class T, int D, int KG, bool Q4>
 __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG == 1 ? 3 : 2) void attention_prefill_kernel(
     AttnArgs a, Grid grid) {
+    typedef std::conditional_t<Q4, Q4Rows<D>, HalfRows<D>> Rows;
     constexpr int kTileBytes = kKeys * D * 2;
     constexpr int kLoads = D / 32;                       // quads of a row, 64-lane loads of a 16-row block
     __shared__ __align__(1024) unsigned char lds[KG][2][2][kTileBytes];         // [group][buffer][K, V]
@@ -205,7 +207,7 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     // block w of K and of V.  Lane j holds it for tile from + j: a table entry looked up for
     // each tile would be waited for each time.
     const int row_mask = (1 << a.kv.page_shift) - 1;
-    int at_lo = 0, at_hi = 0, blocks = 0, from = first;
+    int at_lo = 0, at_hi = 0, to_scales = 0, blocks = 0, from = first;
     auto base_of = [&](int t) {
         t = begin + group + KG * t;
         return (t < sink_tiles ? t : t + window_tile) * kKeys;
@@ -225,21 +227,27 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
             blocks |= is ? 1 << i : 0;
             if (i == wave) {
                 const int key = base + 16 * i;
-                const int64_t at = ((((int64_t)(is ? page[i] : 0) * a.kv_heads + kvh) << a.kv.page_shift) +
-                                    (key & row_mask)) * (D * 2);
+                int64_t at = ((((int64_t)(is ? page[i] : 0) * a.kv_heads + kvh) << a.kv.page_shift) +
+                              (key & row_mask)) * (D * 2);
+                if constexpr (Q4) {
+                    const Q4Row row(is ? page[i] : 0, a.kv_heads, a.kv.page_shift, D, kvh, key & row_mask);
+                    at = row.codes;
+                    to_scales = (int)(row.scales - row.codes);
+                }
                 at_lo = (int)at;
                 at_hi = (int)(at >> 32);
                 blocks |= is ? max(0, min(16, keys - key)) << 4 : 0;
             }
         }
     };
-    struct Place { int base, blocks, lo, hi; };
+    struct Place { int base, blocks, lo, hi, to_scales; };
     auto place = [&](int t) {
         Place x;
         x.base = base_of(t);
         x.blocks = __builtin_amdgcn_readlane(blocks, t - from);
         x.lo = __builtin_amdgcn_readlane(at_lo, t - from);
         x.hi = __builtin_amdgcn_readlane(at_hi, t - from);
+        if constexpr (Q4) x.to_scales = __builtin_amdgcn_readlane(to_scales, t - from);
         return x;
     };
     // Load j takes quad j of a 16-row block, 4 lanes a row.
@@ -265,11 +273,60 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         for (int n = 0; n < kLoads; ++n) load_piece(is_v, s, n);
     };
 
+    // 4 bits: the codes of a 16-row block, lane (row, quad) = (lane % 16, lane / 16)
+    // a quad's 16 bytes and its scale (at head size 64 half of them, at 96 the last
+    // quad twice, at 256 two quads), pass through registers, and from there into
+    // the places that the loads above bring halves to, 16 consecutive lanes' into
+    // 16 different bank groups - also those of V, which is turned as K is then.
+    constexpr int kQuads = Q4 && D == 256 ? 2 : 1, kWords = Q4 && D == 64 ? 2 : 4;
+    constexpr int kPieces = Q4 ? kQuads * kWords : 1;            // dwords of codes, 16-byte chunks of halves
+    struct Raw { uint32_t codes[kQuads][kWords], scale[kQuads]; };
+    Raw raw_k, raw_v;
+    const int q4_row = lane & 15, q4_quad = D == 64 ? lane >> 5 : D == 96 ? min(lane >> 4, 2) : lane >> 4;
+    const int q4_part = D == 64 ? (lane >> 4 & 1) * 8 : 0;       // of the quad's codes, bytes
+    auto fetch = [&](bool is_v, const Place& x, bool any) {
+        const unsigned char* pool = reinterpret_cast<const unsigned char*>(is_v ? a.kv.v : a.kv.k) +
+                                    (int64_t)((uint64_t)(uint32_t)x.lo | (uint64_t)(uint32_t)x.hi << 32);
+        const int rows_of = any ? x.blocks >> 4 : 0;
+        const __amdgpu_buffer_rsrc_t codes = make_rsrc(pool, rows_of * (D / 2));
+        const __amdgpu_buffer_rsrc_t scales = make_rsrc(pool + x.to_scales, D / 2);
+        Raw& to = is_v ? raw_v : raw_k;
+#pragma unroll
+        for (int j = 0; j < kQuads; ++j) {
+            const int at = q4_row * (D / 2) + (q4_quad + 4 * j) * 16 + q4_part;
+            if constexpr (kWords == 2) {
+                const u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_raw_buffer_load_b64(codes, at, 0, 0));
+                to.codes[j][0] = w[0];
+                to.codes[j][1] = w[1];
+            } else {
+                const u4 w = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(codes, at, 0, 0));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to.codes[j][i] = w[i];
+            }
+            // (Rows past the end: codes of 0, and no scale that makes NaN of them.)
+            to.scale[j] = __builtin_amdgcn_raw_buffer_load_b8(scales, q4_row < rows_of ? (q4_quad + 4 * j) * 16 + q4_row : kOOB, 0, 0);
+        }
+    };
+    const uint32_t q4_to = lds0 + (wave * 16 + q4_row) * kQuad + q4_quad * kKeys * kQuad;
+    auto write_piece = [&](bool is_v, int buf, int i) {
+        const Raw& x = is_v ? raw_v : raw_k;
+        const int j = i / kWords, c = i % kWords;
+        const uint32_t at = q4_to + (2 * buf + is_v) * kTileBytes + 4 * j * kKeys * kQuad +
+                            ((c + q4_part / 4) ^ k_turn(q4_row)) * 16;
+        *(__attribute__((address_space(3))) u4*)(size_t)at = q4_values<T>(x.codes[j][c], q4_scale(x.scale[j]));
+    };
+    auto write = [&](bool is_v, int buf) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) write_piece(is_v, buf, i);
+    };
+
     // Where this lane reads a tile: K row col, chunk 2 i + half (places 0 or 1, 2 or 3
     // of a quad by i's low bit, turned); V rows 4 half + lane % 16 / 4 (+ 8, + 16 g),
     // elements 32 i + 16 (col / 16) + 4 (lane % 4).
     const uint32_t k_at = lds0 + col * kQuad + (half ^ k_turn(col)) * 16;
-    const uint32_t v_at = lds0 + kTileBytes + (4 * half + ((lane & 15) >> 2)) * kQuad + 32 * (col >> 4) + (lane & 3) * 8;
+    // (4 bits: chunks turned by the row, that of the rows 8 further on by two more.)
+    const uint32_t v_at = lds0 + kTileBytes + (4 * half + ((lane & 15) >> 2)) * kQuad +
+                          ((32 * (col >> 4) + (lane & 3) * 8) ^ (Q4 ? 16 * half : 0));
     auto k_read = [&](uint32_t at, int i, int rows_of) { return (at ^ (32u * (i & 1))) + (i >> 1) * rows_of * kQuad; };
 
     // The wave's queries go through LDS as a key tile does (waves 0 and 1 of the
@@ -406,7 +463,7 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
                 nxt = T::mfma32(kf[k], qf[k], nxt);
                 const int g = k / kV, i = k % kV;                 // kK == 2 kV
                 const uint32_t at = v_at + v_cur + (i * kKeys + g * 16) * kQuad;
-                const u2 x = lds_tr(at), y = lds_tr(at + 8 * kQuad);
+                const u2 x = lds_tr(at), y = lds_tr((Q4 ? at ^ 32u : at) + 8 * kQuad);
                 vf[g][i] = u4{x[0], x[1], y[0], y[1]};
                 kf[k] = lds_ld<u4>(k_read(k_at + k_next, k, kKeys));
             }
@@ -434,35 +491,59 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     // landed for all waves (in step first - 1 K only), and all are done with K of
     // tile t and V of tile t - 1 (or the queries), so the loads of K of tile t + 2 and
     // V of tile t + 1 may begin.
-    Place cur, next, after;                       // of tiles t, t + 1 and t + 2
+    // 4 bits: in step t what registers hold of K of tile t + 2 and V of tile t + 1
+    // is written, and then K of tile t + 3 and V of tile t + 2 requested.
+    Place cur, next, after, later;                // of tiles t, t + 1, t + 2 and t + 3
     if (first < last) {
         look_up(first, load_queries);
         cur = next = place(first);
         after = place(min(first + 1, last - 1));
-        load(false, 0, next);
-        load(true, 0, next);
+        if constexpr (Q4) {
+            later = place(min(first + 2, last - 1));
+            fetch(false, next, true);
+            fetch(true, next, true);
+            wait_vmem_below<0>();                 // the queries too, which the compiler does not know of
+        } else {
+            load(false, 0, next);
+            load(true, 0, next);
+        }
     }
     auto advance = [&](int t) {
         if (t >= first) {
             cur = next;
             next = after;
-            wait_vmem_below<0>();
-        } else {
+            if constexpr (Q4) after = later;
+            else wait_vmem_below<0>();
+        } else if constexpr (!Q4) {
             wait_vmem_below<kLoads>();
         }
         __syncthreads();
-        if (t >= first && t + 2 < last) {
-            if (t + 2 - from == 64) look_up(t + 2, [] {});
-            after = place(t + 2);
+        constexpr int kAhead = Q4 ? 3 : 2;
+        if (t >= first && t + kAhead < last) {
+            if (t + kAhead - from == 64) look_up(t + kAhead, [] {});
+            (Q4 ? later : after) = place(t + kAhead);
         }
     };
     auto load_all = [&](int t) {
-        if (t + 2 < last) load(false, (t - first) & 1, after);
-        if (t >= first && t + 1 < last) load(true, (t + 1 - first) & 1, next);
+        if constexpr (Q4) {
+            if (t + 2 < last) write(false, (t - first) & 1);
+            if (t >= first && t + 1 < last) write(true, (t + 1 - first) & 1);
+            if (t + 3 < last) fetch(false, later, true);
+            if (t + 2 < last) fetch(true, after, true);
+        } else {
+            if (t + 2 < last) load(false, (t - first) & 1, after);
+            if (t >= first && t + 1 < last) load(true, (t + 1 - first) & 1, next);
+        }
     };
     constexpr uint32_t kHalf = kKeys / 2 * kQuad;
     if (first < last) {
-        wait_vmem_below<kLoads>();                // the queries; V of the first tile may still be on its way
+        if constexpr (Q4) {
+            write(false, 0);
+            write(true, 0);
+            if (first + 1 < last) fetch(false, after, true);
+        } else {
+            wait_vmem_below<kLoads>();            // the queries; V of the first tile may still be on its way
+        }
 #pragma unroll
         for (int i = 0; i < kK; ++i)
             qf[i] = (lds_ld<u4>(k_read(k_at + 2 * kTileBytes + wave * 32 * D * 2, i, 32)) ^ flip) & keep;
@@ -487,6 +568,22 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
             // A workgroup's loads all at once would queue at the address unit
             // (32 of 16 cycles); here each wave spreads its own over the first half.
             // Past the last tile they read nothing (and write zeros nobody reads).
+            if constexpr (Q4) {
+                half_step(s0, s1, cur.base, cur.blocks & 3, other, buf, [&](int n, int of) {
+#pragma unroll
+                    for (int i = n * 2 * kPieces / of; i < (n + 1) * 2 * kPieces / of; ++i) {
+                        if (i < kPieces) write_piece(true, odd ^ 1, i);
+                        else write_piece(false, odd, i - kPieces);
+                    }
+                });
+                half_step(s1, s0, cur.base + kKeys / 2, cur.blocks >> 2 & 3, other + kHalf, buf + kHalf, [&](int n, int) {
+                    if (n == 0) {
+                        fetch(true, after, t + 2 < last);
+                        fetch(false, later, t + 3 < last);
+                    }
+                });
+                continue;
+            }
             const Source k_source = source_of(false, odd, after, t + 2 < last);
             const Source v_source = source_of(true, odd ^ 1, next, t + 1 < last);
             half_step(s0, s1, cur.base, cur.blocks & 3, other, buf, [&](int n, int of) {
@@ -548,8 +645,8 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         for (int r = 32 * wave; r < 32 * wave + w_rows; ++r) {
             const int p = token_of(r), tk = row_first + token0 + p, hd = kvh * share + skip + r - p * share;
             float x[4], mx, lx;
-            plain_row<D, kKeys>(a, span, begin, end, key_span(a, p_first + p), table, kvh, a.q + tk * a.sq + (int64_t)hd * D,
-                                x, mx, lx);
+            plain_row<D, kKeys, Rows>(a, span, begin, end, key_span(a, p_first + p), table, kvh,
+                                      a.q + tk * a.sq + (int64_t)hd * D, x, mx, lx);
             store_plain_row<T, D>(a, parts, splits > 1, tk, hd, split, x, mx, lx);
         }
         return;
@@ -593,7 +690,7 @@ int64_t slots_of(const AttnArgs& a) {
     return (int64_t)a.tokens * (a.q_heads / a.kv_heads) / kRows + a.kv.seqs;
 }
 
-template <class T, int D, int KG>
+template <class T, int D, int KG, bool Q4>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     const int64_t slots = slots_of(a);
     int64_t most = a.max_len;
@@ -606,7 +703,7 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     const int64_t per_slot = a.kv_heads * splits, round = max((int64_t)1, kSplitTarget / per_slot), at_once = ((int64_t(1) << 32) / (64 * kRowWaves * KG) - 1) / per_slot;
     for (int64_t s = 0; s < slots; s += at_once) {
         const int64_t n = min(at_once, slots - s);
-        hipLaunchKernelGGL((attention_prefill_kernel<T, D, KG>), dim3((unsigned)(n * per_slot)), dim3(64 * kRowWaves * KG), 0,
+        hipLaunchKernelGGL((attention_prefill_kernel<T, D, KG, Q4>), dim3((unsigned)(n * per_slot)), dim3(64 * kRowWaves * KG), 0,
                            stream, a,
                            Grid{Divisor(a.kv_heads), Divisor(splits), Divisor(a.q_heads / a.kv_heads), (int)slots, (int)s,
                                 chunk, (int)round});
@@ -626,23 +723,23 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
 // is then alone on its CU for most of its time (1100 tokens of 32 heads on 8
 // 26.1 us in one group, 23.7 in two; 1536 33.3 and 30.8; 1900 44.2 and 41.3; 1280 behind 320 34.3
 // and 33.1; head size 64, 1900 tokens 33.6 and 28.6), up to nearly two rounds (2048 tokens 48.6 and 50.2).
-template <class T, int D>
+template <class T, int D, bool Q4>
 hipError_t launch_groups(const AttnArgs& a, hipStream_t stream) {
     const int64_t rows = (int64_t)a.tokens * (a.q_heads / a.kv_heads);
     const int64_t blocks = a.kv.seqs == 1 ? (rows + kRows - 1) / kRows : slots_of(a);
     const bool uneven = a.kv.seqs == 1 && 4 * (int64_t)a.max_len <= 5 * (int64_t)a.tokens &&
                         (a.window == 0 || a.window >= a.tokens);
     const int64_t most = uneven ? 2 * kSplitTarget - kSplitTarget / 8 : kSplitTarget;
-    return blocks * a.kv_heads <= most ? launch<T, D, 2>(a, stream) : launch<T, D, 1>(a, stream);
+    return blocks * a.kv_heads <= most ? launch<T, D, 2, Q4>(a, stream) : launch<T, D, 1, Q4>(a, stream);
 }
 
-template <class T>
+template <class T, bool Q4>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
     switch (a.head_dim) {
-        case 64: return launch_groups<T, 64>(a, stream);
-        case 96: return launch_groups<T, 96>(a, stream);
-        case 128: return launch_groups<T, 128>(a, stream);
-        default: return launch<T, 256, 1>(a, stream);           // two groups' tiles do not fit LDS
+        case 64: return launch_groups<T, 64, Q4>(a, stream);
+        case 96: return launch_groups<T, 96, Q4>(a, stream);
+        case 128: return launch_groups<T, 128, Q4>(a, stream);
+        default: return launch<T, 256, 1, Q4>(a, stream);           // two groups' tiles do not fit LDS
     }
 }
 
@@ -651,7 +748,12 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
 hipError_t launch_attention_prefill(const AttnArgs& a, hipStream_t stream) {
     // One new token of every sequence is the single-token form.
     if (!a.kv.starts) return launch_attention_decode(a, stream);
-    return a.dtype == 0 ? launch_dim<Fp16>(a, stream) : launch_dim<Bf16>(a, stream);
+    return a.dtype == 0 ? launch_dim<Fp16, false>(a, stream) : launch_dim<Bf16, false>(a, stream);
+}
+
+hipError_t launch_attention_prefill_q4(const AttnArgs& a, hipStream_t stream) {
+    if (!a.kv.starts) return launch_attention_decode_q4(a, stream);
+    return a.dtype == 0 ? launch_dim<Fp16, true>(a, stream) : launch_dim<Bf16, true>(a, stream);
 }
 
 }  // namespace slim

@@ -4,7 +4,9 @@ The keys and values of all layers live in two pools [layers, pages, kv_heads,
 page_size, head_dim]; a page is the same index in every layer.  This class does
 the bookkeeping on the host (a free list, a count of owners per page, each
 sequence's list of pages) and moves data with kv_copy_pages only, on the
-current stream.  Forks share pages: a sequence gets its own copy of a shared
+current stream.  With bits=4 the pools are uint8 pages of 4 bits a value
+[layers, pages, kv_heads, page_size, head_dim * 17 / 32], as kv_append_q4 writes
+and the _q4 attention calls read them.  Forks share pages: a sequence gets its own copy of a shared
 page when it first writes to it.
 """
 from __future__ import annotations
@@ -43,11 +45,15 @@ class _Sequence:
 
 class KVCache:
     def __init__(self, layers: int, pages: int, kv_heads: int, head_dim: int, page_size: int = 64,
-                 dtype: torch.dtype = torch.float16, device="cuda"):
+                 dtype: torch.dtype = torch.float16, device="cuda", bits: int = 16):
         if min(layers, pages, kv_heads, head_dim, page_size) <= 0:
             raise ValueError("layers, pages, kv_heads, head_dim and page_size must be positive")
         if layers > 4096 or pages > 1 << 24:
             raise ValueError("at most 4096 layers and 2^24 pages")
+        if bits not in (4, 16):
+            raise ValueError(f"bits must be 4 or 16, not {bits}")
+        if bits == 4 and (head_dim % 32 or page_size % 16):
+            raise ValueError("a cache of 4 bits needs heads of whole groups of 32 and pages of whole blocks of 16")
         # What the calls on these pools would refuse later, with pages handed
         # out already.  (Pools on the host serve the bookkeeping alone.)
         if torch.device(device).type != "cpu":
@@ -57,8 +63,9 @@ class KVCache:
                 raise ValueError(f"no attention with {kv_heads} key heads of size {head_dim}")
             if page_size not in PAGE_SIZES:
                 raise ValueError(f"page_size must be one of {PAGE_SIZES}, not {page_size}")
-        self.page_size = page_size
-        self.k = torch.empty((layers, pages, kv_heads, page_size, head_dim), dtype=dtype, device=device)
+        self.page_size, self.bits, self.dtype = page_size, bits, dtype
+        row = (head_dim, dtype) if bits == 16 else (head_dim * 17 // 32, torch.uint8)
+        self.k = torch.empty((layers, pages, kv_heads, page_size, row[0]), dtype=row[1], device=device)
         self.v = torch.empty_like(self.k)
         self._owners = [0] * pages
         self._free = list(range(pages))      # a heap: the lowest free page goes out first
