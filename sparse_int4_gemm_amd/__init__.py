@@ -290,17 +290,19 @@ def attention_prefill(q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor,
     return out
 
 
-def _empty_like(x, stream):
-    """A tensor of x's shape, made on the stream that the call runs on."""
-    with torch.cuda.stream(stream):            # None: no change
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+def _empty(shape, dtype, device, stream):
+    """A tensor made on the stream that a call runs on (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Rows x [tokens, heads, head_dim] (fp16 or bf16) turned to positions
     int32 [tokens]; a negative position turns back.  out: may be x itself."""
     if out is None:
-        out = _empty_like(x, stream)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     slim_rope(x, out, positions, rope, stream=stream)
     return out
 
@@ -312,7 +314,7 @@ def kv_append_rope(K: torch.Tensor, V: torch.Tensor, kpool: torch.Tensor, vpool:
     them the step's queries q [tokens, q_heads, head_dim], which are returned
     (in q_out, which may be q itself)."""
     if q is not None and q_out is None:
-        q_out = _empty_like(q, stream)
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
     slim_kv_append_rope(q, q_out, K, V, kpool, vpool, table, lens, rope, starts, stream=stream)
     return q_out
 
@@ -324,7 +326,7 @@ def kv_append_q4(K: torch.Tensor, V: torch.Tensor, kpool: torch.Tensor, vpool: t
     page_size, head_dim * 17 / 32] (slim.h has the format).  rope None: keys as
     they are, and no queries."""
     if q is not None and q_out is None:
-        q_out = _empty_like(q, stream)
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
     slim_kv_append_q4(q, q_out, K, V, kpool, vpool, table, lens, rope, starts, stream=stream)
     return q_out
 
@@ -342,9 +344,8 @@ def kv_read_q4(kpool: torch.Tensor, vpool: torch.Tensor, table: torch.Tensor, le
             tokens = lens.shape[0]
         if kpool.dim() != 4:
             raise ValueError("the pools must be [pages, kv_heads, page_size, head_dim * 17 / 32]")
-        with torch.cuda.stream(stream):
-            out = tuple(torch.empty((tokens, kpool.shape[1], kpool.shape[3] // 17 * 32), dtype=dtype, device=kpool.device)
-                        for _ in range(2))
+        shape = (tokens, kpool.shape[1], kpool.shape[3] // 17 * 32)
+        out = tuple(_empty(shape, dtype, kpool.device, stream) for _ in range(2))
     slim_kv_read_q4(out[0], out[1], kpool, vpool, table, lens, starts, stream=stream)
     return out
 

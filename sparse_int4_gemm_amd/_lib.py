@@ -321,6 +321,7 @@ _PAGE_TYPES = (*_DTYPES, torch.uint8)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 # (Each attribute of a tensor costs some 50 ns, a call's checks as much as its
@@ -368,7 +369,7 @@ def _pools(kpool, vpool, dims, dtypes=_DTYPES):
 
 def _stream_on(stream, device):
     """The HIP stream of a call on `device`, and a check that launches go there."""
-    if device.index != torch.cuda.current_device():
+    if device.index != _current_device():
         raise ValueError(f"the current device must be the tensors' {device}")
     if stream is not None:
         return stream.cuda_stream

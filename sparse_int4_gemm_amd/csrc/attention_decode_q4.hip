@@ -21,8 +21,8 @@
 namespace slim {
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kTile = 32;            // keys of one wave's step
+constexpr float kLazy = 8.0f;        // a weight may pass 2^kUp by 2^kLazy before the maximum is raised
 
 struct Place {
     int base, page[2];               // first key, pages of the 16-key halves (-1: none)
@@ -33,18 +33,18 @@ struct Place {
 template <int D>
 struct KeyGroups {
     static constexpr int kTwo = D == 96 || D == 256;
-    static __device__ __forceinline__ int first(int g) { return D / 4 * g / 32; }
-    static __device__ __forceinline__ int last(int g) { return (D / 4 * (g + 1) - 1) / 32; }
+    static __device__ __forceinline__ uint32_t first(uint32_t g) { return D / 4 * g / 32; }
+    static __device__ __forceinline__ uint32_t last(uint32_t g) { return (D / 4 * (g + 1) - 1) / 32; }
     // Whether chunk i of eight elements lies in the last.
-    static __device__ __forceinline__ bool in_last(int g, int i) { return (D / 4 * g + 8 * i) / 32 != first(g); }
+    static __device__ __forceinline__ bool in_last(uint32_t g, uint32_t i) { return (D / 4 * g + 8 * i) / 32 != first(g); }
 };
 // The same of its elements of a value (D/16 from D/16 c on).
 template <int D>
 struct ValueGroups {
     static constexpr int kTwo = D == 96;
-    static __device__ __forceinline__ int first(int c) { return D / 16 * c / 32; }
-    static __device__ __forceinline__ int last(int c) { return (D / 16 * (c + 1) - 1) / 32; }
-    static __device__ __forceinline__ bool in_last(int c, int e) { return (D / 16 * c + e) / 32 != first(c); }
+    static __device__ __forceinline__ uint32_t first(uint32_t c) { return D / 16 * c / 32; }
+    static __device__ __forceinline__ uint32_t last(uint32_t c) { return (D / 16 * (c + 1) - 1) / 32; }
+    static __device__ __forceinline__ bool in_last(uint32_t c, uint32_t e) { return (D / 16 * c + e) / 32 != first(c); }
 };
 
 // The registers of one tile.
@@ -57,41 +57,54 @@ struct Tile {
     Place at;
 };
 
+// (A uniform base and a lane's 32-bit offset for each load, so that the vector unit adds no addresses.)
 template <int D>
 __device__ __forceinline__ void load_tile(Tile<D>& x, const AttnArgs& a, int kvh, const Place& at) {
-    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const uint32_t lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     x.at = at;
     const unsigned char *kp = reinterpret_cast<const unsigned char*>(a.kv.k), *vp = reinterpret_cast<const unsigned char*>(a.kv.v);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const Q4Row row(max(at.page[t], 0), a.kv_heads, a.kv.page_shift, D, kvh,
                         (at.base + 16 * t) & ((1 << a.kv.page_shift) - 1));
-        const uint32_t* k = reinterpret_cast<const uint32_t*>(kp + row.codes + c * (D / 2) + g * (D / 8));
+        const unsigned char *kc = kp + row.codes, *ks = kp + row.scales, *vc = vp + row.codes, *vs = vp + row.scales;
+        const uint32_t k = c * (D / 2) + g * (D / 8);
         if constexpr (D == 96) {
 #pragma unroll
-            for (int i = 0; i < 3; ++i) x.k[t][i] = k[i];
+            for (int i = 0; i < 3; ++i) x.k[t][i] = *reinterpret_cast<const uint32_t*>(kc + k + 4 * i);
         } else {
-            load_words<D / 32>(x.k[t], reinterpret_cast<const uint16_t*>(k));
+            load_words<D / 32>(x.k[t], reinterpret_cast<const uint16_t*>(kc + k));
         }
-        const unsigned char* ks = kp + row.scales + c;
-        x.ks[t][0] = ks[16 * KeyGroups<D>::first(g)];
-        if constexpr (KeyGroups<D>::kTwo) x.ks[t][1] = ks[16 * KeyGroups<D>::last(g)];
+        x.ks[t][0] = ks[16 * KeyGroups<D>::first(g) + c];
+        if constexpr (KeyGroups<D>::kTwo) x.ks[t][1] = ks[16 * KeyGroups<D>::last(g) + c];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const unsigned char* v = vp + row.codes + (4 * g + i) * (D / 2) + c * (D / 32);
+            const unsigned char* v = vc + (4 * g * (D / 2) + c * (D / 32)) + i * (D / 2);
             if constexpr (D == 64) x.v[t][i][0] = *reinterpret_cast<const uint16_t*>(v);
-            else if constexpr (D == 96) x.v[t][i][0] = v[0] | v[1] << 8 | v[2] << 16;
+            // (Three bytes, and one that does not count: the next row's, or the scales' behind the last one.)
+            else if constexpr (D == 96) __builtin_memcpy(&x.v[t][i][0], v, 4);
             else load_words<Tile<D>::kV>(x.v[t][i], reinterpret_cast<const uint16_t*>(v));
         }
-        const unsigned char* vs = vp + row.scales + 4 * g;
-        x.vs[t][0] = *reinterpret_cast<const uint32_t*>(vs + 16 * ValueGroups<D>::first(c));
-        if constexpr (ValueGroups<D>::kTwo) x.vs[t][1] = *reinterpret_cast<const uint32_t*>(vs + 16 * ValueGroups<D>::last(c));
+        x.vs[t][0] = *reinterpret_cast<const uint32_t*>(vs + 16 * ValueGroups<D>::first(c) + 4 * g);
+        if constexpr (ValueGroups<D>::kTwo)
+            x.vs[t][1] = *reinterpret_cast<const uint32_t*>(vs + 16 * ValueGroups<D>::last(c) + 4 * g);
     }
 }
 
-template <class T, int D>
-__global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_q4_kernel(AttnArgs a, int splits, int chunk, int groups,
-                                                                             int sort_most) {
+// The largest of x over the four lanes of a column (lane % 16).
+__device__ __forceinline__ float column_max(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(int, x), __builtin_bit_cast(int, x), false, false);
+    const unsigned r0 = r[0], r1 = r[1];
+    const float y = fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+    const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(int, y), __builtin_bit_cast(int, y), false, false);
+    const unsigned s0 = s[0], s1 = s[1];
+    return fmaxf(__builtin_bit_cast(float, s0), __builtin_bit_cast(float, s1));
+}
+
+// kWaves waves a workgroup, each with every kWaves-th tile.
+template <class T, int D, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void attention_decode_q4_kernel(
+    AttnArgs a, int splits, int chunk, int groups, int sort_most) {
     constexpr int VE = D / 16;
     __shared__ float o_join[kWaves][16][D + 4];
     __shared__ float m_join[kWaves][16], l_join[kWaves][16];
@@ -134,7 +147,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_q4_kernel(Att
         qf[i] = u4{0, 0, 0, 0};
         if (c < heads) qf[i] = *reinterpret_cast<const u4*>(a.q + b * a.sq + (int64_t)(h0 + c) * D + D / 4 * g + 8 * i);
     }
-    const float scale = a.scale * 1.4426950408889634f;
+    // Scores are compared before they are scaled, so the scale's sign goes into the queries (exact).
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, keep = a.scale == 0.0f ? 0u : ~0u;
+    const float scale = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) qf[i] = (qf[i] ^ flip) & keep;
+    constexpr float kUp = T::kTop > kLazy ? T::kTop - kLazy : 0.0f;        // so that no weight passes 2^kTop
     float m = -INFINITY, l = 0.0f;
     f4 o[VE];
 #pragma unroll
@@ -151,7 +169,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_q4_kernel(Att
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
                 s[t] = T::mfma16(q4_values<T>(x.k[t][i], KeyGroups<D>::in_last(g, i) ? last_scale : first_scale), qf[i], s[t]);
-            s[t] *= scale;
         }
         // A tile whose every key is seen and owned needs no mask (the same answer in all lanes).
         if (!(span.all_seen(x.at.base, kTile) && x.at.page[0] >= 0 && x.at.page[1] >= 0)) {
@@ -172,19 +189,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_q4_kernel(Att
         }
         float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                           fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float mn = fmaxf(m, top - T::kTop);            // the largest weight is 2^kTop
-        const float ms = mn == -INFINITY ? 0.0f : mn;        // nothing seen so far: all weights are 2^-inf = 0
-        const float f = exp2_fast(m - ms);
-        m = mn;
+        top = fmaf(column_max(top), scale, -kUp);
+        if (__any(top > m + kLazy)) {
+            const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) o[e] *= f;
+        }
+        const float ms = m == -INFINITY ? 0.0f : m;          // nothing seen so far: all weights are 2^-inf = 0
         float w[8], sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            w[j] = exp2_fast(s[j >> 2][j & 3] - ms);
+            w[j] = exp2_fast(fmaf(s[j >> 2][j & 3], scale, -ms));
             sum += w[j];
         }
-        l = l * f + sum;
+        l += sum;
         u4 hi, lo;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -194,8 +214,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_q4_kernel(Att
         float vs[8], vs_last[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            vs[j] = q4_scale(x.vs[j >> 2][0] >> 8 * (j & 3) & 0xFFu);
-            if constexpr (ValueGroups<D>::kTwo) vs_last[j] = q4_scale(x.vs[j >> 2][1] >> 8 * (j & 3) & 0xFFu);
+            vs[j] = q4_scale_of(x.vs[j >> 2][0], j & 3);
+            if constexpr (ValueGroups<D>::kTwo) vs_last[j] = q4_scale_of(x.vs[j >> 2][1], j & 3);
         }
         // Elements e and e + 1 of a lane's: two keys' pairs, then their low and their high halves side by side.
         auto two = [&](auto byte, int word) {
@@ -215,8 +235,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_q4_kernel(Att
                 highs[j] = __builtin_amdgcn_perm(p[1], p[0], 0x07060302u);
             }
             f4 &even = o[8 * word + e], &odd = o[8 * word + e + 1];
-            even = T::mfma16(lows, lo, T::mfma16(lows, hi, even * f));
-            odd = T::mfma16(highs, lo, T::mfma16(highs, hi, odd * f));
+            even = T::mfma16(lows, lo, T::mfma16(lows, hi, even));
+            odd = T::mfma16(highs, lo, T::mfma16(highs, hi, odd));
         };
 #pragma unroll
         for (int word = 0; word < Tile<D>::kV; ++word) {
@@ -276,8 +296,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_q4_kernel(Att
     const uint64_t odd = __ballot(c < heads && !(probe[0] + probe[1] + probe[2] + probe[3] == 0.0f));
     if (lane == 0) bad_join[wave] = (uint32_t)(odd | odd >> 16 | odd >> 32 | odd >> 48) & 0xFFFFu;
     __syncthreads();
-    static_assert(kWaves == 4, "the waves' rows below");
-    const uint32_t bad = __builtin_amdgcn_readfirstlane(bad_join[0] | bad_join[1] | bad_join[2] | bad_join[3]);
+    uint32_t bad = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) bad |= bad_join[w];
+    bad = __builtin_amdgcn_readfirstlane(bad);
     for (int at = threadIdx.x; at < heads * (D / 4); at += 64 * kWaves) {
         const int r = at / (D / 4), d = (at - r * (D / 4)) * 4;
         if (bad >> r & 1) continue;
@@ -311,25 +333,40 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_decode_q4_kernel(Att
     }
 }
 
-// As attention_decode.hip's plan.
-constexpr int kSplitTarget = 512, kMinTiles = 16, kSortFrom = 512;
+// The plan: kWavesTarget waves in all (16 a CU; 8 at head size 256, whose
+// registers hold no more), each with at least kMinTiles tiles.  Those of a key
+// head share a workgroup up to 16 (8), and only beyond that the keys are split
+// over workgroups, at the cost of partial results and another launch.
+constexpr int kCus = 256, kMinTiles = 4, kSortFrom = 512;
+
+template <class T, int D, int kWaves>
+hipError_t launch_waves(const AttnArgs& a, int splits, int tiles, int64_t most, hipStream_t stream) {
+    const int share = a.q_heads / a.kv_heads, groups = (share + 15) / 16;
+    const int64_t units = (int64_t)a.tokens * a.kv_heads * groups;
+    const int chunk = max(kWaves, (tiles + splits - 1) / splits);
+    dim3 grid((unsigned)(a.tokens * splits), (unsigned)(a.kv_heads * groups));
+    // More than a round of workgroups: longest first (attention_decode.hip).
+    const int sort_most = kWaves == 4 && splits == 1 && units > 2 * kCus && most >= kSortFrom ? (int)most : 0;
+    hipLaunchKernelGGL((attention_decode_q4_kernel<T, D, kWaves>), grid, dim3(64 * kWaves), 0, stream, a, splits, chunk,
+                       groups, sort_most);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || splits == 1 ? e : launch_attention_join(a, splits, stream);
+}
 
 template <class T, int D>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
+    constexpr int kMost = D == 256 ? 8 : 16;                 // waves a CU holds, and a workgroup at most
     const int share = a.q_heads / a.kv_heads, groups = (share + 15) / 16;
     int64_t most = (int64_t)a.max_len;
     if (a.window && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;
     const int tiles = (int)((most + kTile - 1) / kTile);
     const int64_t units = (int64_t)a.tokens * a.kv_heads * groups;
-    const int64_t want = min(kSplitTarget / units, (int64_t)((tiles + kMinTiles - 1) / kMinTiles));
-    const int splits = (int)max((int64_t)1, min(want, kAttnSplitRows / ((int64_t)a.tokens * a.q_heads)));
-    const int chunk = max(kWaves, (tiles + splits - 1) / splits);
-    dim3 grid((unsigned)(a.tokens * splits), (unsigned)(a.kv_heads * groups));
-    const int sort_most = units > kSplitTarget && most >= kSortFrom ? (int)most : 0;
-    hipLaunchKernelGGL((attention_decode_q4_kernel<T, D>), grid, dim3(64 * kWaves), 0, stream, a, splits, chunk, groups,
-                       sort_most);
-    const hipError_t e = hipGetLastError();
-    return e != hipSuccess || splits == 1 ? e : launch_attention_join(a, splits, stream);
+    const int64_t waves = min(kCus * kMost / units, (int64_t)(tiles + kMinTiles - 1) / kMinTiles);
+    if (waves <= 4) return launch_waves<T, D, 4>(a, 1, tiles, most, stream);
+    if (waves <= 8 && kMost == 16) return launch_waves<T, D, 8>(a, 1, tiles, most, stream);
+    const int64_t rows = (int64_t)a.tokens * a.q_heads;
+    const int splits = (int)max((int64_t)1, min(waves / kMost, kAttnSplitRows / rows));
+    return launch_waves<T, D, kMost>(a, splits, tiles, most, stream);
 }
 
 template <class T>

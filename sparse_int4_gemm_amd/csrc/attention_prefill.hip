@@ -76,18 +76,6 @@ __device__ __forceinline__ Halves halves(float x) {
     return {__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
 }
 
-// Division by a number that the launch knows: a product with m = (2^32 - 1) / d
-// (rounded down) gives the quotient or one less.  (The compiler's own takes some 30
-// instructions, and the kernel's beginning is bound by their number.)
-struct Divisor {
-    uint32_t d, m;
-    explicit Divisor(int64_t by) : d((uint32_t)by), m(0xFFFFFFFFu / (uint32_t)by) {}
-    __device__ __forceinline__ int quotient(uint32_t n) const {
-        const uint32_t q = __umulhi(n, m);
-        return (int)(n - q * d >= d ? q + 1 : q);
-    }
-};
-
 // What the launch knows of the grid: key heads x splits x slots (from slot0 on).
 struct Grid {
     Divisor kv_heads, splits, share;
@@ -280,17 +268,17 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     // 16 different bank groups - also those of V, which is turned as K is then.
     constexpr int kQuads = Q4 && D == 256 ? 2 : 1, kWords = Q4 && D == 64 ? 2 : 4;
     constexpr int kPieces = Q4 ? kQuads * kWords : 1;            // dwords of codes, 16-byte chunks of halves
-    struct Raw { uint32_t codes[kQuads][kWords], scale[kQuads]; };
+    // (The scale as the byte it is loaded as: widened, it would be waited for before its step.)
+    struct Raw { uint32_t codes[kQuads][kWords]; uint8_t scale[kQuads]; };
     Raw raw_k, raw_v;
     const int q4_row = lane & 15, q4_quad = D == 64 ? lane >> 5 : D == 96 ? min(lane >> 4, 2) : lane >> 4;
     const int q4_part = D == 64 ? (lane >> 4 & 1) * 8 : 0;       // of the quad's codes, bytes
-    auto fetch = [&](bool is_v, const Place& x, bool any) {
+    auto fetch = [&](Raw& to, bool is_v, const Place& x, bool any) {
         const unsigned char* pool = reinterpret_cast<const unsigned char*>(is_v ? a.kv.v : a.kv.k) +
                                     (int64_t)((uint64_t)(uint32_t)x.lo | (uint64_t)(uint32_t)x.hi << 32);
         const int rows_of = any ? x.blocks >> 4 : 0;
         const __amdgpu_buffer_rsrc_t codes = make_rsrc(pool, rows_of * (D / 2));
         const __amdgpu_buffer_rsrc_t scales = make_rsrc(pool + x.to_scales, D / 2);
-        Raw& to = is_v ? raw_v : raw_k;
 #pragma unroll
         for (int j = 0; j < kQuads; ++j) {
             const int at = q4_row * (D / 2) + (q4_quad + 4 * j) * 16 + q4_part;
@@ -307,17 +295,23 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
             to.scale[j] = __builtin_amdgcn_raw_buffer_load_b8(scales, q4_row < rows_of ? (q4_quad + 4 * j) * 16 + q4_row : kOOB, 0, 0);
         }
     };
-    const uint32_t q4_to = lds0 + (wave * 16 + q4_row) * kQuad + q4_quad * kKeys * kQuad;
-    auto write_piece = [&](bool is_v, int buf, int i) {
-        const Raw& x = is_v ? raw_v : raw_k;
+    // Chunk c of a quad is at place c ^ k_turn(row): the lane's address with c's bits turned over.
+    const uint32_t q4_to = lds0 + (wave * 16 + q4_row) * kQuad + q4_quad * kKeys * kQuad +
+                           ((q4_part / 4) ^ k_turn(q4_row)) * 16;
+    auto write_to = [&](bool is_v, int buf) {
+        uint32_t at = q4_to + (2 * buf + is_v) * kTileBytes;
+        asm("" : "+v"(at));
+        return at;
+    };
+    auto write_piece = [&](const Raw& x, uint32_t to, int i) {
         const int j = i / kWords, c = i % kWords;
-        const uint32_t at = q4_to + (2 * buf + is_v) * kTileBytes + 4 * j * kKeys * kQuad +
-                            ((c + q4_part / 4) ^ k_turn(q4_row)) * 16;
+        const uint32_t at = (to ^ 16u * c) + 4 * j * kKeys * kQuad;
         *(__attribute__((address_space(3))) u4*)(size_t)at = q4_values<T>(x.codes[j][c], q4_scale(x.scale[j]));
     };
-    auto write = [&](bool is_v, int buf) {
+    auto write = [&](const Raw& x, bool is_v, int buf) {
+        const uint32_t to = write_to(is_v, buf);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) write_piece(is_v, buf, i);
+        for (int i = 0; i < kPieces; ++i) write_piece(x, to, i);
     };
 
     // Where this lane reads a tile: K row col, chunk 2 i + half (places 0 or 1, 2 or 3
@@ -327,6 +321,8 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     // (4 bits: chunks turned by the row, that of the rows 8 further on by two more.)
     const uint32_t v_at = lds0 + kTileBytes + (4 * half + ((lane & 15) >> 2)) * kQuad +
                           ((32 * (col >> 4) + (lane & 3) * 8) ^ (Q4 ? 16 * half : 0));
+    uint32_t v_at8 = (Q4 ? v_at ^ 32u : v_at) + 8 * kQuad;
+    if constexpr (Q4) asm("" : "+v"(v_at8));      // a register of its own: offsets are the instruction's
     auto k_read = [&](uint32_t at, int i, int rows_of) { return (at ^ (32u * (i & 1))) + (i >> 1) * rows_of * kQuad; };
 
     // The wave's queries go through LDS as a key tile does (waves 0 and 1 of the
@@ -396,6 +392,8 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     // that neither unit waits for the other.
     auto half_step = [&](f16v& cur, f16v& nxt, int base, int blocks_of, uint32_t k_next, uint32_t v_cur,
                          auto&& between) {
+        uint32_t v_base8 = v_at8 + v_cur;
+        if constexpr (Q4) asm("" : "+v"(v_base8));
         // Keys that some row does not see: element e's is c + base + 4 half, c a
         // constant, so a limit is compared with constants.  Mostly only one of the two ends cuts.
         if (base > all_to || blocks_of != 3) {
@@ -463,7 +461,8 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
                 nxt = T::mfma32(kf[k], qf[k], nxt);
                 const int g = k / kV, i = k % kV;                 // kK == 2 kV
                 const uint32_t at = v_at + v_cur + (i * kKeys + g * 16) * kQuad;
-                const u2 x = lds_tr(at), y = lds_tr((Q4 ? at ^ 32u : at) + 8 * kQuad);
+                const uint32_t at8 = Q4 ? v_base8 + (i * kKeys + g * 16) * kQuad : at + 8 * kQuad;
+                const u2 x = lds_tr(at), y = lds_tr(at8);
                 vf[g][i] = u4{x[0], x[1], y[0], y[1]};
                 kf[k] = lds_ld<u4>(k_read(k_at + k_next, k, kKeys));
             }
@@ -500,9 +499,13 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
         after = place(min(first + 1, last - 1));
         if constexpr (Q4) {
             later = place(min(first + 2, last - 1));
-            fetch(false, next, true);
-            fetch(true, next, true);
+            Raw first_k;
+            fetch(first_k, false, next, true);
+            fetch(raw_v, true, next, true);
+            fetch(raw_k, false, after, first + 1 < last);
             wait_vmem_below<0>();                 // the queries too, which the compiler does not know of
+            write(first_k, false, 0);
+            write(raw_v, true, 0);
         } else {
             load(false, 0, next);
             load(true, 0, next);
@@ -526,10 +529,10 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     };
     auto load_all = [&](int t) {
         if constexpr (Q4) {
-            if (t + 2 < last) write(false, (t - first) & 1);
-            if (t >= first && t + 1 < last) write(true, (t + 1 - first) & 1);
-            if (t + 3 < last) fetch(false, later, true);
-            if (t + 2 < last) fetch(true, after, true);
+            if (t + 2 < last) write(raw_k, false, (t - first) & 1);
+            if (t >= first && t + 1 < last) write(raw_v, true, (t + 1 - first) & 1);
+            if (t + 3 < last) fetch(raw_k, false, later, true);
+            if (t + 2 < last) fetch(raw_v, true, after, true);
         } else {
             if (t + 2 < last) load(false, (t - first) & 1, after);
             if (t >= first && t + 1 < last) load(true, (t + 1 - first) & 1, next);
@@ -537,13 +540,7 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     };
     constexpr uint32_t kHalf = kKeys / 2 * kQuad;
     if (first < last) {
-        if constexpr (Q4) {
-            write(false, 0);
-            write(true, 0);
-            if (first + 1 < last) fetch(false, after, true);
-        } else {
-            wait_vmem_below<kLoads>();            // the queries; V of the first tile may still be on its way
-        }
+        if constexpr (!Q4) wait_vmem_below<kLoads>();       // the queries; V of the first tile may still be on its way
 #pragma unroll
         for (int i = 0; i < kK; ++i)
             qf[i] = (lds_ld<u4>(k_read(k_at + 2 * kTileBytes + wave * 32 * D * 2, i, 32)) ^ flip) & keep;
@@ -569,19 +566,17 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
             // (32 of 16 cycles); here each wave spreads its own over the first half.
             // Past the last tile they read nothing (and write zeros nobody reads).
             if constexpr (Q4) {
+                const uint32_t to_v = write_to(true, odd ^ 1), to_k = write_to(false, odd);
                 half_step(s0, s1, cur.base, cur.blocks & 3, other, buf, [&](int n, int of) {
 #pragma unroll
                     for (int i = n * 2 * kPieces / of; i < (n + 1) * 2 * kPieces / of; ++i) {
-                        if (i < kPieces) write_piece(true, odd ^ 1, i);
-                        else write_piece(false, odd, i - kPieces);
+                        if (i < kPieces) write_piece(raw_v, to_v, i);
+                        else write_piece(raw_k, to_k, i - kPieces);
+                        if (i == kPieces - 1) fetch(raw_v, true, after, t + 2 < last);
+                        if (i == 2 * kPieces - 1) fetch(raw_k, false, later, t + 3 < last);
                     }
                 });
-                half_step(s1, s0, cur.base + kKeys / 2, cur.blocks >> 2 & 3, other + kHalf, buf + kHalf, [&](int n, int) {
-                    if (n == 0) {
-                        fetch(true, after, t + 2 < last);
-                        fetch(false, later, t + 3 < last);
-                    }
-                });
+                half_step(s1, s0, cur.base + kKeys / 2, cur.blocks >> 2 & 3, other + kHalf, buf + kHalf, [](int, int) {});
                 continue;
             }
             const Source k_source = source_of(false, odd, after, t + 2 < last);

@@ -35,4 +35,16 @@ __device__ __forceinline__ int find_seq(const PagedKV& kv, int t) {
     return kv.starts[lo] <= t && t < kv.starts[lo + 1] ? lo : -1;
 }
 
+// Division by a number that the launch knows: a product with m = (2^32 - 1) / d
+// (rounded down) gives the quotient or one less.  (The compiler's own takes some 30
+// instructions, and a kernel's beginning is bound by their number.)
+struct Divisor {
+    uint32_t d, m;
+    explicit Divisor(int64_t by) : d((uint32_t)by), m(0xFFFFFFFFu / (uint32_t)by) {}
+    __device__ __forceinline__ int quotient(uint32_t n) const {
+        const uint32_t q = __umulhi(n, m);
+        return (int)(n - q * d >= d ? q + 1 : q);
+    }
+};
+
 }  // namespace slim

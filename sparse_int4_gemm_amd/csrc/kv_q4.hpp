@@ -26,6 +26,12 @@ struct Q4Row {
 // A scale byte as the conversions take it: the exponent of an fp32.  255 makes NaN.
 __device__ __forceinline__ float q4_scale(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
 
+// Byte i of four.  (The conversions read the exponent's eight bits and no
+// others: checked for every code and exponent with other bits set, so one shift does.)
+__device__ __forceinline__ float q4_scale_of(uint32_t bytes, int i) {
+    return __builtin_bit_cast(float, i < 3 ? bytes << (23 - 8 * i) : bytes >> 1);
+}
+
 // The two values of byte I of `codes`, element 0 in the low half.
 template <class T, int I>
 __device__ __forceinline__ uint32_t q4_pair(uint32_t codes, float scale);

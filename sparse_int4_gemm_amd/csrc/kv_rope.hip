@@ -101,137 +101,183 @@ __global__ __launch_bounds__(64 * kRopeWaves) void kv_append_rope_kernel(AppendR
     }
 }
 
-// One lane's eight elements of a key or value, and the eight they turn with.
-struct Chunk {
-    uint32_t own[4], other[2][2];
-    int at;                                   // first element in its head
-};
-
-// First element of the four that elements at .. at + 3 turn with (halves layout).
-__device__ __forceinline__ int partner(const Rotation& by, int at) {
-    return at >= 2 * by.half ? at : at < by.half ? at + by.half : at - by.half;
-}
-
-// Elements of a chunk, turned in fp64 and rounded to fp32: what a code is
-// chosen by must not depend on the order of fp32 operations.
+// Eight elements of a head, `own`, and those that they turn with, turned in fp64
+// and rounded to fp32: what a code is chosen by must not depend on the order
+// of fp32 operations.  first: the first element's place in its head; turns: of its fours.
 template <class T>
-__device__ __forceinline__ void turned_chunk(float (&y)[8], const Chunk& c, const Rotation& by, const double2* turns) {
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = T::low(c.own[j]);
-        x[2 * j + 1] = T::high(c.own[j]);
-    }
+__device__ __forceinline__ void turned_chunk(float (&y)[8], const uint32_t (&own)[4], const uint32_t (&other)[4], int first,
+                                             const Rotation& by, const double2* turns) {
+    const int step = by.half >> 2;                // from a pair to the next one in LDS (turn_place)
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const int at = c.at + 4 * q;
+        const int at = first + 4 * q;
+        float x[4], z[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            x[2 * j] = T::low(own[2 * q + j]);
+            x[2 * j + 1] = T::high(own[2 * q + j]);
+            z[2 * j] = T::low(other[2 * q + j]);
+            z[2 * j + 1] = T::high(other[2 * q + j]);
+        }
         if (at >= 2 * by.half) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[4 * q + j] = x[4 * q + j];
+            for (int j = 0; j < 4; ++j) y[4 * q + j] = x[j];
         } else if (by.interleaved) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const double2 r = turns[at / 2 + j];
-                const double p = x[4 * q + 2 * j], s = x[4 * q + 2 * j + 1];
+                const double2 r = turns[turn_place(by, at / 2 + j)];
+                const double p = x[2 * j], s = x[2 * j + 1];
                 y[4 * q + 2 * j] = (float)(p * r.x - s * r.y);
                 y[4 * q + 2 * j + 1] = (float)(s * r.x + p * r.y);
             }
         } else {
             const bool low = at < by.half;
+            const double2* four = turns + ((low ? at : at - by.half) >> 2);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const double2 r = turns[(low ? at : at - by.half) + j];
-                const double own = x[4 * q + j];
-                const double other = (j & 1) ? T::high(c.other[q][j >> 1]) : T::low(c.other[q][j >> 1]);
-                y[4 * q + j] = (float)(own * r.x + other * (low ? -r.y : r.y));
+                const double2 r = four[j * step];
+                y[4 * q + j] = (float)((double)x[j] * r.x + (double)z[j] * (low ? -r.y : r.y));
             }
         }
     }
 }
 
 // The same into pages of 4 bits.  Keys and values go in chunks of eight
-// elements a lane, four lanes a group of 32, so that a group's largest
-// element is two exchanges away; a chunk's partners are loaded beside it (from the
-// cache: the same row).
-template <class T, int C, int N>
-__global__ __launch_bounds__(64 * kRopeWaves) void kv_append_q4_kernel(AppendRopeArgs a, int token0, int units,
-                                                                       int q_slices, int slices) {
+// elements a lane, whole heads side by side: four lanes are a group of 32, so that
+// its largest element is two exchanges away, and the elements that a chunk
+// turns with come from other lanes.  A token's work is a row of batches: of
+// its queries (N / 2 units a lane), its keys, its values (N chunks a lane).  A wave
+// takes `per` of them, the next one's loads in flight while it works on one,
+// so that a prompt's tokens pay the chain and the cosines once or twice.
+template <class T, int C, int D, int N>
+__global__ __launch_bounds__(64 * kRopeWaves) void kv_append_q4_kernel(AppendRopeArgs a, int token0, Divisor units,
+                                                                       int q_batches, int kv_batches, int per, int slices) {
     __shared__ double2 lds[kRopeWaves][kMaxHalf];
     const Task task = task_of(token0, slices);
     const int t = task.token;
     if (t >= a.to.tokens) return;
-    const int lane = threadIdx.x & 63, D = a.to.head_dim;
+    constexpr int kChunks = D / 8, kHeads = 64 / kChunks;           // of a head; heads of the wave's lanes
+    const int lane = threadIdx.x & 63, q_all = a.q_heads * (int)units.d;
+    const int my_head = min(lane / kChunks, kHeads - 1), at = lane % kChunks * 8;
     double2* turns = lds[threadIdx.x >> 6];
-    if (task.slice < q_slices) {
-        const int all = a.q_heads * units, first = task.slice * (64 * N) + lane;
-        Vectors<C> v[N];
-        Unit<C> u[N];
-        int head[N];
+    const int first = task.slice * per, last = min(first + per, q_batches + 2 * kv_batches);
+
+    struct Batch { uint32_t w[N][4]; };
+    auto unit_at = [&](int i, int& head) {
+        head = units.quotient((uint32_t)i);
+        return unit_of<C>(a.by, D, i - head * (int)units.d);
+    };
+    auto load = [&](Batch& x, int b) {
+        if (b < q_batches) {
+            const uint16_t* q = a.q + t * a.sq;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int i = min(first + 64 * n, all - 1);
-            head[n] = i / units;
-            u[n] = unit_of<C>(a.by, D, i - head[n] * units);
-            load_unit(v[n], u[n], a.q + t * a.sq + head[n] * D);
-        }
-        const Target to = target_of(a.to.kv, t);
-        if (to.seq < 0) return;
-        turns_to_lds(turns, a.by, to.pos);
+            for (int n = 0; n < N / 2; ++n) {
+                int head;
+                const Unit<C> u = unit_at(min((b * (N / 2) + n) * 64 + lane, q_all - 1), head);
+                Vectors<C> y;
+                load_unit(y, u, q + head * D);
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            if (first + 64 * n >= all) continue;
-            turn_unit<T>(v[n], u[n], a.by, turns);
-            store_unit(v[n], u[n], a.q_out + t * a.sqo + head[n] * D);
-        }
-        return;
-    }
-    const int chunks = D / 8, half_all = a.to.kv_heads * chunks, all = 2 * half_all;       // of keys, then of values
-    const int first = (task.slice - q_slices) * (64 * N) + lane;
-    Chunk c[N];
-    int head[N];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        // (Lanes past the end repeat the last chunk's group in its order: `all` is a multiple of 4.)
-        const int i = first + 64 * n < all ? first + 64 * n : all - 4 + (lane & 3);
-        const bool key = i < half_all;
-        const int j = key ? i : i - half_all;
-        head[n] = j / chunks;
-        c[n].at = (j - head[n] * chunks) * 8;
-        const uint16_t* from = (key ? a.to.k_new + t * a.to.sk : a.to.v_new + t * a.to.sv) + head[n] * D;
-        load_words<4>(c[n].own, from + c[n].at);
-        if (key && !a.by.interleaved) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) load_words<2>(c[n].other[q], from + partner(a.by, c[n].at + 4 * q));
-        }
-    }
-    const Target to = target_of(a.to.kv, t);
-    if (to.page < 0) return;
-    if ((task.slice - q_slices) * (64 * N) < half_all) turns_to_lds(turns, a.by, to.pos);
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const int i = first + 64 * n;
-        const bool key = i < half_all;
-        float x[8];
-        if (key) {
-            turned_chunk<T>(x, c[n], a.by, turns);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[2 * j] = T::low(c[n].own[j]);
-                x[2 * j + 1] = T::high(c[n].own[j]);
+                for (int j = 0; j < C / 2; ++j) {
+                    x.w[2 * n][j] = y.a[0][j];
+                    x.w[2 * n + 1][j] = y.a[1][j];
+                }
             }
+            return;
         }
-        uint32_t e;
-        const uint32_t codes = q4_encode<T>(x, e);
-        if (i >= all) continue;
-        const Q4Row at(to.page, a.to.kv_heads, a.to.kv.page_shift, D, head[n], to.row);
+        const bool key = b < q_batches + kv_batches;
+        const uint16_t* row = key ? a.to.k_new + t * a.to.sk : a.to.v_new + t * a.to.sv;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int head = ((b - q_batches - (key ? 0 : kv_batches)) * N + n) * kHeads + my_head;
+            // (Nobody reads these rows again.)
+            const u4 own = __builtin_nontemporal_load(reinterpret_cast<const u4*>(row + (min(head, a.to.kv_heads - 1) * D + at)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x.w[n][j] = own[j];
+        }
+    };
+    Batch x, y;
+    load(x, first);
+    const Target to = target_of(a.to.kv, t);
+    if (to.seq < 0) return;
+    if (first < q_batches + kv_batches) turns_to_lds(turns, a.by, to.pos);
+
+    // The lane that holds what this one's first four turn with, and whether its fours are the other way
+    // round (halves that begin in the middle of a chunk; then of no other lane than the first four's).
+    const bool crossed = (a.by.half & 7) != 0;
+    auto lane_of = [&](int four) {
+        const int f = at + 4 * four, p = f >= 2 * a.by.half ? f : f < a.by.half ? f + a.by.half : f - a.by.half;
+        return 4 * (lane - at / 8 + p / 8);
+    };
+    const int from[2] = {lane_of(0), lane_of(1)};
+
+    auto work = [&](const Batch& x, int b) {
+        if (b < q_batches) {
+#pragma unroll
+            for (int n = 0; n < N / 2; ++n) {
+                const int i = (b * (N / 2) + n) * 64 + lane;
+                if (i >= q_all) continue;
+                int head;
+                const Unit<C> u = unit_at(i, head);
+                Vectors<C> y;
+#pragma unroll
+                for (int j = 0; j < C / 2; ++j) {
+                    y.a[0][j] = x.w[2 * n][j];
+                    y.a[1][j] = x.w[2 * n + 1][j];
+                }
+                turn_unit<T>(y, u, a.by, turns);
+                store_unit(y, u, a.q_out + t * a.sqo + head * D);
+            }
+            return;
+        }
+        if (to.page < 0) return;
+        const bool key = b < q_batches + kv_batches;
         unsigned char* pool = reinterpret_cast<unsigned char*>(const_cast<uint16_t*>(key ? a.to.kv.k : a.to.kv.v));
-        *reinterpret_cast<uint32_t*>(pool + at.codes + c[n].at / 2) = codes;
-        if ((lane & 3) == 0) pool[at.scales + (c[n].at / 32) * 16] = (unsigned char)e;
+        const Q4Row row(to.page, a.to.kv_heads, a.to.kv.page_shift, D, 0, to.row);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float z[8];
+            if (key) {
+                uint32_t other[4] = {0, 0, 0, 0};
+                if (a.by.half && !a.by.interleaved) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t word = crossed ? x.w[n][j ^ 2] : x.w[n][j];
+                        other[j] = (uint32_t)__builtin_amdgcn_ds_bpermute(from[j >> 1], (int)word);
+                    }
+                }
+                turned_chunk<T>(z, x.w[n], other, at, a.by, turns);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    z[2 * j] = T::low(x.w[n][j]);
+                    z[2 * j + 1] = T::high(x.w[n][j]);
+                }
+            }
+            uint32_t e;
+            const uint32_t codes = q4_encode<T>(z, e);
+            const int head = ((b - q_batches - (key ? 0 : kv_batches)) * N + n) * kHeads + my_head;
+            if (lane >= kHeads * kChunks || head >= a.to.kv_heads) continue;
+            const uint32_t of_head = (uint32_t)head << a.to.kv.page_shift;        // rows before this head's
+            *reinterpret_cast<uint32_t*>(pool + row.codes + (of_head * (D / 2) + at / 2)) = codes;
+            if ((lane & 3) == 0) pool[row.scales + (of_head * (D / 32) + at / 32 * 16)] = (unsigned char)e;
+        }
+    };
+    for (int b = first;;) {
+        if (b + 1 < last) load(y, b + 1);
+        work(x, b);
+        if (++b >= last) break;
+        if (b + 1 < last) load(x, b + 1);
+        work(y, b);
+        if (++b >= last) break;
     }
 }
 
-// Rows of 4-bit pages as halves again.
+// Rows of 4-bit pages as halves again.  Bound by HBM: 8763 tokens of 32 heads of
+// 128, 143 MB written, 30 us with stores that pass the caches by, 39 with
+// those that fill them (and what reads the rows next comes from elsewhere: a copy of the
+// cache, not the attention).  The appends' stores stay in the caches: past them
+// the same 8763 tokens' append alone takes 42.5 us instead of 45.8, with the
+// attention that follows 205.5 instead of 199.7.
 template <class T, int N>
 __global__ __launch_bounds__(64 * kRopeWaves) void kv_read_q4_kernel(AppendArgs a, int token0, int slices) {
     const Task task = task_of(token0, slices);
@@ -260,7 +306,10 @@ __global__ __launch_bounds__(64 * kRopeWaves) void kv_read_q4_kernel(AppendArgs 
         if (i >= 2 * half_all) continue;
         uint16_t* y = const_cast<uint16_t*>(i < half_all ? a.k_new + t * a.sk : a.v_new + t * a.sv);
         const u4 x = q4_values<T>(codes[n], q4_scale(e[n]));
-        *reinterpret_cast<u4*>(y + head[n] * D + at[n]) = to.page >= 0 ? x : u4{0, 0, 0, 0};
+        u4* at_y = reinterpret_cast<u4*>(y + head[n] * D + at[n]);
+        const u4 z = to.page >= 0 ? x : u4{0, 0, 0, 0};
+        if constexpr (N > 1) __builtin_nontemporal_store(z, at_y);
+        else *at_y = z;
     }
 }
 
@@ -290,13 +339,17 @@ hipError_t append_rope(const AppendRopeArgs& a, hipStream_t stream) {
     });
 }
 
-template <class T, int C, int N>
-hipError_t append_q4(const AppendRopeArgs& a, hipStream_t stream) {
-    const int D = a.to.head_dim, units = units_of(a.by, D, C);
-    const int q_slices = (a.q_heads * units + 64 * N - 1) / (64 * N);
-    const int slices = q_slices + (a.to.kv_heads * (D / 8) * 2 + 64 * N - 1) / (64 * N);
+// per: batches a wave takes.
+template <class T, int C, int D, int N>
+hipError_t append_q4(const AppendRopeArgs& a, int per, hipStream_t stream) {
+    constexpr int kHeads = 64 / (D / 8) * N;                            // of a batch of keys or values
+    const int units = units_of(a.by, D, C);
+    const int q_batches = (a.q_heads * units + 32 * N - 1) / (32 * N), kv_batches = (a.to.kv_heads + kHeads - 1) / kHeads;
+    const int slices = (q_batches + 2 * kv_batches + per - 1) / per;
+    per = (q_batches + 2 * kv_batches + slices - 1) / slices;           // as even as they come
     return in_parts(a.to.tokens, slices, [&](int t, dim3 grid) {
-        hipLaunchKernelGGL((kv_append_q4_kernel<T, C, N>), grid, kBlock, 0, stream, a, t, units, q_slices, slices);
+        hipLaunchKernelGGL((kv_append_q4_kernel<T, C, D, N>), grid, kBlock, 0, stream, a, t, Divisor(units), q_batches,
+                           kv_batches, per, slices);
     });
 }
 
@@ -314,9 +367,18 @@ template <class T, int C>
 hipError_t append_rope_n(const AppendRopeArgs& a, hipStream_t stream) {
     return a.to.tokens >= kManyTokens ? append_rope<T, C, 4>(a, stream) : append_rope<T, C, 1>(a, stream);
 }
-template <class T, int C>
+template <class T, int C, int D>
 hipError_t append_q4_n(const AppendRopeArgs& a, hipStream_t stream) {
-    return a.to.tokens >= kManyTokens ? append_q4<T, C, 4>(a, stream) : append_q4<T, C, 1>(a, stream);
+    return a.to.tokens >= kManyTokens ? append_q4<T, C, D, 4>(a, 5, stream) : append_q4<T, C, D, 2>(a, 1, stream);
+}
+template <class T, int C>
+hipError_t append_q4_dim(const AppendRopeArgs& a, hipStream_t stream) {
+    switch (a.to.head_dim) {
+        case 64: return append_q4_n<T, C, 64>(a, stream);
+        case 96: return append_q4_n<T, C, 96>(a, stream);
+        case 128: return append_q4_n<T, C, 128>(a, stream);
+        default: return append_q4_n<T, C, 256>(a, stream);
+    }
 }
 template <class T>
 hipError_t read_q4_n(const AppendArgs& a, hipStream_t stream) {
@@ -333,8 +395,8 @@ hipError_t launch_kv_append_rope(const AppendRopeArgs& a, hipStream_t stream) {
 
 hipError_t launch_kv_append_q4(const AppendRopeArgs& a, hipStream_t stream) {
     const bool wide = rope_vector(a.by) == 8;
-    if (a.dtype == 0) return wide ? append_q4_n<Fp16, 8>(a, stream) : append_q4_n<Fp16, 4>(a, stream);
-    return wide ? append_q4_n<Bf16, 8>(a, stream) : append_q4_n<Bf16, 4>(a, stream);
+    if (a.dtype == 0) return wide ? append_q4_dim<Fp16, 8>(a, stream) : append_q4_dim<Fp16, 4>(a, stream);
+    return wide ? append_q4_dim<Bf16, 8>(a, stream) : append_q4_dim<Bf16, 4>(a, stream);
 }
 
 hipError_t launch_kv_read_q4(const AppendArgs& a, int dtype, hipStream_t stream) {

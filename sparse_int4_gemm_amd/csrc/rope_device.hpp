@@ -17,13 +17,19 @@ __device__ __forceinline__ double2 turn_of(const Rotation& by, int p, int i) {
     return make_double2(c * by.magnitude, s * by.magnitude);
 }
 
+// Where pair i lies in LDS: lanes work on fours of pairs, so those of the same
+// place in their fours lie side by side (in the order of the pairs, sixteen
+// lanes' would share a bank).
+__device__ __forceinline__ int turn_place(const Rotation& by, int i) { return (i & 3) * (by.half >> 2) + (i >> 2); }
+
 // All pairs of position p to the wave's own part of LDS.
 template <class Turn>
 __device__ __forceinline__ void turns_to_lds(Turn* to, const Rotation& by, int p) {
     for (int i = threadIdx.x & 63; i < by.half; i += 64) {
         const double2 t = turn_of(by, p, i);
-        to[i].x = t.x;
-        to[i].y = t.y;
+        Turn& at = to[turn_place(by, i)];
+        at.x = t.x;
+        at.y = t.y;
     }
     // The wave's own LDS accesses are served in order; only the compiler must keep it.
     __builtin_amdgcn_wave_barrier();
@@ -100,10 +106,13 @@ __device__ __forceinline__ void turn_unit(Vectors<C>& v, const Unit<C>& u, const
             x[i][2 * j + 1] = T::high(v.a[i][j]);
         }
     float c[C], s[C];
+    const Turn* fours = turns + (u.pair >> 2);
+    const int step = by.half >> 2;
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-        c[k] = (float)turns[u.pair + k].x;
-        s[k] = (float)turns[u.pair + k].y;
+        const Turn t = fours[(k & 3) * step + (k >> 2)];          // turn_place of pair + k
+        c[k] = (float)t.x;
+        s[k] = (float)t.y;
     }
     auto turn = [](float& a, float& b, float cos, float sin) {
         const float y = a * cos - b * sin;
