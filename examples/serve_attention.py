@@ -1,14 +1,15 @@
 """The attention half of a decoder block served with this library: compressed
-q/k/v/o projections (slim.linear), a paged key-value cache (slim.KVCache),
-attention of the prompts (slim.attention_prefill) and of single tokens
-(slim.attention_decode).
+q/k/v/o projections (slim.linear), rotary positions on the way to a paged
+key-value cache (slim.kv_append_rope, slim.KVCache), attention of the prompts
+(slim.attention_prefill) and of single tokens (slim.attention_decode); with
+--cache-bits 4 the same over a cache of 4 bits a value.
 
 Prompts of different lengths are prefilled together, one conversation is
 forked, all of them decode some tokens, one ends, the cache is compacted and the
 rest go on.  Weights and inputs are random; the last outputs are compared with
 plain float32 attention over the cached keys and values.
 
-  python examples/serve_attention.py [--hidden 4096] [--kv-heads 32] [--steps 32] [--window 0]
+  python examples/serve_attention.py [--hidden 4096] [--kv-heads 32] [--steps 32] [--window 0] [--cache-bits 16]
 """
 from __future__ import annotations
 
@@ -42,17 +43,8 @@ class Projection:
         return slim.linear(x, self.w, self.lt, self.rt, ws=self.ws[m])
 
 
-def rotate(x, positions, base=10000.0):
-    """Rotary positions on [tokens, heads, HEAD_DIM] (first and second half of a head paired)."""
-    half = HEAD_DIM // 2
-    freq = base ** (-torch.arange(half, device=x.device, dtype=torch.float32) / half)
-    angle = positions.float()[:, None, None] * freq
-    a, b = x.float()[..., :half], x.float()[..., half:]
-    return torch.cat([a * angle.cos() - b * angle.sin(), b * angle.cos() + a * angle.sin()], -1).to(x.dtype)
-
-
 class AttentionBlock:
-    def __init__(self, hidden, kv_heads, pages, page_size, window, sinks, seed=0):
+    def __init__(self, hidden, kv_heads, pages, page_size, window, sinks, cache_bits=16, seed=0):
         gen = torch.Generator(device="cuda")
         gen.manual_seed(seed)
         self.q_heads, self.kv_heads = hidden // HEAD_DIM, kv_heads
@@ -60,28 +52,31 @@ class AttentionBlock:
         rank = max(32, hidden // 10 // 32 * 32)
         self.q, self.k, self.v = (Projection(gen, n * HEAD_DIM, hidden, rank) for n in (self.q_heads, kv_heads, kv_heads))
         self.o = Projection(gen, hidden, hidden, rank)
-        self.cache = slim.KVCache(1, pages, kv_heads, HEAD_DIM, page_size=page_size)
+        self.cache = slim.KVCache(1, pages, kv_heads, HEAD_DIM, page_size=page_size, bits=cache_bits)
+        self.rope = slim.Rope(HEAD_DIM)
         self.ws = slim.workspace_attention(1, 1, self.q_heads, kv_heads, HEAD_DIM)     # serves every batch of these heads
 
     def step(self, x, seqs, counts):
         """x [tokens, hidden]: counts[i] new tokens of seqs[i].  Returns the block's
-        output, the queries and the attention's output (for the check)."""
+        output, the turned queries and the attention's output (for the check)."""
         if self.window:                   # (only now: the tokens of the step before saw these pages)
             for s in seqs:
                 self.cache.drop(s, self.window, self.sinks)
         batch = self.cache.extend(seqs, counts)
-        at = [p for s, c in zip(seqs, counts) for p in range(self.cache.length(s) - c, self.cache.length(s))]
-        positions = torch.tensor(at, device=x.device)
-        q = rotate(self.q(x).view(-1, self.q_heads, HEAD_DIM), positions)
-        k = rotate(self.k(x).view(-1, self.kv_heads, HEAD_DIM), positions)
+        q = self.q(x).view(-1, self.q_heads, HEAD_DIM)
+        k = self.k(x).view(-1, self.kv_heads, HEAD_DIM)
         v = self.v(x).view(-1, self.kv_heads, HEAD_DIM)
         pools = (self.cache.k[0], self.cache.v[0])
-        slim.kv_append(k, v, *pools, batch.table, batch.lens, batch.starts)
+        if self.cache.bits == 4:
+            append, decode, prefill = slim.kv_append_q4, slim.attention_decode_q4, slim.attention_prefill_q4
+        else:
+            append, decode, prefill = slim.kv_append_rope, slim.attention_decode, slim.attention_prefill
+        append(k, v, *pools, batch.table, batch.lens, rope=self.rope, starts=batch.starts, q=q, q_out=q)
         kw = dict(max_len=batch.max_len, window=self.window, sinks=self.sinks, ws=self.ws)
         if all(c == 1 for c in counts):
-            y = slim.attention_decode(q, *pools, batch.table, batch.lens, **kw)
+            y = decode(q, *pools, batch.table, batch.lens, **kw)
         else:
-            y = slim.attention_prefill(q, *pools, batch.table, batch.lens, batch.starts, **kw)
+            y = prefill(q, *pools, batch.table, batch.lens, batch.starts, **kw)
         return self.o(y.reshape(x.shape[0], -1)), q, y
 
     def plain(self, q, seq):
@@ -90,9 +85,14 @@ class AttentionBlock:
         j = torch.arange(n, device="cuda")
         seen = (j > n - 1 - self.window) | (j < self.sinks) if self.window else j >= 0
         j = j[seen]
-        page = torch.tensor(pages, device="cuda")[j // size]
-        share = self.q_heads // self.kv_heads
-        k, v = (pool[0][page, :, j % size].float().repeat_interleave(share, 1) for pool in (self.cache.k, self.cache.v))
+        if self.cache.bits == 4:
+            ints = torch.tensor([*pages, n, 0, n], dtype=torch.int32, device="cuda")
+            k, v = slim.kv_read_q4(self.cache.k[0], self.cache.v[0], ints[None, :-3], ints[-3:-2], ints[-2:], n)
+            k, v = k[j], v[j]
+        else:
+            page = torch.tensor(pages, device="cuda")[j // size]
+            k, v = (pool[0][page, :, j % size] for pool in (self.cache.k, self.cache.v))
+        k, v = (x.float().repeat_interleave(self.q_heads // self.kv_heads, 1) for x in (k, v))
         s = (k * q.float()).sum(-1) * HEAD_DIM ** -0.5
         w = torch.exp(s - s.amax(0))
         return (w[..., None] * v).sum(0) / w.sum(0)[:, None]
@@ -104,9 +104,10 @@ def main(argv=None):
     ap.add_argument("--kv-heads", type=int, default=32)
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--window", type=int, default=0)
+    ap.add_argument("--cache-bits", type=int, choices=(4, 16), default=16)
     a = ap.parse_args(argv)
     prompts = [700, 33, 256]
-    block = AttentionBlock(a.hidden, a.kv_heads, 200, 64, a.window, 4 if a.window else 0)
+    block = AttentionBlock(a.hidden, a.kv_heads, 200, 64, a.window, 4 if a.window else 0, a.cache_bits)
     cache = block.cache
     gen = torch.Generator(device="cuda")
     gen.manual_seed(1)
