@@ -333,11 +333,22 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void attention_decod
     }
 }
 
-// The plan: kWavesTarget waves in all (16 a CU; 8 at head size 256, whose
-// registers hold no more), each with at least kMinTiles tiles.  Those of a key
-// head share a workgroup up to 16 (8), and only beyond that the keys are split
-// over workgroups, at the cost of partial results and another launch.
-constexpr int kCus = 256, kMinTiles = 4, kSortFrom = 512;
+// The plan.  Where there are enough key heads for all CUs, and for short
+// lengths, one workgroup a key head.  It has 16 waves (8 at head size 256, whose
+// registers hold no more) or 8 or 4, so that all workgroups run at once (ten
+// sequences of 32 key heads and 2000 keys: 30.0 us with 16 waves, 25.3 with 8), and
+// that a wave has some four tiles (500 keys of 32 key heads, four tiles for each of 4 waves or two of 8: one sequence
+// 7.8 us with 4 and 7.4 with 8, nine 10.9 and 11.5).  More waves a workgroup and
+// fewer workgroups of the same keys save the join: 32 sequences of 8 key heads in a
+// window 19.5 us with 16 waves, 24.3 with 4 and the keys split.
+// Otherwise the keys are split over workgroups, where that spares a SIMD
+// kSplitFrom tiles (0.4 us each); that is what partial results and another
+// launch cost: of 32 query heads on 8, 2000 keys of one sequence 13.6 us whole
+// and 9.6 split, of four 13.8 and 11.4, of eight 14.3 and 15.0, of sixteen 14.7 and 16.5.
+// The workgroups are then as small as gives at most kSplits of a key head (one sequence of 8000:
+// 11.7 us with 62 of 4 waves, 10.6 with 31 of 8, 12.4 with 15 of 16; 131071: 39.1 with 64 of 8, 35.7 with 32 of 16)
+// and two a CU (four of 8000: 17.1 with 1024 of 4 waves, 16.3 with 512 of 8).
+constexpr int kCus = 256, kSplitFrom = 10, kSplits = 32, kSortFrom = 512;
 
 template <class T, int D, int kWaves>
 hipError_t launch_waves(const AttnArgs& a, int splits, int tiles, int64_t most, hipStream_t stream) {
@@ -345,7 +356,8 @@ hipError_t launch_waves(const AttnArgs& a, int splits, int tiles, int64_t most, 
     const int64_t units = (int64_t)a.tokens * a.kv_heads * groups;
     const int chunk = max(kWaves, (tiles + splits - 1) / splits);
     dim3 grid((unsigned)(a.tokens * splits), (unsigned)(a.kv_heads * groups));
-    // More than a round of workgroups: longest first (attention_decode.hip).
+    // More than a round of workgroups: longest first (attention_decode.hip; 64 sequences of 1 to 4096
+    // keys, 32 heads: 105 us, 142 in their order).
     const int sort_most = kWaves == 4 && splits == 1 && units > 2 * kCus && most >= kSortFrom ? (int)most : 0;
     hipLaunchKernelGGL((attention_decode_q4_kernel<T, D, kWaves>), grid, dim3(64 * kWaves), 0, stream, a, splits, chunk,
                        groups, sort_most);
@@ -361,12 +373,19 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     if (a.window && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;
     const int tiles = (int)((most + kTile - 1) / kTile);
     const int64_t units = (int64_t)a.tokens * a.kv_heads * groups;
-    const int64_t waves = min(kCus * kMost / units, (int64_t)(tiles + kMinTiles - 1) / kMinTiles);
-    if (waves <= 4) return launch_waves<T, D, 4>(a, 1, tiles, most, stream);
-    if (waves <= 8 && kMost == 16) return launch_waves<T, D, 8>(a, 1, tiles, most, stream);
-    const int64_t rows = (int64_t)a.tokens * a.q_heads;
-    const int splits = (int)max((int64_t)1, min(waves / kMost, kAttnSplitRows / rows));
-    return launch_waves<T, D, kMost>(a, splits, tiles, most, stream);
+    const int64_t budget = kCus * kMost / units;             // waves of a key head that run at once
+    if (tiles * (kCus - units) <= kSplitFrom * 4 * kCus) {
+        const int few = units > kCus ? 4 : 2, wanted = (tiles + 3) / 4;
+        if (wanted <= few || budget < 8) return launch_waves<T, D, 4>(a, 1, tiles, most, stream);
+        if (wanted <= 8 || budget < 16 || kMost == 8) return launch_waves<T, D, 8>(a, 1, tiles, most, stream);
+        return launch_waves<T, D, kMost>(a, 1, tiles, most, stream);
+    }
+    const int64_t waves = min(budget, (int64_t)tiles), limit = kAttnSplitRows / ((int64_t)a.tokens * a.q_heads);
+    auto splits = [&](int w) { return max((int64_t)1, min(waves / w, limit)); };
+    auto few = [&](int w) { return splits(w) <= kSplits && units * splits(w) <= 2 * kCus; };
+    if (few(4)) return launch_waves<T, D, 4>(a, (int)splits(4), tiles, most, stream);
+    if (kMost == 16 && few(8)) return launch_waves<T, D, 8>(a, (int)splits(8), tiles, most, stream);
+    return launch_waves<T, D, kMost>(a, (int)splits(kMost), tiles, most, stream);
 }
 
 template <class T>

@@ -8,7 +8,8 @@
 // writes what it loaded before.  Waves do not wait for each other, so a
 // token cut over several only costs each of them the chain again.  Bound by HBM
 // for prompts (halves: 4 bytes an element; 4 bits: 2.5), by launch and that chain for
-// single tokens.
+// single tokens.  Of 32 heads of 128, with their queries: 64 tokens 3.4 us into halves
+// and 4.6 into 4 bits, 8192 tokens 80 us (5.0 TB/s) and 65 (4.6 TB/s).
 #include "kv_q4.hpp"
 #include "rope_device.hpp"
 
@@ -16,7 +17,6 @@ namespace slim {
 namespace {
 
 constexpr int kMaxHalf = 128;                 // head_dim is at most 256
-constexpr int kManyTokens = 512;              // from here on a lane takes several units
 
 // Where a token's new row goes.
 struct Target {
@@ -272,9 +272,9 @@ __global__ __launch_bounds__(64 * kRopeWaves) void kv_append_q4_kernel(AppendRop
     }
 }
 
-// Rows of 4-bit pages as halves again.  Bound by HBM: 8763 tokens of 32 heads of
-// 128, 143 MB written, 30 us with stores that pass the caches by, 39 with
-// those that fill them (and what reads the rows next comes from elsewhere: a copy of the
+// Rows of 4-bit pages as halves again.  Bound by HBM: 8192 tokens of 32 heads of
+// 128, 134 MB written and 36 read, 30 us (5.7 TB/s).  The stores pass the caches by: with
+// those that fill them 8763 tokens took 39 us instead of 30 (and what reads the rows next comes from elsewhere: a copy of the
 // cache, not the attention).  The appends' stores stay in the caches: past them
 // the same 8763 tokens' append alone takes 42.5 us instead of 45.8, with the
 // attention that follows 205.5 instead of 199.7.
@@ -329,47 +329,65 @@ hipError_t in_parts(int64_t tokens, int slices, Launch&& launch) {
 const dim3 kBlock(64 * kRopeWaves);
 
 template <class T, int C, int N>
-hipError_t append_rope(const AppendRopeArgs& a, hipStream_t stream) {
-    const Rotation none = {nullptr, 0, 0, 1.0};
-    const int D = a.to.head_dim, units = units_of(a.by, D, C), v_units = units_of(none, D, C);
-    const int all = (a.q_heads + a.to.kv_heads) * units + a.to.kv_heads * v_units;
+hipError_t append_rope(const AppendRopeArgs& a, int units, int v_units, int all, hipStream_t stream) {
     const int slices = (all + 64 * N - 1) / (64 * N);
     return in_parts(a.to.tokens, slices, [&](int t, dim3 grid) {
         hipLaunchKernelGGL((kv_append_rope_kernel<T, C, N>), grid, kBlock, 0, stream, a, t, units, v_units, slices);
     });
 }
 
+// Batches of a token, N as the kernel's.
+template <int C, int D, int N>
+struct Batches {
+    int units, of_q, of_kv;
+    explicit Batches(const AppendRopeArgs& a) {
+        constexpr int kHeads = 64 / (D / 8) * N;                        // of a batch of keys or values
+        units = units_of(a.by, D, C);
+        of_q = (a.q_heads * units + 32 * N - 1) / (32 * N);
+        of_kv = (a.to.kv_heads + kHeads - 1) / kHeads;
+    }
+    int all() const { return of_q + 2 * of_kv; }
+};
+
 // per: batches a wave takes.
 template <class T, int C, int D, int N>
 hipError_t append_q4(const AppendRopeArgs& a, int per, hipStream_t stream) {
-    constexpr int kHeads = 64 / (D / 8) * N;                            // of a batch of keys or values
-    const int units = units_of(a.by, D, C);
-    const int q_batches = (a.q_heads * units + 32 * N - 1) / (32 * N), kv_batches = (a.to.kv_heads + kHeads - 1) / kHeads;
-    const int slices = (q_batches + 2 * kv_batches + per - 1) / per;
-    per = (q_batches + 2 * kv_batches + slices - 1) / slices;           // as even as they come
+    const Batches<C, D, N> n(a);
+    const int slices = (n.all() + per - 1) / per;
+    per = (n.all() + slices - 1) / slices;                              // as even as they come
     return in_parts(a.to.tokens, slices, [&](int t, dim3 grid) {
-        hipLaunchKernelGGL((kv_append_q4_kernel<T, C, D, N>), grid, kBlock, 0, stream, a, t, Divisor(units), q_batches,
-                           kv_batches, per, slices);
+        hipLaunchKernelGGL((kv_append_q4_kernel<T, C, D, N>), grid, kBlock, 0, stream, a, t, Divisor(n.units), n.of_q,
+                           n.of_kv, per, slices);
     });
 }
 
 template <class T, int N>
-hipError_t read_q4(const AppendArgs& a, hipStream_t stream) {
-    const int slices = (a.kv_heads * (a.head_dim / 8) * 2 + 64 * N - 1) / (64 * N);
+hipError_t read_q4(const AppendArgs& a, int all, hipStream_t stream) {
+    const int slices = (all + 64 * N - 1) / (64 * N);
     return in_parts(a.tokens, slices, [&](int t, dim3 grid) {
         hipLaunchKernelGGL((kv_read_q4_kernel<T, N>), grid, kBlock, 0, stream, a, t, slices);
     });
 }
 
-// A token's rows are cut over as many waves as they fill with one unit a lane for
-// few tokens (latency), four units a lane for many (loads in flight).
+// How much a lane takes (32 heads of 128): one unit for few tokens, so that
+// what a token needs is spread over as many waves as can be, more where
+// the waves fill the processor anyway.  Halves: 256 tokens 4.6 us with one unit and 5.1
+// with two, 512 7.8 and 7.2, 4096 43.5 and 43.3 (four: 44.8).  4 bits: 512 tokens (0.75 of a
+// round of waves) 10.0 us with a batch of two and 11.0 with five of four, 1024
+// 15.4 and 14.0, 4096 46.3 and 34.6.  Reading back: 256 tokens 4.0 us with one and
+// 4.3 with eight, 512 5.5 and 4.5, 4096 24.1 and 16.6 (four: 18.9, sixteen: 16.9).
 template <class T, int C>
 hipError_t append_rope_n(const AppendRopeArgs& a, hipStream_t stream) {
-    return a.to.tokens >= kManyTokens ? append_rope<T, C, 4>(a, stream) : append_rope<T, C, 1>(a, stream);
+    const Rotation none = {nullptr, 0, 0, 1.0};
+    const int D = a.to.head_dim, units = units_of(a.by, D, C), v_units = units_of(none, D, C);
+    const int all = (a.q_heads + a.to.kv_heads) * units + a.to.kv_heads * v_units;
+    return rounds(a.to.tokens, all) > 0.5f ? append_rope<T, C, 2>(a, units, v_units, all, stream)
+                                           : append_rope<T, C, 1>(a, units, v_units, all, stream);
 }
 template <class T, int C, int D>
 hipError_t append_q4_n(const AppendRopeArgs& a, hipStream_t stream) {
-    return a.to.tokens >= kManyTokens ? append_q4<T, C, D, 4>(a, 5, stream) : append_q4<T, C, D, 2>(a, 1, stream);
+    return rounds(a.to.tokens, 64 * Batches<C, D, 2>(a).all()) > 1.0f ? append_q4<T, C, D, 4>(a, 5, stream)
+                                                                      : append_q4<T, C, D, 2>(a, 1, stream);
 }
 template <class T, int C>
 hipError_t append_q4_dim(const AppendRopeArgs& a, hipStream_t stream) {
@@ -382,7 +400,8 @@ hipError_t append_q4_dim(const AppendRopeArgs& a, hipStream_t stream) {
 }
 template <class T>
 hipError_t read_q4_n(const AppendArgs& a, hipStream_t stream) {
-    return a.tokens >= kManyTokens ? read_q4<T, 4>(a, stream) : read_q4<T, 1>(a, stream);
+    const int all = a.kv_heads * (a.head_dim / 8) * 2;
+    return rounds(a.tokens, all) > 0.5f ? read_q4<T, 8>(a, all, stream) : read_q4<T, 1>(a, all, stream);
 }
 
 }  // namespace

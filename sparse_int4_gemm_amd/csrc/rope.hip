@@ -8,6 +8,8 @@
 // sines itself, in fp64, into its own part of LDS: a table of them would be
 // read from HBM (8 bytes a pair) and end at some position.  The rows' loads
 // are issued first and are in flight meanwhile.
+//
+// 4096 tokens of 32 heads of 128: 11.8 us, 5.7 TB/s, as a plain copy; one token 2.1 us.
 #include "rope_device.hpp"
 
 namespace slim {
@@ -46,10 +48,13 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_kernel(RopeArgs a, int u
     }
 }
 
+// One unit a lane while the processor holds all waves at once, so that a token's
+// chain is as short as can be, else four, so that fewer waves form its cosines
+// (32 heads of 128, 512 tokens: 3.3 us with one, 4.3 with four; 2048, a round: 8.2 and 8.3; 4096: 13.3 and 11.8).
 template <class T, int C>
 hipError_t launch(const RopeArgs& a, hipStream_t stream) {
     const int units = units_of(a.by, a.head_dim, C), all = a.heads * units;
-    const int n = a.tokens >= 512 ? 4 : 1, slices = (all + 64 * n - 1) / (64 * n);
+    const int n = rounds(a.tokens, all) > 1.0f ? 4 : 1, slices = (all + 64 * n - 1) / (64 * n);
     const int64_t tasks = (int64_t)a.tokens * slices;
     // A grid holds fewer than 2^32 threads; tokens past 2^25 waves go into further launches.
     const int64_t at_once = (int64_t(1) << 25) / slices;

@@ -7,6 +7,9 @@ namespace slim {
 
 constexpr int kRopeWaves = 4;                 // waves of a workgroup; each has its own tokens, none waits for another
 
+// Rounds of waves (32 on each of 256 CUs) that `units` of each token make with one a lane.
+inline float rounds(int64_t tokens, int64_t units) { return (float)(tokens * ((units + 63) / 64)) / (256 * 32); }
+
 // (cos, sin) * magnitude of pair i at position p.  The angle is taken in turns,
 // in fp64: of p * f the fraction of a turn that is left is off by 2^-53 of the number of turns.
 __device__ __forceinline__ double2 turn_of(const Rotation& by, int p, int i) {
