@@ -51,7 +51,10 @@ __device__ __forceinline__ Task task_of(int token0, int slices) {
 }
 
 // Units (rope_device.hpp) of one token: those of the queries' heads, the
-// keys' and the values'; of the values' units all stay as they are.
+// keys' and the values'; of the values' units all stay as they are.  The
+// rows' loads are marked as read once, so that they leave the caches to what is written: 8763
+// tokens of 32 heads on 8 alone 46.0 -> 43.4 us, behind the copies that
+// make the rows 90 -> 79 together, with the attention after them 240 -> 238.
 template <class T, int C, int N>
 __global__ __launch_bounds__(64 * kRopeWaves) void kv_append_rope_kernel(AppendRopeArgs a, int token0, int units,
                                                                          int v_units, int slices) {
@@ -81,7 +84,7 @@ __global__ __launch_bounds__(64 * kRopeWaves) void kv_append_rope_kernel(AppendR
             u[n] = unit_of<C>(none, D, i - k_end - head[n] * v_units);
             from = a.to.v_new + t * a.to.sv;
         }
-        load_unit(v[n], u[n], from + head[n] * D);
+        load_unit<true>(v[n], u[n], from + head[n] * D);
     }
     const Target to = target_of(a.to.kv, t);
     if (to.seq < 0) return;
@@ -175,7 +178,7 @@ __global__ __launch_bounds__(64 * kRopeWaves) void kv_append_q4_kernel(AppendRop
                 int head;
                 const Unit<C> u = unit_at(min((b * (N / 2) + n) * 64 + lane, q_all - 1), head);
                 Vectors<C> y;
-                load_unit(y, u, q + head * D);
+                load_unit<true>(y, u, q + head * D);
 #pragma unroll
                 for (int j = 0; j < C / 2; ++j) {
                     x.w[2 * n][j] = y.a[0][j];

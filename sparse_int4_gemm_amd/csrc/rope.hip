@@ -37,7 +37,7 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_kernel(RopeArgs a, int u
         const int i = min(first + 64 * n, all - 1);
         head[n] = i / units;
         u[n] = unit_of<C>(a.by, a.head_dim, i - head[n] * units);
-        load_unit(v[n], u[n], x + head[n] * a.head_dim);
+        load_unit<false>(v[n], u[n], x + head[n] * a.head_dim);
     }
     turns_to_lds(turns, a.by, a.positions[token]);
 #pragma unroll

@@ -78,10 +78,17 @@ struct Vectors {
     uint32_t a[2][C / 2];
 };
 
-template <int C>
+// kOnce: rows that nobody reads again.
+template <bool kOnce, int C>
 __device__ __forceinline__ void load_unit(Vectors<C>& v, const Unit<C>& u, const uint16_t* head) {
+    using Words = std::conditional_t<C == 8, u4, u2>;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) load_words<C / 2>(v.a[i], head + u.at[i]);
+    for (int i = 0; i < 2; ++i) {
+        const Words* p = reinterpret_cast<const Words*>(head + u.at[i]);
+        const Words x = kOnce ? __builtin_nontemporal_load(p) : *p;
+#pragma unroll
+        for (int j = 0; j < C / 2; ++j) v.a[i][j] = x[j];
+    }
 }
 
 template <int C>
