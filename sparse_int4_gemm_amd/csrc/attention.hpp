@@ -84,6 +84,9 @@ hipError_t launch_kv_append_q4(const AppendRopeArgs& a, hipStream_t stream);
 // k_new, v_new are written.
 hipError_t launch_kv_read_q4(const AppendArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_attention_decode_q4(const AttnArgs& a, hipStream_t stream);
+// Prompts of which each has a few new rows on a key head (few_rows_q4).
+bool few_rows_q4(const AttnArgs& a);
+hipError_t launch_attention_few_q4(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attention_prefill_q4(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_kv_copy_pages(void* k, void* v, int64_t layers, int64_t pages, int64_t page_bytes,
                                 const int32_t* src, const int32_t* dst, int64_t n, hipStream_t stream);

@@ -1,6 +1,6 @@
-// slim_attention_decode_q4: attention of one new token per sequence over pages
-// of 4 bits a value (attention_decode.hip has the mathematics; kv_q4.hpp the
-// format).
+// slim_attention_decode_q4: attention of one new token per sequence, or of a
+// few, over pages of 4 bits a value (attention_decode.hip has the mathematics;
+// kv_q4.hpp the format).
 //
 //   s_j = scale q . k_j,  O = sum_j 2^(c s_j - m) v_j / l.
 //
@@ -101,41 +101,77 @@ __device__ __forceinline__ float column_max(float x) {
     return fmaxf(__builtin_bit_cast(float, s0), __builtin_bit_cast(float, s1));
 }
 
-// kWaves waves a workgroup, each with every kWaves-th tile.
-template <class T, int D, int kWaves>
+// kWaves waves a workgroup, each with every kWaves-th tile.  A workgroup's up to
+// 16 rows share a key head: its query heads of one new token, or with kMany (starts
+// given) of several of a sequence.
+template <class T, int D, int kWaves, bool kMany>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void attention_decode_q4_kernel(
     AttnArgs a, int splits, int chunk, int groups, int sort_most) {
+    // (kMany: groups is not used, sort_most 0.)
     constexpr int VE = D / 16;
     __shared__ float o_join[kWaves][16][D + 4];
     __shared__ float m_join[kWaves][16], l_join[kWaves][16];
     __shared__ uint32_t bad_join[kWaves];        // a bit for each row that is not finite
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    int split, b, unit;                  // unit: key head and group of 16 query heads
-    if (sort_most) {
-        // Longest sequences first, with all their heads (not split: see launch).
-        const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x, rank = id / gridDim.y;
-        unit = (int)(id - rank * gridDim.y);
-        split = 0;
-        b = __builtin_amdgcn_readfirstlane(longest_first(a.kv, (int)rank, sort_most));
+    // Row r of the block: head skip + r - past * share of the key head's, `past`
+    // tokens behind row `token0`, by a product with the reciprocal (exact: attention_prefill.hip).
+    int split, b, kvh, token0, skip, rows, p_first;
+    const int share = a.q_heads / a.kv_heads;
+    const float per_share = 1.0f / (float)share;
+    auto past_of = [&](int r) { return kMany ? (int)(((float)(skip + r) + 0.5f) * per_share) : 0; };
+    if constexpr (kMany) {
+        const int slot = blockIdx.x / splits;
+        split = blockIdx.x - slot * splits;
+        kvh = blockIdx.y;
+        Slot x;
+        if (!find_slot(a, share, 4, slot, x)) return;
+        b = x.b;
+        const uint32_t r0 = (uint32_t)(x.tile * 16), past = r0 / (uint32_t)share;
+        rows = (int)min((int64_t)16, (int64_t)x.count * share - r0);
+        token0 = x.row_first + (int)past;
+        skip = (int)(r0 - past * share);
+        p_first = max(x.len - (x.to_row - x.row_first), -a.tokens) + (int)past;
     } else {
-        split = blockIdx.x % splits;
-        b = blockIdx.x / splits;
-        unit = blockIdx.y;
+        int unit;                        // key head and group of 16 query heads
+        if (sort_most) {
+            // Longest sequences first, with all their heads (not split: see launch).
+            const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x, rank = id / gridDim.y;
+            unit = (int)(id - rank * gridDim.y);
+            split = 0;
+            b = __builtin_amdgcn_readfirstlane(longest_first(a.kv, (int)rank, sort_most));
+        } else {
+            split = blockIdx.x % splits;
+            b = blockIdx.x / splits;
+            unit = blockIdx.y;
+        }
+        kvh = unit / groups;
+        token0 = b;
+        skip = (unit - kvh * groups) * 16;
+        rows = min(16, share - skip);
+        p_first = seq_len(a.kv, b) - 1;
     }
-    const int kvh = unit / groups, share = a.q_heads / a.kv_heads;
-    const int h0 = kvh * share + (unit - kvh * groups) * 16;                   // this workgroup's query heads
-    const int heads = min(16, (kvh + 1) * share - h0);
+    auto token_of = [&](int r) { return token0 + past_of(r); };
+    auto head_of = [&](int r) { return kvh * share + skip + r - past_of(r) * share; };
+    auto row_of = [&](int r) { return (int64_t)token_of(r) * a.q_heads + head_of(r); };
 
-    const Span span = key_span(a, seq_len(a.kv, b) - 1);
+    // What the first row's position up to the last's see, what this lane's
+    // sees, and what all of them see.
+    const int p_last = p_first + __builtin_amdgcn_readfirstlane(past_of(rows - 1));
+    Span span = key_span(a, p_last), mine = span, both = span;
+    if constexpr (kMany) {
+        const Span of_first = key_span(a, p_first);
+        span.start = of_first.start;
+        both.end = of_first.end;
+        mine = key_span(a, c < rows ? p_first + past_of(c) : -1);
+    }
     const int tiles = span.tiles(kTile);
     // At least `chunk` tiles a workgroup, more where the length passes what was planned for.
     const int per = max(chunk, (tiles + splits - 1) / splits);
     const int active = max(1, (tiles + per - 1) / per);
-    const int64_t row0 = (int64_t)b * a.q_heads + h0;
     const Partials parts(a, D, splits);
     if (split >= active) {
-        if ((int)threadIdx.x < heads) parts.mark(row0 + threadIdx.x, split, -INFINITY, 0.0f);
+        if ((int)threadIdx.x < rows) parts.mark(row_of(threadIdx.x), split, -INFINITY, 0.0f);
         return;
     }
     const int first = split * per, last = min(tiles, first + per);
@@ -145,7 +181,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void attention_decod
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
         qf[i] = u4{0, 0, 0, 0};
-        if (c < heads) qf[i] = *reinterpret_cast<const u4*>(a.q + b * a.sq + (int64_t)(h0 + c) * D + D / 4 * g + 8 * i);
+        if (c < rows) qf[i] = *reinterpret_cast<const u4*>(a.q + token_of(c) * a.sq + (int64_t)head_of(c) * D + D / 4 * g + 8 * i);
     }
     // Scores are compared before they are scaled, so the scale's sign goes into the queries (exact).
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, keep = a.scale == 0.0f ? 0u : ~0u;
@@ -171,15 +207,17 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void attention_decod
                 s[t] = T::mfma16(q4_values<T>(x.k[t][i], KeyGroups<D>::in_last(g, i) ? last_scale : first_scale), qf[i], s[t]);
         }
         // A tile whose every key is seen and owned needs no mask (the same answer in all lanes).
-        if (!(span.all_seen(x.at.base, kTile) && x.at.page[0] >= 0 && x.at.page[1] >= 0)) {
+        if (!(both.all_seen(x.at.base, kTile) && x.at.page[0] >= 0 && x.at.page[1] >= 0)) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const bool seen = x.at.page[t] >= 0 && span.seen(x.at.base + 16 * t + 4 * g + i);
-                    if (!seen) {
-                        s[t][i] = -INFINITY;
+                    const int key = x.at.base + 16 * t + 4 * g + i;
+                    const bool any = x.at.page[t] >= 0 && span.seen(key);
+                    if (!(kMany ? any && mine.seen(key) : any)) s[t][i] = -INFINITY;
+                    if (!any) {
                         // What lies there must not reach 0 * v: codes of 0, and no scale that makes NaN of them.
+                        // (What only other rows see may make a row NaN; it is computed again below.)
 #pragma unroll
                         for (int e = 0; e < Tile<D>::kV; ++e) x.v[t][i][e] = 0;
                         x.vs[t][0] &= ~(0xFFu << 8 * i);
@@ -284,7 +322,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void attention_decod
         m_join[wave][c] = m;
         l_join[wave][c] = l;
     }
-    if (c < heads) {
+    if (c < rows) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -293,14 +331,14 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void attention_decod
     f4 probe = f4{0, 0, 0, 0};
 #pragma unroll
     for (int e = 0; e < VE; ++e) probe += o[e] * 0.0f;
-    const uint64_t odd = __ballot(c < heads && !(probe[0] + probe[1] + probe[2] + probe[3] == 0.0f));
+    const uint64_t odd = __ballot(c < rows && !(probe[0] + probe[1] + probe[2] + probe[3] == 0.0f));
     if (lane == 0) bad_join[wave] = (uint32_t)(odd | odd >> 16 | odd >> 32 | odd >> 48) & 0xFFFFu;
     __syncthreads();
     uint32_t bad = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) bad |= bad_join[w];
     bad = __builtin_amdgcn_readfirstlane(bad);
-    for (int at = threadIdx.x; at < heads * (D / 4); at += 64 * kWaves) {
+    for (int at = threadIdx.x; at < rows * (D / 4); at += 64 * kWaves) {
         const int r = at / (D / 4), d = (at - r * (D / 4)) * 4;
         if (bad >> r & 1) continue;
         float top = m_join[0][r];
@@ -316,20 +354,22 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void attention_decod
             acc += *reinterpret_cast<const f4*>(&o_join[w][r][d]) * f;
         }
         if (active == 1) {
-            store_row4<T>(a, b, h0 + r, D, d, acc, top, sum);
-            if (splits > 1 && d == 0) parts.mark(row0 + r, 0, top, kWhole);
+            store_row4<T>(a, token_of(r), head_of(r), D, d, acc, top, sum);
+            if (splits > 1 && d == 0) parts.mark(row_of(r), 0, top, kWhole);
         } else {
-            parts.put4(row0 + r, split, d, acc);
-            if (d == 0) parts.mark(row0 + r, split, top, sum);
+            parts.put4(row_of(r), split, d, acc);
+            if (d == 0) parts.mark(row_of(r), split, top, sum);
         }
     }
-    for (int r = wave; r < heads; r += kWaves) {
+    for (int r = wave; r < rows; r += kWaves) {
         if (!(bad >> r & 1)) continue;
+        const int token = token_of(r), head = head_of(r);
         float x[4], top, sum;
-        plain_row<D, kTile, Q4Rows<D>>(a, span, first, last, span, a.kv.table + (int64_t)b * a.kv.width, kvh,
-                                       a.q + b * a.sq + (int64_t)(h0 + r) * D, x, top, sum);
-        store_plain_row<T, D>(a, parts, active > 1, b, h0 + r, split, x, top, sum);
-        if (active == 1 && splits > 1 && lane == 0) parts.mark(row0 + r, 0, top, kWhole);
+        plain_row<D, kTile, Q4Rows<D>>(a, span, first, last, kMany ? key_span(a, p_first + past_of(r)) : span,
+                                       a.kv.table + (int64_t)b * a.kv.width, kvh, a.q + token * a.sq + (int64_t)head * D, x,
+                                       top, sum);
+        store_plain_row<T, D>(a, parts, active > 1, token, head, split, x, top, sum);
+        if (active == 1 && splits > 1 && lane == 0) parts.mark(row_of(r), 0, top, kWhole);
     }
 }
 
@@ -350,58 +390,94 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void attention_decod
 // and two a CU (four of 8000: 17.1 with 1024 of 4 waves, 16.3 with 512 of 8).
 constexpr int kCus = 256, kSplitFrom = 10, kSplits = 32, kSortFrom = 512;
 
-template <class T, int D, int kWaves>
-hipError_t launch_waves(const AttnArgs& a, int splits, int tiles, int64_t most, hipStream_t stream) {
-    const int share = a.q_heads / a.kv_heads, groups = (share + 15) / 16;
-    const int64_t units = (int64_t)a.tokens * a.kv_heads * groups;
-    const int chunk = max(kWaves, (tiles + splits - 1) / splits);
-    dim3 grid((unsigned)(a.tokens * splits), (unsigned)(a.kv_heads * groups));
+// Prompts (and chunks, and tokens to be verified) of up to kFewRows rows a key head on
+// average go in blocks of 16 rows through this kernel, which reads the keys once for each block, longer
+// ones through attention_prefill.hip with its blocks of 128 (2 tokens of 64 sequences
+// of 2000, 32 heads on 8: 37 us here, 92 there; 4 of 32 of 4000, 32 heads:
+// 114 and 195; 48 of 8 of 4096, 32 heads: 80 and 121; one of 24576, 32 heads
+// on 8: 12 tokens, 48 rows, 27.3 and 30.7, 32 tokens, 128 rows, 40.4 and 41.2; 16 of 8 of 4096, 64 rows: 48.1 and 46.0).
+constexpr int kFewRows = 48;
+
+struct Plan {
+    int64_t units;                   // key heads of blocks of rows, about
+    int64_t most;                    // longest run of keys
+    int tiles, waves, splits;
+};
+
+// Waves a CU holds, and a workgroup at most.
+constexpr int most_waves(int head_dim) { return head_dim == 256 ? 8 : 16; }
+
+Plan plan_of(const AttnArgs& a, int64_t units) {
+    Plan x;
+    const int kMost = most_waves(a.head_dim);
+    x.units = units;
+    x.most = a.max_len;
+    if (a.window && (int64_t)a.window + a.sinks < x.most) x.most = (int64_t)a.window + a.sinks;
+    x.tiles = (int)((x.most + kTile - 1) / kTile);
+    x.splits = 1;
+    const int64_t budget = kCus * kMost / units;             // waves of a unit that run at once
+    if (x.tiles * (kCus - units) <= kSplitFrom * 4 * kCus) {
+        const int few = units > kCus ? 4 : 2, wanted = (x.tiles + 3) / 4;
+        x.waves = wanted <= few || budget < 8 ? 4 : wanted <= 8 || budget < 16 ? 8 : 16;
+        x.waves = min(x.waves, kMost);
+        return x;
+    }
+    const int64_t waves = min(budget, (int64_t)x.tiles), limit = kAttnSplitRows / ((int64_t)a.tokens * a.q_heads);
+    for (x.waves = 4;; x.waves *= 2) {
+        x.splits = (int)max((int64_t)1, min(waves / x.waves, limit));
+        if (x.waves == kMost || (x.splits <= kSplits && units * x.splits <= 2 * kCus)) return x;
+    }
+}
+
+template <class T, int D, int kWaves, bool kMany>
+hipError_t launch_waves(const AttnArgs& a, const Plan& plan, hipStream_t stream) {
+    const int share = a.q_heads / a.kv_heads, groups = (share + 15) / 16, splits = plan.splits;
+    const int chunk = max(kWaves, (plan.tiles + splits - 1) / splits);
+    // kMany: slots (find_slot), at most 4 a sequence: a grid of one split stays below 2^32 threads.
+    const int64_t blocks = kMany ? (int64_t)a.tokens * share / 16 + a.kv.seqs : a.tokens;
+    const dim3 grid((unsigned)(blocks * splits), (unsigned)(kMany ? a.kv_heads : a.kv_heads * groups));
     // More than a round of workgroups: longest first (attention_decode.hip; 64 sequences of 1 to 4096
     // keys, 32 heads: 105 us, 142 in their order).
-    const int sort_most = kWaves == 4 && splits == 1 && units > 2 * kCus && most >= kSortFrom ? (int)most : 0;
-    hipLaunchKernelGGL((attention_decode_q4_kernel<T, D, kWaves>), grid, dim3(64 * kWaves), 0, stream, a, splits, chunk,
-                       groups, sort_most);
+    const int sort_most = !kMany && kWaves == 4 && splits == 1 && plan.units > 2 * kCus && plan.most >= kSortFrom ? (int)plan.most : 0;
+    hipLaunchKernelGGL((attention_decode_q4_kernel<T, D, kWaves, kMany>), grid, dim3(64 * kWaves), 0, stream, a, splits,
+                       chunk, groups, sort_most);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || splits == 1 ? e : launch_attention_join(a, splits, stream);
 }
 
-template <class T, int D>
-hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-    constexpr int kMost = D == 256 ? 8 : 16;                 // waves a CU holds, and a workgroup at most
-    const int share = a.q_heads / a.kv_heads, groups = (share + 15) / 16;
-    int64_t most = (int64_t)a.max_len;
-    if (a.window && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;
-    const int tiles = (int)((most + kTile - 1) / kTile);
-    const int64_t units = (int64_t)a.tokens * a.kv_heads * groups;
-    const int64_t budget = kCus * kMost / units;             // waves of a key head that run at once
-    if (tiles * (kCus - units) <= kSplitFrom * 4 * kCus) {
-        const int few = units > kCus ? 4 : 2, wanted = (tiles + 3) / 4;
-        if (wanted <= few || budget < 8) return launch_waves<T, D, 4>(a, 1, tiles, most, stream);
-        if (wanted <= 8 || budget < 16 || kMost == 8) return launch_waves<T, D, 8>(a, 1, tiles, most, stream);
-        return launch_waves<T, D, kMost>(a, 1, tiles, most, stream);
-    }
-    const int64_t waves = min(budget, (int64_t)tiles), limit = kAttnSplitRows / ((int64_t)a.tokens * a.q_heads);
-    auto splits = [&](int w) { return max((int64_t)1, min(waves / w, limit)); };
-    auto few = [&](int w) { return splits(w) <= kSplits && units * splits(w) <= 2 * kCus; };
-    if (few(4)) return launch_waves<T, D, 4>(a, (int)splits(4), tiles, most, stream);
-    if (kMost == 16 && few(8)) return launch_waves<T, D, 8>(a, (int)splits(8), tiles, most, stream);
-    return launch_waves<T, D, kMost>(a, (int)splits(kMost), tiles, most, stream);
+template <class T, int D, bool kMany>
+hipError_t launch(const AttnArgs& a, const Plan& plan, hipStream_t stream) {
+    if (plan.waves == 4) return launch_waves<T, D, 4, kMany>(a, plan, stream);
+    if constexpr (most_waves(D) == 16)
+        if (plan.waves == 16) return launch_waves<T, D, 16, kMany>(a, plan, stream);
+    return launch_waves<T, D, 8, kMany>(a, plan, stream);
 }
 
-template <class T>
-hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
+template <class T, bool kMany>
+hipError_t launch_dim(const AttnArgs& a, const Plan& plan, hipStream_t stream) {
     switch (a.head_dim) {
-        case 64: return launch<T, 64>(a, stream);
-        case 96: return launch<T, 96>(a, stream);
-        case 128: return launch<T, 128>(a, stream);
-        default: return launch<T, 256>(a, stream);
+        case 64: return launch<T, 64, kMany>(a, plan, stream);
+        case 96: return launch<T, 96, kMany>(a, plan, stream);
+        case 128: return launch<T, 128, kMany>(a, plan, stream);
+        default: return launch<T, 256, kMany>(a, plan, stream);
     }
 }
 
 }  // namespace
 
 hipError_t launch_attention_decode_q4(const AttnArgs& a, hipStream_t stream) {
-    return a.dtype == 0 ? launch_dim<Fp16>(a, stream) : launch_dim<Bf16>(a, stream);
+    const Plan plan = plan_of(a, (int64_t)a.tokens * a.kv_heads * ((a.q_heads / a.kv_heads + 15) / 16));
+    return a.dtype == 0 ? launch_dim<Fp16, false>(a, plan, stream) : launch_dim<Bf16, false>(a, plan, stream);
+}
+
+bool few_rows_q4(const AttnArgs& a) {
+    return (int64_t)a.tokens * (a.q_heads / a.kv_heads) <= (int64_t)kFewRows * a.kv.seqs;
+}
+
+hipError_t launch_attention_few_q4(const AttnArgs& a, hipStream_t stream) {
+    const int64_t rows = (int64_t)a.tokens * (a.q_heads / a.kv_heads), blocks = (rows + 16 * a.kv.seqs - 1) / (16 * a.kv.seqs);
+    const Plan plan = plan_of(a, a.kv.seqs * blocks * a.kv_heads);
+    return a.dtype == 0 ? launch_dim<Fp16, true>(a, plan, stream) : launch_dim<Bf16, true>(a, plan, stream);
 }
 
 }  // namespace slim

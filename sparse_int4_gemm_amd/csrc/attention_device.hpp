@@ -116,6 +116,45 @@ __device__ __forceinline__ Span key_span(const AttnArgs& a, int p) {
     return s;
 }
 
+// New rows of a key head, (token, its query heads) one behind the other, go in
+// blocks of 2^log of one sequence each.  Sequence b's slots begin at starts[b] * share / 2^log + b (of
+// its start among the rows there are, [0, tokens]): at least as many as its rows fill.
+struct Slot {
+    int b, len;                       // sequence, its length
+    int from_row, to_row;             // its starts
+    int row_first, count;             // its rows among those there are
+    int64_t tile;                     // block of it; may be past its rows
+};
+
+// What slot `slot` holds (the same in all lanes), or false: nothing.  Found as
+// find_seq finds a token's sequence; the last step has its starts and length in the lanes already.
+__device__ __forceinline__ bool find_slot(const AttnArgs& a, int share, int log, int slot, Slot& x) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = a.kv.seqs, found, starts, ends, lens;
+    do {
+        const int step = (n + 63) >> 6, i = lo + min(lane * step, n - 1);
+        starts = a.kv.starts[i];
+        ends = a.kv.starts[i + 1];
+        lens = a.kv.lens[i];
+        const int row = min(max(starts, 0), a.tokens);
+        const uint64_t ok = __ballot(lane * step < n && (((int64_t)row * share) >> log) + i <= slot);
+        if (ok == 0) return false;
+        found = 63 - __builtin_clzll(ok);
+        lo += found * step;
+        n = min(step, n - found * step);
+    } while (n > 1);
+    // Of one value for all lanes from here on, in variables that never held
+    // another: else every branch and loop that follows would run under a lane mask.
+    x.from_row = __builtin_amdgcn_readlane(starts, found);
+    x.to_row = __builtin_amdgcn_readlane(ends, found);
+    x.len = min(max(__builtin_amdgcn_readlane(lens, found), 0), kMaxLen);
+    x.b = __builtin_amdgcn_readfirstlane(lo);
+    x.row_first = min(max(x.from_row, 0), a.tokens);
+    x.count = max(min(x.to_row, a.tokens) - x.row_first, 0);
+    x.tile = slot - ((((int64_t)x.row_first * share) >> log) + x.b);
+    return x.tile >= 0 && (x.tile << log) < (int64_t)x.count * share;
+}
+
 __device__ __forceinline__ float half_value(const AttnArgs& a, uint16_t x) {
     return a.dtype == 0 ? (float)__builtin_bit_cast(_Float16, x) : __builtin_bit_cast(float, (uint32_t)x << 16);
 }

@@ -111,31 +111,10 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     }
     const int slot = grid.slots - 1 - order;
 
-    // Sequence b's slots begin at starts[b] * share / kRows + b (of its start
-    // among the rows there are, [0, tokens]): at least as many as its rows fill.
-    // Found as find_seq finds a token's sequence; the last step has its starts
-    // and length in the lanes already.
-    int lo = 0, n = a.kv.seqs, found, starts, ends, lens;
-    do {
-        const int step = (n + 63) >> 6, i = lo + min(lane * step, n - 1);
-        starts = a.kv.starts[i];
-        ends = a.kv.starts[i + 1];
-        lens = a.kv.lens[i];
-        const int row = min(max(starts, 0), a.tokens);
-        const uint64_t ok = __ballot(lane * step < n && (((int64_t)row * share) >> kRowsLog) + i <= slot);
-        if (ok == 0) return;
-        found = 63 - __builtin_clzll(ok);
-        lo += found * step;
-        n = min(step, n - found * step);
-    } while (n > 1);
-    // Of one value for all lanes from here on, in variables that never held
-    // another: else every branch and loop below would run under a lane mask.
-    const int from_row = __builtin_amdgcn_readlane(starts, found), to_row = __builtin_amdgcn_readlane(ends, found);
-    const int len = min(max(__builtin_amdgcn_readlane(lens, found), 0), kMaxLen);
-    const int b = __builtin_amdgcn_readfirstlane(lo);
-    const int row_first = min(max(from_row, 0), a.tokens), count = max(min(to_row, a.tokens) - row_first, 0);
-    const int64_t tile = slot - ((((int64_t)row_first * share) >> kRowsLog) + b);
-    if (tile < 0 || tile * kRows >= (int64_t)count * share) return;
+    Slot at_slot;
+    if (!find_slot(a, share, kRowsLog, slot, at_slot)) return;
+    const int b = at_slot.b, len = at_slot.len, row_first = at_slot.row_first, count = at_slot.count;
+    const int64_t tile = at_slot.tile;
 
     // Row r of the block is token (skip + r) / share past `token0`: 32-bit
     // divisions, of small numbers by a product with the reciprocal (exact:
@@ -148,7 +127,7 @@ __global__ __launch_bounds__(64 * kRowWaves * KG, D == 256 ? 1 : D == 64 && KG =
     auto token_of = [&](int r) { return (int)(((float)(skip + r) + 0.5f) * per_share); };
     // Position of the first of them; new tokens before or behind the rows there are
     // count too (held at where all positions are negative: nothing below overflows).
-    const int before = max(len - (to_row - row_first), -a.tokens);
+    const int before = max(len - (at_slot.to_row - row_first), -a.tokens);
     const int p_first = before + token0;
     const int p_last = p_first + __builtin_amdgcn_readfirstlane(token_of(rows - 1));
     Span span = key_span(a, p_last);
@@ -748,6 +727,7 @@ hipError_t launch_attention_prefill(const AttnArgs& a, hipStream_t stream) {
 
 hipError_t launch_attention_prefill_q4(const AttnArgs& a, hipStream_t stream) {
     if (!a.kv.starts) return launch_attention_decode_q4(a, stream);
+    if (few_rows_q4(a)) return launch_attention_few_q4(a, stream);
     return a.dtype == 0 ? launch_dim<Fp16, true>(a, stream) : launch_dim<Bf16, true>(a, stream);
 }
 
