@@ -71,5 +71,10 @@ class Rope:
         self.magnitude = 1.0 if magnitude is None else float(magnitude)
         if not math.isfinite(self.magnitude):
             raise ValueError("magnitude must be finite")
-        self.freqs = freqs.to(device).contiguous()
-        self.params = _lib.Rotation(ctypes.c_void_p(self.freqs.data_ptr()), rot_dim, int(self.interleaved), self.magnitude)
+        self._freqs = freqs.to(device, copy=True).contiguous()
+        self.params = _lib.Rotation(ctypes.c_void_p(self._freqs.data_ptr()), rot_dim, int(self.interleaved), self.magnitude)
+
+    @property
+    def freqs(self) -> torch.Tensor:
+        """The frequencies on the GPU (not to be replaced: calls hold their address)."""
+        return self._freqs
