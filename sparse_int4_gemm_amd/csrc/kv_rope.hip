@@ -9,7 +9,7 @@
 // token cut over several only costs each of them the chain again.  Bound by HBM
 // for prompts (halves: 4 bytes an element; 4 bits: 2.5), by launch and that chain for
 // single tokens.  Of 32 heads of 128, with their queries: 64 tokens 3.4 us into halves
-// and 4.6 into 4 bits, 8192 tokens 80 us (5.0 TB/s) and 65 (4.6 TB/s).
+// and 4.6 into 4 bits, 8192 tokens 79 us (5.1 TB/s) and 62 (4.9 TB/s).
 #include "kv_q4.hpp"
 #include "rope_device.hpp"
 
@@ -41,11 +41,19 @@ __device__ __forceinline__ Target target_of(const PagedKV& kv, int t) {
 }
 
 // The token and slice of this wave, tokens from token0 on; token >= tokens: none.
+// kRuns: an XCD (a workgroup's is its index mod 8) takes runs of 32 workgroups, where
+// there are eight such runs left.  Pages of 4 bits need it, as 16 tokens share 16
+// bytes of scales, and two a line of codes, that each XCD's L2 would read and write for
+// itself (8763 tokens of 32 heads appended and read back: 126 MB written and 70 read
+// without, 111 and 40 with, 106 -> 100 us; runs of 8: 102, of 128: 111; pages of halves, 8192 tokens: 78 and 80).
 struct Task {
     int token, slice;
 };
+template <bool kRuns>
 __device__ __forceinline__ Task task_of(int token0, int slices) {
-    const uint32_t task = blockIdx.x * kRopeWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    uint32_t block = blockIdx.x;
+    if (kRuns && (block | 255) < gridDim.x) block = (block & ~255u) | (block & 7) * 32 | (block >> 3 & 31);
+    const uint32_t task = block * kRopeWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t token = task / (uint32_t)slices;
     return {token0 + (int)token, (int)(task - token * (uint32_t)slices)};
 }
@@ -59,7 +67,7 @@ template <class T, int C, int N>
 __global__ __launch_bounds__(64 * kRopeWaves) void kv_append_rope_kernel(AppendRopeArgs a, int token0, int units,
                                                                          int v_units, int slices) {
     __shared__ float2 lds[kRopeWaves][kMaxHalf];
-    const Task task = task_of(token0, slices);
+    const Task task = task_of<false>(token0, slices);
     const int t = task.token;
     if (t >= a.to.tokens) return;
     const int lane = threadIdx.x & 63, D = a.to.head_dim;
@@ -156,7 +164,7 @@ template <class T, int C, int D, int N>
 __global__ __launch_bounds__(64 * kRopeWaves) void kv_append_q4_kernel(AppendRopeArgs a, int token0, Divisor units,
                                                                        int q_batches, int kv_batches, int per, int slices) {
     __shared__ double2 lds[kRopeWaves][kMaxHalf];
-    const Task task = task_of(token0, slices);
+    const Task task = task_of<true>(token0, slices);
     const int t = task.token;
     if (t >= a.to.tokens) return;
     constexpr int kChunks = D / 8, kHeads = 64 / kChunks;           // of a head; heads of the wave's lanes
@@ -276,14 +284,14 @@ __global__ __launch_bounds__(64 * kRopeWaves) void kv_append_q4_kernel(AppendRop
 }
 
 // Rows of 4-bit pages as halves again.  Bound by HBM: 8192 tokens of 32 heads of
-// 128, 134 MB written and 36 read, 30 us (5.7 TB/s).  The stores pass the caches by: with
+// 128, 134 MB written and 36 read, 27 us (6.3 TB/s).  The stores pass the caches by: with
 // those that fill them 8763 tokens took 39 us instead of 30 (and what reads the rows next comes from elsewhere: a copy of the
 // cache, not the attention).  The appends' stores stay in the caches: past them
 // the same 8763 tokens' append alone takes 42.5 us instead of 45.8, with the
 // attention that follows 205.5 instead of 199.7.
 template <class T, int N>
 __global__ __launch_bounds__(64 * kRopeWaves) void kv_read_q4_kernel(AppendArgs a, int token0, int slices) {
-    const Task task = task_of(token0, slices);
+    const Task task = task_of<true>(token0, slices);
     const int t = task.token;
     if (t >= a.tokens) return;
     const int lane = threadIdx.x & 63, D = a.head_dim, chunks = D / 8, half_all = a.kv_heads * chunks;
@@ -379,6 +387,7 @@ hipError_t read_q4(const AppendArgs& a, int all, hipStream_t stream) {
 // round of waves) 10.0 us with a batch of two and 11.0 with five of four, 1024
 // 15.4 and 14.0, 4096 46.3 and 34.6.  Reading back: 256 tokens 4.0 us with one and
 // 4.3 with eight, 512 5.5 and 4.5, 4096 24.1 and 16.6 (four: 18.9, sixteen: 16.9).
+// (4 bits all without runs, see Task.)
 template <class T, int C>
 hipError_t append_rope_n(const AppendRopeArgs& a, hipStream_t stream) {
     const Rotation none = {nullptr, 0, 0, 1.0};
