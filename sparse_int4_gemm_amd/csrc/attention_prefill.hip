@@ -37,6 +37,16 @@
 // bf16: 391 to 403 us on different cards, 1.02 to 1.05 PFLOP/s (a library
 // product of 8192^3: 1.40 to 1.45); 719 thousand cycles, so 1.8 GHz over the call,
 // of which the matrix unit is busy for 57% and the vector unit for 55%.
+//
+// slim_attention_prefill_q4 is the same kernel over pages of 4 bits (Q4): a
+// tile's codes pass through registers, requested a step ahead, are turned into halves by
+// one instruction for two, and are written to the places in LDS that the loads
+// of halves fill.  A quarter of the bytes, and some 80 vector instructions and
+// 32 LDS writes for each of 4 waves and tile more, which two workgroups a CU mostly
+// hide: 8192 windowed tokens 392 to 409 us, four prompts of up to 4096 365 to 377 where
+// the 16-bit cache takes 367 to 382; not so one wave a SIMD (head size 256: 79 and 66 us) or
+// short prompts (2048 tokens of 32 heads: 53 and 49).  LDS writes of 16 rows' chunks take 16 cycles,
+// 13 with rows taken in another order (no bank met twice), which changed no case's time.
 #include "kv_q4.hpp"
 
 namespace slim {
@@ -697,6 +707,8 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
 // is then alone on its CU for most of its time (1100 tokens of 32 heads on 8
 // 26.1 us in one group, 23.7 in two; 1536 33.3 and 30.8; 1900 44.2 and 41.3; 1280 behind 320 34.3
 // and 33.1; head size 64, 1900 tokens 33.6 and 28.6), up to nearly two rounds (2048 tokens 48.6 and 50.2).
+// The same with 4 bits (61 on 24576 55.2 in one group, 49.1 in two; 1100 tokens 32.6 and 29.1; 1536
+// behind 800 59.5 and 62.3; four prompts of 2000 167 and 197; 8192 windowed 409 and 457).
 template <class T, int D, bool Q4>
 hipError_t launch_groups(const AttnArgs& a, hipStream_t stream) {
     const int64_t rows = (int64_t)a.tokens * (a.q_heads / a.kv_heads);
