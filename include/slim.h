@@ -551,7 +551,9 @@ slim_status slim_kv_append_rope(const uint16_t* Q, int64_t stride_Q, uint16_t* Q
  * slim_attention_decode_q4, slim_attention_prefill_q4
  *                     slim_attention_decode and slim_attention_prefill over
  *                     such pools, on the values the codes stand for; dtype is that of
- *                     Q, O and the append.  Workspace: slim_attention_workspace_bytes
+ *                     Q, O and the append.  Workspace: slim_attention_workspace_bytes.
+ *                     The numbers of rows and sequences plan the work too, rows of no
+ *                     sequence among them, and may change results in their last bits
  */
 size_t slim_q4_page_bytes(int64_t kv_heads, int64_t page_size, int64_t head_dim);
 slim_status slim_kv_append_q4(const uint16_t* Q, int64_t stride_Q, uint16_t* Qout, int64_t stride_Qout,

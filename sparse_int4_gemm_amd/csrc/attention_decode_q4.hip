@@ -401,12 +401,12 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void attention_decod
 constexpr int kCus = 256, kSplitFrom = 10, kSplits = 32, kSortFrom = 512;
 
 // Prompts (and chunks, and tokens to be verified) of up to kFewRows rows a key head on
-// average go in blocks of 16 rows through this kernel, which reads the keys once for each block, longer
+// average, two blocks, go in blocks of 16 rows through this kernel, which reads the keys once for each block, longer
 // ones through attention_prefill.hip with its blocks of 128 (2 tokens of 64 sequences
 // of 2000, 32 heads on 8: 37 us here, 92 there; 4 of 32 of 4000, 32 heads:
-// 114 and 195; 48 of 8 of 4096, 32 heads: 80 and 121; one of 24576, 32 heads
-// on 8: 12 tokens, 48 rows, 27.3 and 30.7, 32 tokens, 128 rows, 40.4 and 41.2; 16 of 8 of 4096, 64 rows: 48.1 and 46.0).
-constexpr int kFewRows = 48;
+// 114 and 195; 32 of 32 of 4000, 32 rows: 179 and 192; one of 24576, 32 heads on 8: 8 tokens, 32 rows, 23.7 and
+// 27.6, 32 tokens, 128 rows, 40.4 and 41.2; 16 of 8 of 4096, 64 rows: 48.1 and 46.0).
+constexpr int kFewRows = 32;
 
 struct Plan {
     int64_t units;                   // key heads of blocks of rows, about

@@ -142,9 +142,28 @@ def test_few_rows_scale_and_peaked_scores(env):
     check(c, run(env, c), what="scale 0: the mean of the values")
 
 
+@pytest.mark.parametrize("dtype,dim", [("fp16", 64), ("bf16", 128), ("bf16", 96), ("fp16", 256)])
+@pytest.mark.parametrize("q_heads,kv_heads,new", [(4, 2, [20, 1, 20, 9, 12]), (40, 1, [1, 0, 2, 0, 0]), (8, 8, [30, 1, 32, 40, 12])])
+def test_few_rows_windows_of_other_heads(env, dtype, dim, q_heads, kv_heads, new):
+    c = q4_case(env[0], 70, dtype, [300, 1, 500, 700, 12], q_heads, kv_heads, dim, 16, new=new)
+    for window, sinks in [(0, 0), *WINDOWS]:
+        y, lse = run(env, c, window, sinks, lse=True)
+        check(c, y, lse, window, sinks)
+
+
+@pytest.mark.parametrize("dtype,dim", [("fp16", 64), ("bf16", 96), ("bf16", 128), ("fp16", 256)])
+@pytest.mark.parametrize("q_heads,kv_heads,new", [(8, 1, 4), (32, 8, 7), (3, 3, 29)])
+def test_few_rows_of_one_sequence_split(env, dtype, dim, q_heads, kv_heads, new):
+    c = q4_case(env[0], 72, dtype, [5000], q_heads, kv_heads, dim, 64, new=[new])
+    y, lse = run(env, c, lse=True)
+    check(c, y, lse)
+    y, lse = run(env, c, 3000, 9, lse=True, max_len=200000)
+    check(c, y, lse, 3000, 9)
+
+
 # --------------------------------------------------------- the border, many rows
 @pytest.mark.parametrize("dtype,dim", [("fp16", 64), ("bf16", 128)])
-@pytest.mark.parametrize("new", [[96, 0], [97, 0], [48, 48], [47, 50], [1, 200], [90, 1, 1, 1, 200, 1, 1, 1]])
+@pytest.mark.parametrize("new", [[64, 0], [65, 0], [32, 32], [31, 34], [96, 0], [97, 0], [48, 48], [47, 50], [1, 200], [90, 1, 1, 1, 200, 1, 1, 1]])
 def test_around_the_border(env, dtype, dim, new):
     c = q4_case(env[0], 69, dtype, [n + 100 for n in new], 3, 3, dim, 32, new=new)
     y, lse = run(env, c, lse=True)
