@@ -17,13 +17,14 @@ def encode(x, dtype):
     lo, hi = RANGE[dtype]
     limits = 7.0 * 2.0 ** np.arange(lo, hi + 1, dtype=np.float64)
     e = lo + np.minimum(np.searchsorted(limits, np.abs(groups).max(-1), side="left"), hi - lo)
-    a = groups / 2.0 ** e[..., None].astype(np.float64)
-    # The nearest level; of two as near the one with the even code.
-    off = np.abs(np.abs(a)[..., None] - LEVELS)
-    near = off == off.min(-1, keepdims=True)
-    code = np.where(near & (np.arange(8) % 2 == 0), np.arange(8), 99).min(-1)
-    code = np.where(code == 99, near.argmax(-1), code)
-    code = (code | np.where(np.signbit(groups), 8, 0)).astype(np.uint8)
+    a = np.abs(groups) / 2.0 ** e[..., None].astype(np.float64)
+    # The nearest level: that of code k + 1 from the middle between it and k's
+    # on, the middle itself to the even code.
+    code = np.zeros(groups.shape, dtype=np.uint8)
+    for k in range(7):
+        middle = (LEVELS[k] + LEVELS[k + 1]) / 2
+        code += a >= middle if k % 2 else a > middle
+    code |= np.signbit(groups).astype(np.uint8) << 3
     code = np.where(finite[..., None], code, 0).astype(np.uint8)
     return code.reshape(x.shape), np.where(finite, e + 127, 255).astype(np.uint8)
 

@@ -133,6 +133,21 @@ def test_few_rows_far_starts(env, starts):
         assert ((np.abs(got[t] - want[0]) - bound(one, want[0], mass[0])) <= 0).all()
 
 
+@pytest.mark.parametrize("lens,new", [([5000], [4]), ([9000, 300], [3, 0]), ([40, 70], [2, 7])])
+def test_few_rows_among_rows_of_no_sequence(env, lens, new):
+    torch, slim = env
+    c = q4_case(torch, 73, "fp16", lens, 4, 2, 64, 16, new=new)
+    q = torch.cat([c["q"][:1], c["q"], c["q"][:2]])
+    out = torch.full_like(q, 77.0)
+    lse = torch.full(q.shape[:2], 77.0, device="cuda")
+    slim.attention_prefill_q4(q, c["k4"], c["v4"], c["d_table"], c["d_lens"], c["d_starts"] + 1, scale=c["scale"], out=out, lse=lse)
+    torch.cuda.synchronize()
+    n = sum(new)
+    check(c, out[1:n + 1], lse[1:n + 1])
+    for x in (out, lse):
+        assert (x[:1] == 77).all() and (x[n + 1:] == 77).all()
+
+
 def test_few_rows_scale_and_peaked_scores(env):
     c = q4_case(env[0], 68, "fp16", [700, 64, 9], 4, 2, 128, 16, new=[9, 2, 9], q_std=3.0)
     check(c, run(env, c))
