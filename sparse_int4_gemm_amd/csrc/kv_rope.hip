@@ -40,7 +40,7 @@ __device__ __forceinline__ Target target_of(const PagedKV& kv, int t) {
     return x;
 }
 
-// The token and slice of this wave, tokens from token0 on; token >= tokens: none.
+// The token and slice of this wave, tokens from token0 on; token >= tokens (the call's, or its part's end): none.
 // kRuns: an XCD (a workgroup's is its index mod 8) takes runs of 32 workgroups, where
 // there are eight such runs left.  Pages of 4 bits need it, as 16 tokens share 16
 // bytes of scales, and two a line of codes, that each XCD's L2 would read and write for
@@ -324,13 +324,18 @@ __global__ __launch_bounds__(64 * kRopeWaves) void kv_read_q4_kernel(AppendArgs 
     }
 }
 
-// Calls launch(first token, grid) for as many tokens at a time as a grid's 2^32 threads hold.
-template <class Launch>
-hipError_t in_parts(int64_t tokens, int slices, Launch&& launch) {
-    const int64_t at_once = (int64_t(1) << 25) / slices;
+// Calls launch(arguments, first token, grid) for as many tokens at a time as a grid's
+// 2^32 threads hold; the arguments' `tokens` ends at the part's last one, so that what
+// a part's last workgroup has over does nothing.
+AppendArgs& of_tokens(AppendArgs& a) { return a; }
+AppendArgs& of_tokens(AppendRopeArgs& a) { return a.to; }
+template <class Args, class Launch>
+hipError_t in_parts(Args a, int slices, Launch&& launch) {
+    const int64_t at_once = (int64_t(1) << 25) / slices, tokens = of_tokens(a).tokens;
     for (int64_t t = 0; t < tokens; t += at_once) {
-        const int64_t waves = min(at_once, tokens - t) * slices;
-        launch((int)t, dim3((unsigned)((waves + kRopeWaves - 1) / kRopeWaves)));
+        const int64_t end = min(t + at_once, tokens);
+        of_tokens(a).tokens = (int32_t)end;
+        launch(a, (int)t, dim3((unsigned)(((end - t) * slices + kRopeWaves - 1) / kRopeWaves)));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -342,8 +347,8 @@ const dim3 kBlock(64 * kRopeWaves);
 template <class T, int C, int N>
 hipError_t append_rope(const AppendRopeArgs& a, int units, int v_units, int all, hipStream_t stream) {
     const int slices = (all + 64 * N - 1) / (64 * N);
-    return in_parts(a.to.tokens, slices, [&](int t, dim3 grid) {
-        hipLaunchKernelGGL((kv_append_rope_kernel<T, C, N>), grid, kBlock, 0, stream, a, t, units, v_units, slices);
+    return in_parts(a, slices, [&](const AppendRopeArgs& part, int t, dim3 grid) {
+        hipLaunchKernelGGL((kv_append_rope_kernel<T, C, N>), grid, kBlock, 0, stream, part, t, units, v_units, slices);
     });
 }
 
@@ -366,8 +371,8 @@ hipError_t append_q4(const AppendRopeArgs& a, int per, hipStream_t stream) {
     const Batches<C, D, N> n(a);
     const int slices = (n.all() + per - 1) / per;
     per = (n.all() + slices - 1) / slices;                              // as even as they come
-    return in_parts(a.to.tokens, slices, [&](int t, dim3 grid) {
-        hipLaunchKernelGGL((kv_append_q4_kernel<T, C, D, N>), grid, kBlock, 0, stream, a, t, Divisor(n.units), n.of_q,
+    return in_parts(a, slices, [&](const AppendRopeArgs& part, int t, dim3 grid) {
+        hipLaunchKernelGGL((kv_append_q4_kernel<T, C, D, N>), grid, kBlock, 0, stream, part, t, Divisor(n.units), n.of_q,
                            n.of_kv, per, slices);
     });
 }
@@ -375,8 +380,8 @@ hipError_t append_q4(const AppendRopeArgs& a, int per, hipStream_t stream) {
 template <class T, int N>
 hipError_t read_q4(const AppendArgs& a, int all, hipStream_t stream) {
     const int slices = (all + 64 * N - 1) / (64 * N);
-    return in_parts(a.tokens, slices, [&](int t, dim3 grid) {
-        hipLaunchKernelGGL((kv_read_q4_kernel<T, N>), grid, kBlock, 0, stream, a, t, slices);
+    return in_parts(a, slices, [&](const AppendArgs& part, int t, dim3 grid) {
+        hipLaunchKernelGGL((kv_read_q4_kernel<T, N>), grid, kBlock, 0, stream, part, t, slices);
     });
 }
 
