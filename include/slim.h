@@ -485,7 +485,7 @@ slim_status slim_attention_prefill(const uint16_t* Q, int64_t stride_Q, uint16_t
  *   rot_dim      the first rot_dim elements of a head are turned (a multiple of
  *                8, at most head_dim), the others are left as they are
  *   interleaved  0: pair i is elements i and i + rot_dim / 2, 1: 2 i and 2 i + 1
- *   magnitude    finite; 1 leaves lengths as they are
+ *   magnitude    fp64, finite and within fp32's range; 1 leaves lengths as they are
  * Angles, cosines and sines are formed in fp64 (position 2^30 is as exact as 1),
  * half outputs are turned in fp32 and rounded once.  The struct is host memory, read
  * during the call; freqs is read when the call runs.
@@ -494,7 +494,7 @@ typedef struct {
     const double* freqs;
     int64_t rot_dim;
     int32_t interleaved;
-    float magnitude;
+    double magnitude;
 } slim_rotation;
 
 /*

@@ -42,7 +42,7 @@ _lib = None
 class Rotation(ctypes.Structure):
     """slim_rotation."""
     _fields_ = [("freqs", ctypes.c_void_p), ("rot_dim", ctypes.c_int64), ("interleaved", ctypes.c_int32),
-                ("magnitude", ctypes.c_float)]
+                ("magnitude", ctypes.c_double)]
 
 
 class SlimError(RuntimeError):

@@ -1,6 +1,8 @@
 // C-ABI front end of the paged key-value cache and its attention (declarations
 // and the contract of every call are in include/slim.h).  Checks every
 // argument before anything is launched; never aborts or throws.
+#include <float.h>
+
 #include "api_util.hpp"
 #include "attention.hpp"
 
@@ -118,11 +120,13 @@ slim_status check_rotation(const slim_rotation* r, int64_t head_dim, slim::Rotat
     if (!r->freqs) return fail(SLIM_EINVAL, "freqs is NULL");
     if (reinterpret_cast<uintptr_t>(r->freqs) & 7u) return fail(SLIM_EINVAL, "freqs must be 8-byte aligned");
     if (r->interleaved != 0 && r->interleaved != 1) return fail(SLIM_EINVAL, "interleaved must be 0 or 1");
-    if (!(r->magnitude - r->magnitude == 0.0f)) return fail(SLIM_EINVAL, "magnitude must be finite");
+    // (Half rows are turned in fp32, with the products of it and the cosines.)
+    if (!(r->magnitude >= -(double)FLT_MAX && r->magnitude <= (double)FLT_MAX))
+        return fail(SLIM_EINVAL, "magnitude must be finite and within fp32's range");
     to->freqs = r->freqs;
     to->half = (int32_t)(r->rot_dim / 2);
     to->interleaved = r->interleaved;
-    to->magnitude = (double)r->magnitude;
+    to->magnitude = r->magnitude;
     return SLIM_OK;
 }
 

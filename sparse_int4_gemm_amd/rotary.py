@@ -15,6 +15,7 @@ import torch
 from . import _lib
 
 SCALINGS = ("none", "linear", "ntk", "yarn")
+_FP32_MAX = torch.finfo(torch.float32).max
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -69,8 +70,8 @@ class Rope:
                              f"{tuple(freqs.shape)} for {rot_dim}")
         self.rot_dim, self.interleaved = rot_dim, bool(interleaved)
         self.magnitude = 1.0 if magnitude is None else float(magnitude)
-        if not math.isfinite(self.magnitude):
-            raise ValueError("magnitude must be finite")
+        if not abs(self.magnitude) <= _FP32_MAX:
+            raise ValueError("magnitude must be finite and within fp32's range")
         self._freqs = freqs.to(device, copy=True).contiguous()
         self.params = _lib.Rotation(ctypes.c_void_p(self._freqs.data_ptr()), rot_dim, int(self.interleaved), self.magnitude)
 
