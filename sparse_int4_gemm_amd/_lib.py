@@ -358,7 +358,8 @@ def _pools(kpool, vpool, dims, dtypes=_DTYPES):
         raise ValueError("tensors must live on the GPU (a ROCm 'cuda' device)")
     device, shape, dtype = kpool.device, kpool.shape, kpool.dtype
     if dtype not in dtypes:
-        raise TypeError("the pools must be float16 or bfloat16")
+        raise TypeError("the pools must be float16 or bfloat16" if dtypes is _DTYPES else
+                        "the pools must be float16, bfloat16 or uint8 (pages of 4 bits)")
     if len(shape) not in dims or shape != vpool.shape or dtype is not vpool.dtype or device != vpool.device:
         raise ValueError(f"the pools must be two {' or '.join(map(str, dims))}-dimensional tensors of one shape, type "
                          "and device")
