@@ -407,6 +407,9 @@ constexpr int kCus = 256, kSplitFrom = 10, kSplits = 32, kSortFrom = 512;
 // 114 and 195; 32 of 32 of 4000, 32 rows: 179 and 192; one of 24576, 32 heads on 8: 8 tokens, 32 rows, 23.7 and
 // 27.6, 32 tokens, 128 rows, 40.4 and 41.2; 16 of 8 of 4096, 64 rows: 48.1 and 46.0).
 constexpr int kFewRows = 32;
+// A sequence has at most kFewRows / 16 + 1 slots on average (find_slot), and there are at most 2^22
+// sequences: their grid, of 4 waves a workgroup (plan_of: with more than 512 units), is one launch.
+static_assert((kFewRows / 16 + 1) * (int64_t(1) << 22) * 64 * 4 < int64_t(1) << 32, "a grid holds fewer than 2^32 threads");
 
 struct Plan {
     int64_t units;                   // key heads of blocks of rows, about
@@ -443,7 +446,7 @@ template <class T, int D, int kWaves, bool kMany>
 hipError_t launch_waves(const AttnArgs& a, const Plan& plan, hipStream_t stream) {
     const int share = a.q_heads / a.kv_heads, groups = (share + 15) / 16, splits = plan.splits;
     const int chunk = max(kWaves, (plan.tiles + splits - 1) / splits);
-    // kMany: slots (find_slot), at most 4 a sequence: a grid of one split stays below 2^32 threads.
+    // kMany: slots (find_slot).
     const int64_t blocks = kMany ? (int64_t)a.tokens * share / 16 + a.kv.seqs : a.tokens;
     const dim3 grid((unsigned)(blocks * splits), (unsigned)(kMany ? a.kv_heads : a.kv_heads * groups));
     // More than a round of workgroups: longest first (attention_decode.hip; 64 sequences of 1 to 4096
