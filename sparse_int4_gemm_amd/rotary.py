@@ -68,14 +68,26 @@ class Rope:
         elif rot_dim <= 0 or rot_dim % 8 or freqs.dtype != torch.float64 or freqs.shape != (rot_dim // 2,):
             raise ValueError(f"freqs must be float64 [rot_dim / 2] and rot_dim a multiple of 8, got {freqs.dtype} "
                              f"{tuple(freqs.shape)} for {rot_dim}")
-        self.rot_dim, self.interleaved = rot_dim, bool(interleaved)
-        self.magnitude = 1.0 if magnitude is None else float(magnitude)
-        if not abs(self.magnitude) <= _FP32_MAX:
+        magnitude = 1.0 if magnitude is None else float(magnitude)
+        if not abs(magnitude) <= _FP32_MAX:
             raise ValueError("magnitude must be finite and within fp32's range")
         self._freqs = freqs.to(device, copy=True).contiguous()
-        self.params = _lib.Rotation(ctypes.c_void_p(self._freqs.data_ptr()), rot_dim, int(self.interleaved), self.magnitude)
+        self.params = _lib.Rotation(ctypes.c_void_p(self._freqs.data_ptr()), rot_dim, int(bool(interleaved)), magnitude)
 
+    # (None to be replaced: calls pass on `params`, and in it the frequencies' address.)
     @property
     def freqs(self) -> torch.Tensor:
-        """The frequencies on the GPU (not to be replaced: calls hold their address)."""
+        """The frequencies on the GPU."""
         return self._freqs
+
+    @property
+    def rot_dim(self) -> int:
+        return self.params.rot_dim
+
+    @property
+    def interleaved(self) -> bool:
+        return bool(self.params.interleaved)
+
+    @property
+    def magnitude(self) -> float:
+        return self.params.magnitude
