@@ -486,8 +486,9 @@ slim_status slim_attention_prefill(const uint16_t* Q, int64_t stride_Q, uint16_t
  *                8, at most head_dim), the others are left as they are
  *   interleaved  0: pair i is elements i and i + rot_dim / 2, 1: 2 i and 2 i + 1
  *   magnitude    fp64, finite and within fp32's range; 1 leaves lengths as they are
- * Angles, cosines and sines are formed in fp64 (position 2^30 is as exact as 1),
- * half outputs are turned in fp32 and rounded once.  The struct is host memory, read
+ * Angles, cosines and sines are formed in fp64: an angle is off by at most
+ * 3 * 2^-53 of itself (3.6e-7 radians of 2^30, far below a half's rounding).  Half
+ * outputs are turned in fp32 and rounded once.  The struct is host memory, read
  * during the call; freqs is read when the call runs.
  */
 typedef struct {
@@ -533,8 +534,10 @@ slim_status slim_kv_append_rope(const uint16_t* Q, int64_t stride_Q, uint16_t* Q
  *   within [-23, 13] in fp16 and [-125, 125] in bf16: half of 2^e is then a
  *   number of the type, and 6 * 2^e finite.  An element goes to the nearest
  *   code, ties to the even one, 6 at most.  A group that holds an infinity
- *   or NaN reads back as 32 NaNs.  Keys that are turned on the way are held
- *   in fp32 before they are coded.
+ *   or NaN reads back as 32 NaNs.  Keys that are turned on the way are turned in
+ *   fp64 and held in fp32 before they are coded.
+ * A page does not say which type its values are of: dtype of every call on it must be
+ * the append's (fp16 has no place for values far out of its range that bf16 pages hold).
  * A page of K or V is slim_q4_page_bytes(kv_heads, page_size, head_dim) =
  * kv_heads * page_size * head_dim * 17 / 32 bytes (0 for a rejected shape): all codes
  * [kv_heads][page_size][head_dim / 2] (element 2 i of a row in the low four bits
@@ -553,7 +556,13 @@ slim_status slim_kv_append_rope(const uint16_t* Q, int64_t stride_Q, uint16_t* Q
  *                     such pools, on the values the codes stand for; dtype is that of
  *                     Q, O and the append.  Workspace: slim_attention_workspace_bytes.
  *                     The numbers of rows and sequences plan the work too, rows of no
- *                     sequence among them, and may change results in their last bits
+ *                     sequence among them, and may change results in their last bits:
+ *                     with up to 32 rows of a key head (new tokens times q_heads / kv_heads)
+ *                     a sequence on average, slim_attention_prefill_q4's weights enter
+ *                     with the accuracy of fp32, with more they are rounded once to the
+ *                     type, as slim_attention_prefill's.  One plan serves a batch: among many
+ *                     sequences a single far longer one is not split and takes
+ *                     as long as its keys take one workgroup a key head
  */
 size_t slim_q4_page_bytes(int64_t kv_heads, int64_t page_size, int64_t head_dim);
 slim_status slim_kv_append_q4(const uint16_t* Q, int64_t stride_Q, uint16_t* Qout, int64_t stride_Qout,

@@ -324,7 +324,8 @@ def kv_append_q4(K: torch.Tensor, V: torch.Tensor, kpool: torch.Tensor, vpool: t
                  q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
     """kv_append_rope into pages of 4 bits a value: uint8 pools [pages, kv_heads,
     page_size, head_dim * 17 / 32] (slim.h has the format).  rope None: keys as
-    they are, and no queries."""
+    they are, and no queries.  The pages do not say whether they hold float16 or
+    bfloat16 values: what reads them has to go by K's type."""
     if q is not None and q_out is None:
         q_out = _empty(q.shape, q.dtype, q.device, stream)
     slim_kv_append_q4(q, q_out, K, V, kpool, vpool, table, lens, rope, starts, stream=stream)
@@ -354,7 +355,7 @@ def attention_decode_q4(q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tenso
                         lens: torch.Tensor, max_len: int | None = None, window: int = 0, sinks: int = 0,
                         scale: float | None = None, lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
                         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """attention_decode over pages of 4 bits (kv_append_q4)."""
+    """attention_decode over pages of 4 bits (kv_append_q4), q of the type that was appended."""
     if out is None or ws is None:
         out, ws = _attention_buffers(q, lens, kpool, ws, out, stream, kpool.shape[-1] // 17 * 32)
     slim_attention_decode_q4(q, out, kpool, vpool, table, lens, ws, max_len, window, sinks, scale, lse, stream)
@@ -365,7 +366,7 @@ def attention_prefill_q4(q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tens
                          lens: torch.Tensor, starts: torch.Tensor | None, max_len: int | None = None, window: int = 0,
                          sinks: int = 0, scale: float | None = None, lse: torch.Tensor | None = None,
                          ws: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """attention_prefill over pages of 4 bits (kv_append_q4)."""
+    """attention_prefill over pages of 4 bits (kv_append_q4), q of the type that was appended."""
     if out is None or ws is None:
         out, ws = _attention_buffers(q, lens, kpool, ws, out, stream, kpool.shape[-1] // 17 * 32)
     slim_attention_prefill_q4(q, out, kpool, vpool, table, lens, starts, ws, max_len, window, sinks, scale, lse, stream)

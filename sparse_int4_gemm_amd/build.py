@@ -33,11 +33,11 @@ COMMON_FLAGS = [
 ]
 
 
-# Extra flags per source.  The prompt attention kernel of head size 256 uses
-# more than 256 registers a lane (the others 155 to 231); this keeps the results
-# of its matrix instructions in registers that vector instructions can read.
-# Without it: 256 accumulation registers instead of 148, 40 vector spills
-# instead of none, 3572 moves between the two kinds in the file instead of 570.
+# Extra flags per source.  The prompt attention kernels of head size 256 use
+# more than 256 registers a lane (the others 156 to 251); this keeps the results
+# of their matrix instructions in registers that vector instructions can read.
+# Without it: 256 accumulation registers instead of 149 (180 over pages of 4 bits), 40
+# (114) vector spills instead of none, 7126 accesses to them in the file instead of 1386.
 FILE_FLAGS: dict[str, list[str]] = {
     "attention_prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }

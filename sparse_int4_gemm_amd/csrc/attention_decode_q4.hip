@@ -398,6 +398,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void attention_decod
 // The workgroups are then as small as gives at most kSplits of a key head (one sequence of 8000:
 // 11.7 us with 62 of 4 waves, 10.6 with 31 of 8, 12.4 with 15 of 16; 131071: 39.1 with 64 of 8, 35.7 with 32 of 16)
 // and two a CU (four of 8000: 17.1 with 1024 of 4 waves, 16.3 with 512 of 8).
+// The plan knows the longest length only.  With a workgroup for every CU nothing is split, however uneven
+// the lengths: one sequence of 131071 among 63 of 100, 32 heads on 8, takes 997 us, alone 34.
 constexpr int kCus = 256, kSplitFrom = 10, kSplits = 32, kSortFrom = 512;
 
 // Prompts (and chunks, and tokens to be verified) of up to kFewRows rows a key head on
@@ -405,7 +407,9 @@ constexpr int kCus = 256, kSplitFrom = 10, kSplits = 32, kSortFrom = 512;
 // ones through attention_prefill.hip with its blocks of 128 (2 tokens of 64 sequences
 // of 2000, 32 heads on 8: 37 us here, 92 there; 4 of 32 of 4000, 32 heads:
 // 114 and 195; 32 of 32 of 4000, 32 rows: 179 and 192; one of 24576, 32 heads on 8: 8 tokens, 32 rows, 23.7 and
-// 27.6, 32 tokens, 128 rows, 40.4 and 41.2; 16 of 8 of 4096, 64 rows: 48.1 and 46.0).
+// 27.6, 32 tokens, 128 rows, 40.4 and 41.2; 16 of 8 of 4096, 64 rows: 48.1 and 46.0).  The average
+// decides for the whole batch: 61 tokens on 24576 beside 40 single ones of 1000, 32 heads on 8, take 196 us (apart 50 and 17), a prompt
+// of 2048 beside 64 of them 81 (apart 55 and 19), beside 500 of them 194 (apart 55 and 111).
 constexpr int kFewRows = 32;
 // A sequence has at most kFewRows / 16 + 1 slots on average (find_slot), and there are at most 2^22
 // sequences: their grid, of 4 waves a workgroup (plan_of: with more than 512 units), is one launch.

@@ -45,7 +45,12 @@
 // 32 LDS writes for each of 4 waves and tile more, which two workgroups a CU mostly
 // hide: 8192 windowed tokens 392 to 409 us, four prompts of up to 4096 365 to 377 where
 // the 16-bit cache takes 367 to 382; not so one wave a SIMD (head size 256: 79 and 66 us) or
-// short prompts (2048 tokens of 32 heads: 53 and 49).  LDS writes of 16 rows' chunks take 16 cycles,
+// short prompts (2048 tokens of 32 heads: 53 and 49).  The weights are rounded once here
+// too: with their low halves as a second operand, as in attention_decode_q4.hip, the error against
+// 64 bits falls from 2.3e-3 to 1.7e-3 of the outputs' norm in bf16 and from 2.7e-4 to 2.1e-4 in fp16, where
+// the outputs' own rounding puts it, and 8192 windowed tokens take 528 us instead of 398 (four prompts of
+// 2000 202 and 161, 61 tokens on 24576 57 and 48).  At head size 64, one group,
+// one register more than there are spills (8 bytes a lane).  LDS writes of 16 rows' chunks take 16 cycles,
 // 13 with rows taken in another order (no bank met twice), which changed no case's time.
 #include "kv_q4.hpp"
 

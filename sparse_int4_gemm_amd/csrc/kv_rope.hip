@@ -429,6 +429,8 @@ hipError_t launch_kv_append_rope(const AppendRopeArgs& a, hipStream_t stream) {
     return wide ? append_rope_n<Bf16, 8>(a, stream) : append_rope_n<Bf16, 4>(a, stream);
 }
 
+// (Vectors of 4, for halves of a head that begin in the middle of a chunk, keep 20 bytes a lane in scratch
+// memory: 8192 tokens of 32 heads on 8 of 96 take 44.0 us with rot_dim 24 and 37.3 with 32.)
 hipError_t launch_kv_append_q4(const AppendRopeArgs& a, hipStream_t stream) {
     const bool wide = rope_vector(a.by) == 8;
     if (a.dtype == 0) return wide ? append_q4_dim<Fp16, 8>(a, stream) : append_q4_dim<Fp16, 4>(a, stream);

@@ -11,7 +11,7 @@ constexpr int kRopeWaves = 4;                 // waves of a workgroup; each has 
 inline float rounds(int64_t tokens, int64_t units) { return (float)(tokens * ((units + 63) / 64)) / (256 * 32); }
 
 // (cos, sin) * magnitude of pair i at position p.  The angle is taken in turns,
-// in fp64: of p * f the fraction of a turn that is left is off by 2^-53 of the number of turns.
+// in fp64: 1 / (2 pi) and two products, so off by at most 3 * 2^-53 of itself.
 __device__ __forceinline__ double2 turn_of(const Rotation& by, int p, int i) {
     double t = (double)p * (by.freqs[i] * 0.15915494309189533577);       // 1 / (2 pi)
     t -= rint(t);

@@ -6,8 +6,9 @@ the bookkeeping on the host (a free list, a count of owners per page, each
 sequence's list of pages) and moves data with kv_copy_pages only, on the
 current stream.  With bits=4 the pools are uint8 pages of 4 bits a value
 [layers, pages, kv_heads, page_size, head_dim * 17 / 32], as kv_append_q4 writes
-and the _q4 attention calls read them.  Forks share pages: a sequence gets its own copy of a shared
-page when it first writes to it.
+and the _q4 attention calls read them; `dtype` is then the type of the rows that
+are appended and of the queries (the pages do not say it).  Forks share pages: a sequence
+gets its own copy of a shared page when it first writes to it.
 """
 from __future__ import annotations
 

@@ -57,7 +57,11 @@ class Rope:
 
     interleaved: pair i is elements 2 i and 2 i + 1 of a head, otherwise i and
     i + rot_dim / 2.  freqs: float64 [rot_dim / 2], in place of base and scaling;
-    magnitude: in place of theirs."""
+    magnitude: in place of theirs.
+
+    Its frequencies are made on the current stream, and calls read them when they run: like
+    any tensor it has to be kept until calls on other streams are done, and
+    as long as a graph that captured one is replayed."""
 
     def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
                  factor: float = 1.0, original_len: int = 0, turns: tuple[float, float] = (32.0, 1.0),
