@@ -374,7 +374,12 @@ def _stream_on(stream, device):
         raise ValueError(f"the current device must be the tensors' {device}")
     if stream is not None:
         return stream.cuda_stream
-    # (The public way to the current stream's handle costs as much as the launch.)
+    return _current_stream(device)
+
+
+def _current_stream(device):
+    """Handle of the device's current stream."""
+    # (The public way to it costs as much as the launch.)
     return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
 
 
@@ -490,12 +495,17 @@ def _half(t, name):
     return t.dtype
 
 
-def _rotation(rope, device):
-    """slim_rotation of a Rope (kept by it), None of None."""
+def _rotation(rope, device, handle, stream):
+    """slim_rotation of a Rope (kept by it) for a call on stream `handle` (`stream`, or the current one if None);
+    None of None."""
     if rope is None:
         return None
-    if rope.freqs.device != device:
-        raise ValueError(f"the rotation must be on {device}, got {rope.freqs.device}")
+    freqs = rope.freqs
+    if freqs.device != device:
+        raise ValueError(f"the rotation must be on {device}, got {freqs.device}")
+    if handle != rope.made_on:
+        # It may be let go before that stream has read its frequencies.
+        freqs.record_stream(torch.cuda.current_stream(device) if stream is None else stream)
     return rope.params
 
 
@@ -511,8 +521,9 @@ def slim_rope(X, Y, positions, rope, stream=None) -> None:
     pp, (count,) = _ints("positions", positions, dev, 1)
     if y_tokens != tokens or count != tokens:
         raise ValueError(f"X has {tokens} rows, Y {y_tokens}, and there are {count} positions")
-    _check(load().slim_rope(px, sx, py, sy, tokens, heads, X.shape[2], _DTYPES[dtype], pp, _rotation(rope, dev),
-                            _stream_on(stream, dev)))
+    handle = _stream_on(stream, dev)
+    _check(load().slim_rope(px, sx, py, sy, tokens, heads, X.shape[2], _DTYPES[dtype], pp,
+                            _rotation(rope, dev, handle, stream), handle))
 
 
 def _append_args(K, V, heads, dim, dtype, dev):
@@ -535,8 +546,9 @@ def _append(call, Q, Qout, K, V, pkp, pvp, pages, heads, page, dim, dtype, dev, 
             raise ValueError(f"K has {tokens} rows, Q {q_tokens} and Qout {o_tokens}")
         queries = (pq, sq, po, so, q_heads)
     pt, pl, ps, seqs, width = _batch(table, lens, starts, tokens, dev)
+    handle = _stream_on(stream, dev)
     _check(call(*queries, pk, sk, pv, sv, tokens, seqs, heads, dim, _DTYPES[dtype], pt, width, pl, ps, pkp, pvp, pages, page,
-                _rotation(rope, dev), _stream_on(stream, dev)))
+                _rotation(rope, dev, handle, stream), handle))
 
 
 def slim_kv_append_rope(Q, Qout, K, V, kpool, vpool, table, lens, rope, starts=None, stream=None) -> None:

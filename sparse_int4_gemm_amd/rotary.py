@@ -59,9 +59,9 @@ class Rope:
     i + rot_dim / 2.  freqs: float64 [rot_dim / 2], in place of base and scaling;
     magnitude: in place of theirs.
 
-    Its frequencies are made on the current stream, and calls read them when they run: like
-    any tensor it has to be kept until calls on other streams are done, and
-    as long as a graph that captured one is replayed."""
+    Its frequencies are made on the current stream, and calls read them when they run.  It
+    may be let go after a call on any stream, but has to be kept as long as a
+    graph that captured one is replayed."""
 
     def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
                  factor: float = 1.0, original_len: int = 0, turns: tuple[float, float] = (32.0, 1.0),
@@ -76,6 +76,7 @@ class Rope:
         if not abs(magnitude) <= _FP32_MAX:
             raise ValueError("magnitude must be finite and within fp32's range")
         self._freqs = freqs.to(device, copy=True).contiguous()
+        self.made_on = _lib._current_stream(self._freqs.device) if self._freqs.is_cuda else None
         self.params = _lib.Rotation(ctypes.c_void_p(self._freqs.data_ptr()), rot_dim, int(bool(interleaved)), magnitude)
 
     # (None to be replaced: calls pass on `params`, and in it the frequencies' address.)
